@@ -133,8 +133,9 @@ def _fp4(x, fmt):
     six = torch.full((), 6.0, device=x.device)
     a = x.abs()
     fine = torch.isfinite(a)
-    blocks = torch.where(fine, a, torch.zeros_like(a)).unflatten(-1, (-1, block)).amax(-1)
-    bad = ~fine.unflatten(-1, (-1, block)).all(-1)
+    bad = ~fine.unflatten(-1, (-1, block)).all(-1)  # a NaN scale, and nothing for the row's
+    blocks = a.unflatten(-1, (-1, block)).amax(-1)
+    blocks = torch.where(bad, torch.zeros_like(blocks), blocks)
     if fmt == "nvfp4":
         frac, e = torch.frexp(blocks.amax(-1))
         e = (e - 12 + (frac > 0.65625)).clamp(-126, 127)  # the least with amax <= 6 * 448 * 2^e
