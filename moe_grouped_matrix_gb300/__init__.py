@@ -460,3 +460,10 @@ def read_device_errors(device=None, workspace=None, stream=None) -> int:
     if rc != 0:
         raise GmmError("gmm_read_device_errors", rc)
     return int(flags.value)
+
+
+from .moe import (MAX_TOPK, ExpertOrder, Fp4Tensor, combine, combine_backward, dequantize_fp4, dispatch,  # noqa: E402
+                  dispatch_backward, gmm_fp4, quantize_fp4, route, route_backward, sort_by_expert)
+
+__all__ += ["MAX_TOPK", "ExpertOrder", "Fp4Tensor", "combine", "combine_backward", "dequantize_fp4", "dispatch",
+            "dispatch_backward", "gmm_fp4", "quantize_fp4", "route", "route_backward", "sort_by_expert"]

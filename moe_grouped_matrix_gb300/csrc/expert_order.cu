@@ -1,0 +1,473 @@
+// Tokens' rows sorted by expert, and back with the router's weights, with
+// their gradients.
+//
+//   sort      a stable counting sort of the tokens * topk slots by expert
+//   dispatch  out[rows[t, j]] = x[t]
+//   combine   out[t] = sum_j w[t, j] in[rows[t, j]]
+//   its gradients  din[rows[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], in[rows[t, j]]>
+//
+// All but the sort are bound by memory: they go token by token, so that what
+// is shared by a token's slots (x[t], dout[t]) is read once, and the expert
+// order is only ever the address of whole rows.
+#include <cuda_bf16.h>
+
+#include <climits>
+#include <type_traits>
+
+#include "../../include/libgmm_moe.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gmmk {
+namespace {
+
+// Slots of an order: a step past the last still fits in int32.
+constexpr int64_t kMaxSlots = int64_t(INT32_MAX) - 1023;
+
+// The row of a slot as a call is given it; anything that is no row of the order counts as dropped.
+__device__ __forceinline__ int32_t slot_row(const int32_t* rows, int64_t slot, int64_t slots) {
+  const int32_t r = __ldg(rows + slot);
+  return r < slots ? r : -1;
+}
+
+// ------------------------------------------------------------------ the sort
+// One cluster of CTAs.  Every warp owns a run of consecutive slots: it counts its
+// experts in its own row of a table in shared memory, the table is summed down
+// the warps and (through distributed shared memory) across the CTAs, and then
+// the warp walks its run again and gives each slot the next place of its
+// expert, equal experts within a step of 32 in lane order.  So the order is
+// stable and no result hangs on the order of an atomic.  Dropped slots count as
+// one more expert after the last.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+// Up to this many slots one CTA alone is used: 4 steps a warp.
+constexpr int64_t kSortOneCta = 4 * kSortThreads;
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    sort_kernel(const int32_t* __restrict__ experts, int32_t slots, int32_t num_experts, int32_t run,
+                int32_t* __restrict__ group_sizes, int32_t* __restrict__ rows, int32_t* __restrict__ source,
+                int32_t ctas) {
+  extern __shared__ uint32_t table[];  // [kSortWarps][bins], then [bins] of the CTA's sums
+  __shared__ uint32_t warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bins = num_experts + 1;
+  uint32_t* mine = table + warp * bins;
+  uint32_t* total = table + kSortWarps * bins;
+  const int32_t rank = ctas > 1 ? int32_t(cluster_ctarank()) : 0;
+  const int64_t first = int64_t(rank * kSortWarps + warp) * run;
+  const int32_t lo = int32_t(first < slots ? first : slots);
+  const int32_t hi = int32_t(first + run < slots ? first + run : slots);
+  for (int i = tid; i < kSortWarps * bins; i += kSortThreads) table[i] = 0;
+  __syncthreads();
+  auto bin_of = [&](int32_t e) { return e >= 0 && e < num_experts ? e : num_experts; };
+  for (int32_t s = lo + lane; s < hi; s += 32) atomicAdd(mine + bin_of(__ldg(experts + s)), 1u);
+  __syncthreads();
+  for (int b = tid; b < bins; b += kSortThreads) {
+    uint32_t sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = table[w * bins + b];
+      table[w * bins + b] = sum;
+      sum += c;
+    }
+    total[b] = sum;
+  }
+  if (ctas > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // each expert's rows over all CTAs, and those of the CTAs before this one
+  uint32_t all = 0, before = 0;
+  if (tid < num_experts) {
+    if (ctas > 1) {
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t c = ld_cluster_u32(mapa_shared(smem_u32(total + tid), uint32_t(r)));
+        all += c;
+        before += r < rank ? c : 0u;
+      }
+    } else {
+      all = total[tid];
+    }
+    if (rank == 0) group_sizes[tid] = int32_t(all);
+  }
+  uint32_t incl = all;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  uint32_t start = incl - all, end = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    const uint32_t s = warp_sums[w];
+    if (w < warp) start += s;
+    end += s;
+  }
+  if (tid < num_experts)
+    for (int w = 0; w < kSortWarps; ++w) table[w * bins + tid] += start + before;
+  if (tid == 0) {
+    uint32_t gone = 0;  // dropped slots of the CTAs before
+    if (ctas > 1)
+      for (int r = 0; r < rank; ++r) gone += ld_cluster_u32(mapa_shared(smem_u32(total + num_experts), uint32_t(r)));
+    for (int w = 0; w < kSortWarps; ++w) table[w * bins + num_experts] += end + gone;
+  }
+  __syncthreads();
+  for (int32_t s0 = lo; s0 < hi; s0 += 32) {
+    const int32_t s = s0 + lane;
+    const int32_t b = s < hi ? bin_of(__ldg(experts + s)) : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, b);
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    uint32_t at = 0;
+    if (b >= 0) at = mine[b] + uint32_t(ahead);
+    __syncwarp();
+    if (b >= 0) {
+      if (ahead == 0) mine[b] += uint32_t(__popc(same));
+      rows[s] = b < num_experts ? int32_t(at) : -1;
+      source[at] = b < num_experts ? s : -1;
+    }
+    __syncwarp();
+  }
+  if (ctas > 1) cluster_sync();  // no CTA leaves while another may read its sums
+}
+
+cudaError_t launch_sort(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
+                        int32_t* rows, int32_t* source, cudaStream_t stream) {
+  const size_t smem = size_t(kSortWarps + 1) * (num_experts + 1) * sizeof(uint32_t);
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int ctas = slots <= kSortOneCta ? 1 : kSortCluster;
+  const int64_t warps = int64_t(ctas) * kSortWarps;
+  const int32_t run = int32_t(((slots + warps - 1) / warps + 31) / 32 * 32);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = unsigned(ctas);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, sort_kernel, experts, slots, num_experts, run, group_sizes, rows, source,
+                            int32_t(ctas));
+}
+
+// ------------------------------------------------------------------ rows of any width
+// A row is moved in units of 16, 8, 4 or 2 bytes, the widest that every row's
+// address and width are a multiple of; a unit holds kN elements.
+template <class U, class T>
+struct Unit {
+  static constexpr int kN = int(sizeof(U) / sizeof(T));
+  static __device__ __forceinline__ void unpack(U u, float (&f)[kN]) {
+    T t[kN];
+    memcpy(t, &u, sizeof(U));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = float(t[i]);
+  }
+  static __device__ __forceinline__ U pack(const float (&f)[kN]) {
+    T t[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if constexpr (std::is_same<T, float>::value)
+        t[i] = f[i];
+      else
+        t[i] = __float2bfloat16_rn(f[i]);
+    }
+    U u;
+    memcpy(&u, t, sizeof(U));
+    return u;
+  }
+};
+
+constexpr int kThreads = 128;
+
+template <class U>
+__device__ __forceinline__ U zero_unit() {
+  U u;
+  memset(&u, 0, sizeof(U));
+  return u;
+}
+
+// One warp for each token and run of 32 * kPer units of its row.
+template <class U, int kPer>
+__global__ void __launch_bounds__(kThreads)
+    dispatch_kernel(const U* __restrict__ x, int64_t tokens, int64_t units, int64_t x_units, int32_t topk,
+                    int64_t parts, const int32_t* __restrict__ rows, const int32_t* __restrict__ source,
+                    U* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = w / parts;
+  if (t >= tokens) return;
+  const int64_t c0 = (w - t * parts) * (32 * kPer) + lane;
+  const int32_t r = lane < topk ? slot_row(rows, t * topk + lane, tokens * topk) : -1;
+  const int32_t s = lane < topk ? __ldg(source + t * topk + lane) : 0;
+  U v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (c0 + 32 * i < units) v[i] = __ldg(x + t * x_units + c0 + 32 * i);
+  for (int j = 0; j < topk; ++j) {
+    const int32_t to = __shfl_sync(0xffffffffu, r, j);
+    if (to >= 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c0 + 32 * i < units) out[to * units + c0 + 32 * i] = v[i];
+    }
+    if (__shfl_sync(0xffffffffu, s, j) < 0) {  // row t * topk + j is past the groups
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c0 + 32 * i < units) out[(t * topk + j) * units + c0 + 32 * i] = zero_unit<U>();
+    }
+  }
+}
+
+template <class U, class T, int kPer>
+__global__ void __launch_bounds__(kThreads)
+    combine_kernel(const U* __restrict__ in, int64_t tokens, int64_t units, int32_t topk, int64_t parts,
+                   const int32_t* __restrict__ rows, const float* __restrict__ weights, U* __restrict__ out) {
+  constexpr int N = Unit<U, T>::kN;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = w / parts;
+  if (t >= tokens) return;
+  const int64_t c0 = (w - t * parts) * (32 * kPer) + lane;
+  const int32_t r = lane < topk ? slot_row(rows, t * topk + lane, tokens * topk) : -1;
+  const float g = lane < topk && weights != nullptr ? __ldg(weights + t * topk + lane) : 1.f;
+  float acc[kPer][N];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[i][n] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < topk; ++j) {
+    const int32_t from = __shfl_sync(0xffffffffu, r, j);
+    const float gj = __shfl_sync(0xffffffffu, g, j);
+    if (from >= 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (c0 + 32 * i < units) {
+          float f[N];
+          Unit<U, T>::unpack(__ldg(in + from * units + c0 + 32 * i), f);
+#pragma unroll
+          for (int n = 0; n < N; ++n) acc[i][n] = fmaf(gj, f[n], acc[i][n]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (c0 + 32 * i < units) out[t * units + c0 + 32 * i] = Unit<U, T>::pack(acc[i]);
+}
+
+constexpr int kBackThreads = 256;
+
+// One CTA for each token: its warps share the row's columns; their parts of the
+// dot products are summed in warp order.
+template <class U, class T, int kPer>
+__global__ void __launch_bounds__(kBackThreads)
+    combine_backward_kernel(const U* __restrict__ dout, const U* __restrict__ in, int64_t tokens, int64_t units,
+                            int32_t topk,
+                            const int32_t* __restrict__ rows, const int32_t* __restrict__ source,
+                            const float* __restrict__ weights, U* __restrict__ din, float* __restrict__ dweights) {
+  constexpr int N = Unit<U, T>::kN;
+  __shared__ float part[kBackThreads / 32][GMM_MAX_TOPK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  const int32_t r = lane < topk ? slot_row(rows, t * topk + lane, tokens * topk) : -1;
+  const int32_t s = lane < topk ? __ldg(source + t * topk + lane) : 0;
+  const float g = lane < topk ? __ldg(weights + t * topk + lane) : 0.f;
+  part[warp][lane] = 0.f;
+  __syncwarp();
+  for (int64_t base = 0; base < units; base += kBackThreads * kPer) {
+    const int64_t c0 = base + threadIdx.x;
+    float d[kPer][N];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (c0 + kBackThreads * i < units) {
+        Unit<U, T>::unpack(__ldg(dout + t * units + c0 + kBackThreads * i), d[i]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) d[i][n] = 0.f;
+      }
+    }
+    for (int j = 0; j < topk; ++j) {
+      const int32_t row = __shfl_sync(0xffffffffu, r, j);
+      const float gj = __shfl_sync(0xffffffffu, g, j);
+      if (row >= 0) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (c0 + kBackThreads * i < units) {
+            float f[N], o[N];
+            Unit<U, T>::unpack(__ldg(in + row * units + c0 + kBackThreads * i), f);
+#pragma unroll
+            for (int n = 0; n < N; ++n) sum = fmaf(d[i][n], f[n], sum), o[n] = gj * d[i][n];
+            din[row * units + c0 + kBackThreads * i] = Unit<U, T>::pack(o);
+          }
+        }
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane == 0) part[warp][j] += sum;
+      }
+      if (__shfl_sync(0xffffffffu, s, j) < 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (c0 + kBackThreads * i < units) din[(t * topk + j) * units + c0 + kBackThreads * i] = zero_unit<U>();
+      }
+    }
+  }
+  __syncthreads();
+  if (int(threadIdx.x) < topk) {
+    float sum = 0.f;
+    for (int w = 0; w < kBackThreads / 32; ++w) sum += part[w][threadIdx.x];
+    dweights[t * topk + threadIdx.x] = sum;
+  }
+}
+
+// go(unit) for the widest unit type that `bits` (addresses and pitches in bytes, or-ed) allows.
+template <class F>
+cudaError_t by_unit(uint64_t bits, F&& go) {
+  if (bits % 16 == 0) return go(uint4{});
+  if (bits % 8 == 0) return go(uint2{});
+  if (bits % 4 == 0) return go(uint32_t{});
+  return go(uint16_t{});
+}
+
+uint64_t address(const void* p) { return uint64_t(reinterpret_cast<uintptr_t>(p)); }
+
+int check(int dtype, int64_t tokens, int64_t d, int32_t topk) {
+  if (dtype != GMM_DTYPE_BF16 && dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
+  if (tokens < 0 || d < 1 || d > INT32_MAX || topk < 1 || topk > GMM_MAX_TOPK || tokens > kMaxSlots / topk)
+    return GMM_ERR_SHAPE;
+  return GMM_OK;
+}
+
+// Warps of `per` units a lane over every token's row, as a grid of kThreads-blocks; 0: too large.
+unsigned row_grid(int64_t tokens, int64_t units, int per, int64_t* parts) {
+  *parts = (units + 32 * per - 1) / (32 * per);
+  const int64_t blocks = (tokens * *parts + kThreads / 32 - 1) / (kThreads / 32);
+  return blocks <= INT32_MAX ? unsigned(blocks) : 0u;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? GMM_OK : record_cuda_error(e); }
+
+template <class T>
+cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, const int32_t* rows,
+                    const float* weights, void* out, cudaStream_t s) {
+  return by_unit(address(in) | address(out) | uint64_t(d) * sizeof(T), [&](auto unit) -> cudaError_t {
+    using U = decltype(unit);
+    if constexpr (sizeof(U) < sizeof(T)) {
+      return cudaErrorInvalidValue;  // excluded by the alignment check
+    } else {
+      const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
+      int64_t parts;
+      const unsigned grid = row_grid(tokens, units, 2, &parts);
+      if (grid == 0) return cudaErrorInvalidConfiguration;
+      combine_kernel<U, T, 2><<<grid, kThreads, 0, s>>>(static_cast<const U*>(in), tokens, units, topk, parts, rows,
+                                                       weights, static_cast<U*>(out));
+      return cudaGetLastError();
+    }
+  });
+}
+
+template <class T>
+cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, int64_t d, int32_t topk,
+                             const int32_t* rows, const int32_t* source, const float* weights, void* din,
+                             float* dweights, cudaStream_t s) {
+  return by_unit(address(dout) | address(in) | address(din) | uint64_t(d) * sizeof(T), [&](auto unit) -> cudaError_t {
+    using U = decltype(unit);
+    if constexpr (sizeof(U) < sizeof(T)) {
+      return cudaErrorInvalidValue;
+    } else {
+      combine_backward_kernel<U, T, 2><<<unsigned(tokens), kBackThreads, 0, s>>>(
+          static_cast<const U*>(dout), static_cast<const U*>(in), tokens, d * int64_t(sizeof(T)) / int64_t(sizeof(U)), topk,
+          rows, source, weights, static_cast<U*>(din), dweights);
+      return cudaGetLastError();
+    }
+  });
+}
+
+}  // namespace
+}  // namespace gmmk
+
+extern "C" int gmm_sort_by_expert(const int32_t* experts, int64_t tokens, int32_t topk, int32_t num_experts,
+                                  int32_t* group_sizes, int32_t* rows, int32_t* source, void* stream) {
+  using namespace gmmk;
+  if (num_experts < 1 || num_experts > GMM_MAX_GROUPS) return GMM_ERR_SHAPE;
+  if (int st = check(GMM_DTYPE_F32, tokens, 1, topk)) return st;
+  if (group_sizes == nullptr || (tokens > 0 && (experts == nullptr || rows == nullptr || source == nullptr)))
+    return GMM_ERR_NULL;
+  if ((address(experts) | address(group_sizes) | address(rows) | address(source)) % 4 != 0) return GMM_ERR_ALIGN;
+  if (int st = require_device(nullptr)) return st;
+  return done(launch_sort(experts, int32_t(tokens * topk), num_experts, group_sizes, rows, source,
+                          static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int gmm_dispatch(const void* x, int dtype, int64_t tokens, int64_t d, int64_t x_ld, int32_t topk,
+                            const int32_t* rows, const int32_t* source, void* out, void* stream) {
+  using namespace gmmk;
+  if (int st = check(dtype, tokens, d, topk)) return st;
+  if (x_ld < d) return GMM_ERR_SHAPE;
+  if (tokens > 0 && (x == nullptr || rows == nullptr || source == nullptr || out == nullptr))
+    return GMM_ERR_NULL;
+  const uint64_t el = dtype == GMM_DTYPE_F32 ? 4 : 2;
+  if ((address(x) | address(out)) % el != 0 || (address(rows) | address(source)) % 4 != 0) return GMM_ERR_ALIGN;
+  if (int st = require_device(nullptr)) return st;
+  if (tokens == 0) return GMM_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(by_unit(address(x) | address(out) | uint64_t(d) * el | uint64_t(x_ld) * el, [&](auto unit) -> cudaError_t {
+    using U = decltype(unit);
+    const int64_t units = d * int64_t(el) / int64_t(sizeof(U));
+    int64_t parts;
+    const unsigned grid = row_grid(tokens, units, 4, &parts);
+    if (grid == 0) return cudaErrorInvalidConfiguration;
+    dispatch_kernel<U, 4><<<grid, kThreads, 0, s>>>(static_cast<const U*>(x), tokens, units,
+                                                   x_ld * int64_t(el) / int64_t(sizeof(U)), topk, parts, rows, source,
+                                                   static_cast<U*>(out));
+    return cudaGetLastError();
+  }));
+}
+
+extern "C" int gmm_combine(const void* in, int dtype, int64_t tokens, int64_t d, int32_t topk, const int32_t* rows,
+                           const float* weights, void* out, void* stream) {
+  using namespace gmmk;
+  if (int st = check(dtype, tokens, d, topk)) return st;
+  if (tokens > 0 && (in == nullptr || rows == nullptr || out == nullptr))
+    return GMM_ERR_NULL;
+  if ((address(in) | address(out)) % (dtype == GMM_DTYPE_F32 ? 4 : 2) != 0 ||
+      (address(rows) | address(weights)) % 4 != 0)
+    return GMM_ERR_ALIGN;
+  if (int st = require_device(nullptr)) return st;
+  if (tokens == 0) return GMM_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(dtype == GMM_DTYPE_F32 ? combine<float>(in, tokens, d, topk, rows, weights, out, s)
+                                     : combine<__nv_bfloat16>(in, tokens, d, topk, rows, weights, out, s));
+}
+
+extern "C" int gmm_combine_backward(const void* dout, const void* in, int dtype, int64_t tokens, int64_t d,
+                                    int32_t topk, const int32_t* rows, const int32_t* source, const float* weights,
+                                    void* din, float* dweights, void* stream) {
+  using namespace gmmk;
+  if (int st = check(dtype, tokens, d, topk)) return st;
+  if (tokens > 0 && (dout == nullptr || in == nullptr || rows == nullptr || source == nullptr || weights == nullptr || din == nullptr || dweights == nullptr))
+    return GMM_ERR_NULL;
+  if ((address(dout) | address(in) | address(din)) % (dtype == GMM_DTYPE_F32 ? 4 : 2) != 0 ||
+      (address(rows) | address(source) | address(weights) | address(dweights)) % 4 != 0)
+    return GMM_ERR_ALIGN;
+  if (int st = require_device(nullptr)) return st;
+  if (tokens == 0) return GMM_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(dtype == GMM_DTYPE_F32
+                  ? combine_backward<float>(dout, in, tokens, d, topk, rows, source, weights, din, dweights, s)
+                  : combine_backward<__nv_bfloat16>(dout, in, tokens, d, topk, rows, source, weights, din, dweights,
+                                                    s));
+}

@@ -207,6 +207,25 @@ const char* dtype_name(int d) {
 
 }  // namespace
 
+namespace gmmk {
+
+int require_device(int* sms) {
+  DeviceInfo dev;
+  if (int st = current_device(&dev)) return st;
+  if (sms != nullptr) *sms = dev.sms;
+  return GMM_OK;
+}
+
+int record_cuda_error(int code) { return cuda_fail(code); }
+
+int byte_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint32_t* box) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rank, base, dims, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool call_log_enabled() { return log_enabled(); }
+
+}  // namespace gmmk
+
 extern "C" {
 
 size_t gmm_workspace_bytes(void) { return kWorkspaceBytes; }

@@ -147,6 +147,16 @@ cudaError_t launch_f16w(const ScaledLaunch& p, int weight_format, bool out_f32, 
 cudaError_t launch_quantize_e4m3(const void* x, int64_t m, int64_t k, int64_t group, void* q, float* scale,
                                  cudaStream_t stream);
 
+// Host helpers of gmm_api.cu for the other entry points.  require_device: GMM_OK
+// on a GB300 (with its SM count in *sms unless NULL), else the status to return.
+// record_cuda_error: keeps `code` for gmm_last_cuda_error() and returns
+// GMM_ERR_CUDA.  byte_map: a tiled tensor map over dense bytes (dims and box
+// innermost first, 128-byte swizzle).
+int require_device(int* sms);
+int record_cuda_error(int code);
+int byte_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint32_t* box);
+bool call_log_enabled();
+
 // Per-shape kernel table (tuning.cu).  kernel: a GMM_KERNEL_* id; raster 0 =
 // the default super-column width.
 int32_t tuning_rows_log2(int64_t m, int32_t num_total_groups);
