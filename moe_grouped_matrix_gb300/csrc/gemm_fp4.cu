@@ -8,27 +8,44 @@
 // accumulators in tensor memory.  Products of codes and scales are exact there;
 // only the fp32 sums round.
 //
-// The weights are the M side (128 rows of n a tile) and up to 224 of a group's
-// rows the N side, so a group of a few rows costs an MMA of N = 16 and the
-// weights' bytes, and the output is written with n along the lanes.
+// The weights are the MMA's M side and a group's rows its N side, so a group of
+// a few rows costs an MMA of N = 16 or 32 and the weights' bytes.  One kernel,
+// two shapes:
+//   pair   256 weight rows on an SM pair (tcgen05.mma.cta_group::2), 128 in each
+//          CTA, by up to 224 rows of a group, half of them in each CTA's shared
+//          memory.  Two accumulators of 224 columns, 16 columns of weight scales
+//          and 32 of row scales take 496 of the 512 columns of tensor memory;
+//          256 rows would leave one accumulator, and every tile would wait for
+//          the epilogue of the one before.
+//   single 128 weight rows on one SM by up to 64 rows: for groups of a few rows,
+//          where the time is the reading of the weights and stages are small.
 //
 // Scales reach tensor memory as the MMA wants them: for every 128 rows and 4
-// bytes of scales (64 k of NVFP4, 128 k of MXFP4) lane l of the 32 lanes holds
-// the 4 bytes of rows l, l + 32, l + 64 and l + 96.  A window of 16 scale bytes
-// of 128 rows is stored as 2 KB in row order, so a bulk copy brings it from any
-// first row, and a warp turns it into four such blocks in place: its lane l
-// reads the 16 bytes of those four rows and writes the transposed 4 x 4 words.
-// tcgen05.cp then copies each 512-byte block into tensor memory in order with
-// the MMAs.
+// bytes of scales (64 k of NVFP4, 128 k of MXFP4) lane l of 32 holds the 4 bytes
+// of rows l, l + 32, l + 64 and l + 96.  A window of 16 scale bytes of 128 rows
+// is stored as 2 KB in row order, so a bulk copy brings it from any first row,
+// and a warp turns it into four such blocks in place: its lane l reads the 16
+// bytes of those four rows and writes the transposed 4 x 4 words.  tcgen05.cp
+// then copies each 512-byte block into tensor memory in order with the MMAs; in
+// a pair the leader's copy moves both CTAs' blocks, each into its own memory.
+// In a pair each CTA holds the scales of its own weight rows and of all the
+// chunk's rows.
 //
-// Roles (288 threads): warp 0 TMA producer; warp 1 tensor memory and MMA; warps
-// 2-5 epilogue; warps 6-8 turn the scales (128 weight rows, 2 x 128 rows).
-// Tensor memory: two accumulators of 224 columns, 16 columns of weight scales
-// and 32 of row scales.
+// Each role is a warp of its own, and every loop is uniform over its warp (waits
+// end in a vote, tiles are broadcast), so that addresses and descriptors stay in
+// uniform registers: with one lane's own loop each tensor-core instruction and
+// each copy took some 80 cycles to issue, a stage over 1300 for 420 cycles of
+// MMA.  For the same reason a warp turns the whole of a stage, and has stages of
+// its own.
+//
+// Roles (512 threads): warp 0 copies codes; warp 1 tensor memory and MMA (the
+// leader's in a pair); warps 2-9 epilogue, each set of four every other 32 rows;
+// warp 10 copies scales; warps 11-15 turn them.
 #include <cuda_bf16.h>
 
 #include <climits>
 #include <cstdio>
+#include <utility>
 
 #include "../../include/libgmm_moe.h"
 #include "internal.h"
@@ -38,332 +55,553 @@
 namespace gmmk {
 namespace {
 
-constexpr int BW = 128;       // weight rows a tile
-constexpr int CHUNK = 224;    // most rows of a group a tile
-constexpr int BK = 256;       // k a stage: 128 bytes of codes
-constexpr int STAGES = 4;
-constexpr int TBOX = 32;      // rows of one copy of row codes
-constexpr int kThreads = 288;
+constexpr int BW = 128;   // weight rows a CTA
+constexpr int BK = 256;   // k a stage: 128 bytes of codes
+constexpr int kThreads = 512;
+constexpr int kTurners = 5;
 constexpr int kMaxGroups = GMM_MAX_GROUPS;
-constexpr uint32_t A_BYTES = BW * BK / 2;
-constexpr uint32_t B_BYTES = CHUNK * BK / 2;
-constexpr uint32_t TBOX_BYTES = TBOX * BK / 2;
+constexpr uint32_t ROW_BYTES = BK / 2;
+constexpr uint32_t A_BYTES = BW * ROW_BYTES;
 constexpr uint32_t SF_BYTES = 128 * 16;  // a window of 128 rows' scales
-constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TM_SFA = 2 * CHUNK, TM_SFB = TM_SFA + 16;
-static_assert(TM_SFB + 32 <= TMEM_COLS, "tensor memory budget");
+constexpr uint32_t OUT_PITCH = 80;       // of 32 bf16 columns in an epilogue warp's buffer: no bank conflicts
+constexpr uint32_t OUT_BYTES = 32 * OUT_PITCH;
 
-constexpr uint32_t OFF_A = 0;
-constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
-constexpr uint32_t OFF_SF = OFF_B + STAGES * B_BYTES;
-constexpr uint32_t OFF_CTRL = OFF_SF + STAGES * 3 * SF_BYTES;
-constexpr uint32_t OFF_FULL = OFF_CTRL;
-constexpr uint32_t OFF_EMPTY = OFF_FULL + 8 * STAGES;
-constexpr uint32_t OFF_TURNED = OFF_EMPTY + 8 * STAGES;
-constexpr uint32_t OFF_ACCF = OFF_TURNED + 8 * STAGES;
-constexpr uint32_t OFF_ACCE = OFF_ACCF + 16;
-constexpr uint32_t OFF_DONE = OFF_ACCE + 16;
-constexpr uint32_t OFF_TMEM = OFF_DONE + 8;
-constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
-constexpr uint32_t OFF_OFFS = OFF_CTRL + 256;
-constexpr uint32_t OFF_TILES = OFF_OFFS + 4 * (kMaxGroups + 4);
-constexpr uint32_t SMEM_BYTES = OFF_TILES + 4 * (kMaxGroups + 4) + 1024;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-static_assert(OFF_ABORT + 4 <= OFF_OFFS, "control block overlaps the tables");
+template <bool kPair>
+struct Shape {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kTileW = kCtas * BW;          // weight rows a tile
+  static constexpr int kChunk = kPair ? 224 : 64;    // most rows of a group a tile
+  static constexpr int kUnit = kPair ? 32 : 16;      // rows a chunk is a multiple of
+  static constexpr int kRows = kChunk / kCtas;       // of them in a CTA's shared memory
+  static constexpr int kParts = kPair ? 3 : 2;       // 128-row windows of scales: weights, rows
+  static constexpr int kStages = kPair ? 5 : 7;
+  static constexpr uint32_t B_BYTES = kRows * ROW_BYTES;
+  static constexpr uint32_t TM_SFA = 2 * kChunk, TM_SFB = TM_SFA + 16;
+  static constexpr uint32_t kColumns = kPair ? 512 : 256;  // TM_SFB + 4 * 8 (4 * 4) columns, to a power of two
+  static constexpr uint32_t OFF_A = 0;
+  static constexpr uint32_t OFF_B = OFF_A + kStages * A_BYTES;
+  static constexpr uint32_t OFF_SF = OFF_B + kStages * B_BYTES;
+  static constexpr uint32_t OFF_OUT = OFF_SF + kStages * kParts * SF_BYTES;
+  static constexpr uint32_t OFF_CTRL = OFF_OUT + 8 * OUT_BYTES;
+  static constexpr uint32_t OFF_FULL = OFF_CTRL;                   // codes (of both CTAs, the leader's)
+  static constexpr uint32_t OFF_EMPTY = OFF_FULL + 8 * kStages;    // the MMA's commit
+  static constexpr uint32_t OFF_SFULL = OFF_EMPTY + 8 * kStages;   // this CTA's scales
+  static constexpr uint32_t OFF_TURNED = OFF_SFULL + 8 * kStages;  // scales turned (in both CTAs, the leader's)
+  static constexpr uint32_t OFF_ACCF = OFF_TURNED + 8 * kStages;
+  static constexpr uint32_t OFF_ACCE = OFF_ACCF + 16;
+  static constexpr uint32_t OFF_DONE = OFF_ACCE + 16;
+  static constexpr uint32_t OFF_REPORT = OFF_DONE + 8;  // pair_report's barrier and count (leader's)
+  static constexpr uint32_t OFF_RWORD = OFF_REPORT + 8;
+  static constexpr uint32_t OFF_TMEM = OFF_RWORD + 4;
+  static constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
+  static constexpr uint32_t OFF_OFFS = OFF_CTRL + 512;
+  static constexpr uint32_t OFF_TILES = OFF_OFFS + 4 * (kMaxGroups + 4);
+  static constexpr uint32_t SMEM_BYTES = OFF_TILES + 4 * (kMaxGroups + 4) + 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(OFF_ABORT + 4 <= OFF_OFFS && OFF_REPORT % 8 == 0, "control block overlaps the tables");
+  static_assert(B_BYTES % 1024 == 0 && OFF_SF % 1024 == 0, "swizzle atoms");
+  static_assert(TM_SFB + (kPair ? 32 : 16) <= kColumns, "tensor memory budget");
+};
 
 struct Params {
   const int32_t* group_sizes;
   int32_t num_total_groups, group_offset, num_local_groups;
   int32_t m, n, k;
-  const uint8_t* lhs_scale;      // [windows, m, 16]
-  const uint8_t* rhs_scale;      // [local groups, windows, n, 16]
-  const float* lhs_row_scale;    // NULL or [m]
-  const float* rhs_row_scale;    // NULL or [local groups, n]
+  const uint8_t* lhs_scale;    // [windows, m, 16]
+  const uint8_t* rhs_scale;    // [local groups, windows, n, 16]
+  const float* lhs_row_scale;  // NULL or [m]
+  const float* rhs_row_scale;  // NULL or [local groups, n]
   void* out;
   const void* bias;
   int32_t bias_f32;
   uint32_t* err;
 };
 
-__device__ __forceinline__ int32_t chunk_rows(const GemmTile& t) { return min(CHUNK, t.row_end - t.row0); }
-__device__ __forceinline__ int32_t chunk_n(const GemmTile& t) { return (chunk_rows(t) + 15) & ~15; }
+// Maps of the row codes in boxes of 64, 32 and 16 rows: a CTA's rows of a chunk,
+// a multiple of 16 up to 112, take three copies at most.
+struct Maps {
+  CUtensorMap rhs, lhs64, lhs32, lhs16;
+};
+
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A wait of a whole warp, with one answer for all of it.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          uint32_t* err) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
+}
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                                  uint32_t* err) {
+  return __all_sync(0xffffffffu, wait_bar_cluster(bar, parity, abort_flag, err));
+}
 
 // Instruction descriptor of the block-scaled 4-bit kinds:
 //   bits 4-5 B's scale id   bits 7-9 A format (1 = e2m1)   bits 10-11 B format (1 = e2m1)
 //   bits 17-22 N >> 3   bit 23 scale format (0 = e4m3, 1 = E8M0)   bits 27-28 M >> 7
 //   bits 29-30 A's scale id: the half word of the scales' column that a K = 64 step of MXFP4 reads
 template <bool kNv>
-__device__ __forceinline__ uint32_t idesc_fp4(int n, uint32_t scale_id) {
-  return (scale_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | ((kNv ? 0u : 1u) << 23) | (1u << 27) |
-         (scale_id << 29);
+__device__ __forceinline__ uint32_t idesc_fp4(int m, int n, uint32_t scale_id) {
+  return (scale_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
+         (uint32_t(m >> 7) << 27) | (scale_id << 29);
 }
 
-template <bool kNv>
+#define GMM_MMA_FP4(group, kind)                                                                              \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::" group ".kind::" kind \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                             \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                \
+               : "memory")
+
+template <bool kPair, bool kNv>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
-  if constexpr (kNv)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+  if constexpr (kPair && kNv) GMM_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  if constexpr (kPair && !kNv) GMM_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+  if constexpr (!kPair && kNv) GMM_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  if constexpr (!kPair && !kNv) GMM_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+}
+#undef GMM_MMA_FP4
+
+// 512 bytes of scales (32 lanes of 16 bytes: unswizzled, 8-lane groups of 128 bytes one after the
+// other) to 4 columns of tensor memory, in each of its four lane quarters.
+template <bool kPair>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// 512 bytes of scales (32 lanes of 16 bytes) to 4 columns of tensor memory, in each of its four
-// lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-  // unswizzled: 8-lane groups of 128 bytes, 128 bytes apart
-  const uint64_t desc = uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    mma_commit_pair(bar, 0x3);
+  else
+    mma_commit(bar);
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-// Turns the 128 rows of 16 scale bytes at `addr` into four 512-byte blocks, in place (one warp).
+// Turns kParts windows of 128 rows of 16 scale bytes into four 512-byte blocks each, in place (one warp).
+template <int kParts>
 __device__ __forceinline__ void turn_scales(uint32_t addr, int lane) {
-  const uint4 r0 = ld_shared_v4(addr + 16u * lane), r1 = ld_shared_v4(addr + 512u + 16u * lane),
-              r2 = ld_shared_v4(addr + 1024u + 16u * lane), r3 = ld_shared_v4(addr + 1536u + 16u * lane);
+  uint4 r[kParts][4];
+#pragma unroll
+  for (int w = 0; w < kParts; ++w)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[w][q] = ld_shared_v4(addr + w * SF_BYTES + 512u * q + 16u * lane);
   __syncwarp();
-  st_shared_v4(addr + 16u * lane, r0.x, r1.x, r2.x, r3.x);
-  st_shared_v4(addr + 512u + 16u * lane, r0.y, r1.y, r2.y, r3.y);
-  st_shared_v4(addr + 1024u + 16u * lane, r0.z, r1.z, r2.z, r3.z);
-  st_shared_v4(addr + 1536u + 16u * lane, r0.w, r1.w, r2.w, r3.w);
+#pragma unroll
+  for (int w = 0; w < kParts; ++w) {
+    const uint32_t a = addr + w * SF_BYTES + 16u * lane;
+    st_shared_v4(a, r[w][0].x, r[w][1].x, r[w][2].x, r[w][3].x);
+    st_shared_v4(a + 512u, r[w][0].y, r[w][1].y, r[w][2].y, r[w][3].y);
+    st_shared_v4(a + 1024u, r[w][0].z, r[w][1].z, r[w][2].z, r[w][3].z);
+    st_shared_v4(a + 1536u, r[w][0].w, r[w][1].w, r[w][2].w, r[w][3].w);
+  }
 }
 
-template <bool kNv, bool kOutF32>
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_lhs, const __grid_constant__ CUtensorMap tm_rhs,
-                    const Params p) {
+// 16 lanes by 32 columns of tensor memory: registers 4g, 4g + 1 hold lane t / 4 and columns
+// 8g + 2 (t % 4) and the next, 4g + 2, 4g + 3 the same of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, stored transposed: register j of thread t holds matrix j's
+// column t / 4 of rows 2 (t % 4) and the next; lane 8j + r gives the address of its row r.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float load_bias(const Params& p, int64_t i) {
+  return p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + i)
+                    : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[i]);
+}
+
+template <bool kPair, bool kNv, bool kOutF32>
+__global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_constant__ Maps maps, const Params p) {
+  using S = Shape<kPair>;
+  constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform(int32_t(threadIdx.x >> 5));
   const int lane = threadIdx.x & 31;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
-  int32_t* offs = reinterpret_cast<int32_t*>(smem + OFF_OFFS);
-  int32_t* tiles = reinterpret_cast<int32_t*>(smem + OFF_TILES);
-  auto full_bar = [&](uint32_t s) { return sbase + OFF_FULL + 8 * s; };
-  auto empty_bar = [&](uint32_t s) { return sbase + OFF_EMPTY + 8 * s; };
-  auto turned_bar = [&](uint32_t s) { return sbase + OFF_TURNED + 8 * s; };
-  auto accf_bar = [&](uint32_t b) { return sbase + OFF_ACCF + 8 * b; };
-  auto acce_bar = [&](uint32_t b) { return sbase + OFF_ACCE + 8 * b; };
-  const uint32_t done_bar = sbase + OFF_DONE;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int32_t pair = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int32_t npairs = kPair ? gridDim.x >> 1 : gridDim.x;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_ABORT);
+  int32_t* offs = reinterpret_cast<int32_t*>(smem + S::OFF_OFFS);
+  int32_t* tiles = reinterpret_cast<int32_t*>(smem + S::OFF_TILES);
+  auto full_bar = [&](uint32_t s) { return sbase + S::OFF_FULL + 8 * s; };
+  auto empty_bar = [&](uint32_t s) { return sbase + S::OFF_EMPTY + 8 * s; };
+  auto sfull_bar = [&](uint32_t s) { return sbase + S::OFF_SFULL + 8 * s; };
+  auto turned_bar = [&](uint32_t s) { return sbase + S::OFF_TURNED + 8 * s; };
+  auto accf_bar = [&](uint32_t b) { return sbase + S::OFF_ACCF + 8 * b; };
+  auto acce_bar = [&](uint32_t b) { return sbase + S::OFF_ACCE + 8 * b; };
+  const uint32_t done_bar = sbase + S::OFF_DONE;
   const int32_t go = p.group_offset;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-      mbar_init(turned_bar(s), 3);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);             // the (leader's) expect_tx; bytes from both CTAs of a pair
+      mbar_init(empty_bar(s), 1);            // the MMA's commit, to both CTAs of a pair
+      mbar_init(sfull_bar(s), 1);            // this CTA's expect_tx
+      mbar_init(turned_bar(s), S::kCtas);    // a turning warp of each CTA
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), 128);
+      mbar_init(accf_bar(b), 1);             // the MMA's commit, to both CTAs of a pair
+      mbar_init(acce_bar(b), 8 * S::kCtas);  // one lane of each epilogue warp
     }
     mbar_init(done_bar, 1);
+    mbar_init(sbase + S::OFF_REPORT, 1);
     *abort_flag = 0u;
     fence_mbar_init();
-    tma_prefetch(&tm_lhs);
-    tma_prefetch(&tm_rhs);
+    tma_prefetch(&maps.rhs);
+    tma_prefetch(&maps.lhs16);
   }
   if (warp == 1) {
-    tmem_alloc(sbase + OFF_TMEM, TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(sbase + S::OFF_TMEM, S::kColumns);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(sbase + S::OFF_TMEM, S::kColumns);
+      tmem_relinquish();
+    }
   }
   if (warp == 2) {
     build_group_offsets(p.group_sizes, p.num_total_groups, p.m, offs, p.err);
-    build_tile_prefix(offs, go, p.num_local_groups, CHUNK, tiles);
+    build_tile_prefix(offs, go, p.num_local_groups, S::kChunk, tiles);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+  const uint32_t tmem_base = uniform(*reinterpret_cast<volatile uint32_t*>(smem + S::OFF_TMEM));
 
-  const int32_t t_tiles = tiles[p.num_local_groups];
-  const int32_t n_tiles = (p.n + BW - 1) / BW;
+  const int32_t t_tiles = uniform(tiles[p.num_local_groups]);
+  const int32_t n_tiles = (p.n + S::kTileW - 1) / S::kTileW;
   const int32_t k_blocks = (p.k + BK - 1) / BK;
   const int32_t windows = (p.k + (kNv ? 255 : 511)) / (kNv ? 256 : 512);
   const int32_t total = t_tiles * n_tiles;
-  // group by group, blocks of 16 chunks meeting the n tiles in turn: each weight tile comes from
-  // memory once for the block, whose rows stay in L2
-  auto item_of = [&](int32_t w) {
-    return decode_gemm_tile(w, t_tiles, n_tiles, -16, tiles, offs, go, p.num_local_groups, CHUNK);
+  // Group by group, blocks of 16 chunks meeting the n tiles in turn: each weight tile comes from
+  // memory once for the block, whose rows stay in L2.  A group's units of rows are spread evenly
+  // over its chunks, so that no tile is left with a few.
+  auto lane_tile = [&](int32_t w) {
+    GemmTile t = decode_gemm_tile(w, t_tiles, n_tiles, -16, tiles, offs, go, p.num_local_groups, S::kChunk);
+    const int32_t start = offs[go + t.local_group];
+    const int32_t chunks = tiles[t.local_group + 1] - tiles[t.local_group];
+    const int32_t i = (t.row0 - start) / S::kChunk;
+    const int32_t units = (t.row_end - start + S::kUnit - 1) / S::kUnit;
+    t.row0 = start + int32_t(int64_t(i) * units / chunks) * S::kUnit;
+    t.row_end = min(t.row_end, start + int32_t(int64_t(i + 1) * units / chunks) * S::kUnit);
+    return t;
   };
+  auto tile_of = [&](int32_t w) {  // a whole warp's
+    const GemmTile t = lane_tile(w);
+    return GemmTile{uniform(t.local_group), uniform(t.row0), uniform(t.row_end), uniform(t.n_tile)};
+  };
+  auto chunk_n = [](const GemmTile& t) { return (t.row_end - t.row0 + S::kUnit - 1) / S::kUnit * S::kUnit; };
+  // bytes of one CTA's copies of codes in a stage of tile t
+  auto code_bytes = [&](const GemmTile& t) { return A_BYTES + uint32_t(chunk_n(t) / S::kCtas) * ROW_BYTES; };
 
+  uint32_t issued = 0;  // codes: stages of the sequence this CTA issued (leader: armed)
   if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, pend_mask = 0;
-      uint32_t pend_par[STAGES];
+    // ---------------------------------------------------------------- copies of codes (both CTAs)
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    const uint32_t full0 = kPair ? mapa_shared(full_bar(0), 0) : full_bar(0);
+    for (int32_t w = pair; w < total && ok; w += npairs) {
+      const GemmTile t = tile_of(w);
+      const int32_t rows = chunk_n(t) / S::kCtas;  // of the chunk that this CTA holds
+      const int32_t trow = t.row0 + int32_t(rank) * rows;
+      const int32_t wrow = t.n_tile * S::kTileW + int32_t(rank) * BW;
+      const uint32_t bytes = S::kCtas * code_bytes(t);
+      for (int32_t kb = 0; kb < k_blocks; ++kb) {
+        if (!wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        if (elected()) {
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
+          const uint32_t fb = full0 + 8 * stage;
+          const int32_t kc = kb * int32_t(ROW_BYTES);
+          uint32_t b_dst = sbase + S::OFF_B + stage * S::B_BYTES;
+          int32_t r = trow;
+          auto rows_of = [&](const CUtensorMap* map, int32_t n) {
+            if constexpr (kPair)
+              tma_load_2d_pair(b_dst, map, fb, kc, r);
+            else
+              tma_load_2d(b_dst, map, fb, kc, r);
+            b_dst += uint32_t(n) * ROW_BYTES;
+            r += n;
+          };
+          if constexpr (kPair)
+            tma_load_3d_pair(sbase + S::OFF_A + stage * A_BYTES, &maps.rhs, fb, kc, wrow, t.local_group);
+          else
+            tma_load_3d(sbase + S::OFF_A + stage * A_BYTES, &maps.rhs, fb, kc, wrow, t.local_group);
+          if (rows & 64) rows_of(&maps.lhs64, 64);
+          if (rows & 32) rows_of(&maps.lhs32, 32);
+          if (rows & 16) rows_of(&maps.lhs16, 16);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if constexpr (kPair) {
+      if (!leader && lane == 0) pair_report(sbase + S::OFF_REPORT, sbase + S::OFF_RWORD, issued);
+    } else if (!ok) {  // the copies in flight: the last kStages at most
+      for (uint32_t i = issued > kStages ? issued - kStages : 0u; i < issued; ++i)
+        drain_bar(full_bar(i % kStages), (i / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (leader) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (int32_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const GemmTile t = item_of(w);
-        const int32_t nbox = (chunk_rows(t) + TBOX - 1) / TBOX;
-        const int32_t n0 = t.n_tile * BW;
-        const uint32_t sfa_bytes = uint32_t(min(BW, p.n - n0)) * 16u, sfb_bytes = uint32_t(chunk_rows(t)) * 16u;
+      for (int32_t w = pair; w < total && ok; w += npairs) {
+        const GemmTile t = tile_of(w);
+        const int32_t ncols = chunk_n(t);
+        if (!wait_warp_cluster(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * S::kChunk;
         for (int32_t kb = 0; kb < k_blocks; ++kb) {
-          if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+          if (!wait_warp_cluster(turned_bar(stage), phase, abort_flag, p.err) ||
+              !wait_warp(full_bar(stage), phase, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          const uint32_t fb = full_bar(stage);
-          mbar_arrive_expect_tx(fb, A_BYTES + uint32_t(nbox) * TBOX_BYTES + sfa_bytes + sfb_bytes);
-          const uint32_t b_dst = sbase + OFF_B + stage * B_BYTES, sf_dst = sbase + OFF_SF + stage * 3 * SF_BYTES;
-          const int64_t win = kNv ? kb : kb >> 1;
-          tma_load_3d(sbase + OFF_A + stage * A_BYTES, &tm_rhs, fb, kb * (BK / 2), n0, t.local_group);
-          for (int32_t j = 0; j < nbox; ++j)
-            tma_load_2d(b_dst + j * TBOX_BYTES, &tm_lhs, fb, kb * (BK / 2), t.row0 + TBOX * j);
-          bulk_load(sf_dst, p.rhs_scale + ((t.local_group * int64_t(windows) + win) * p.n + n0) * 16, sfa_bytes, fb);
-          bulk_load(sf_dst + SF_BYTES, p.lhs_scale + (win * p.m + t.row0) * 16, sfb_bytes, fb);
-          pend_par[stage] = phase;
-          pend_mask |= 1u << stage;
-          if (++stage == STAGES) {
+          tc_fence_after();
+          if (elected()) {
+            // a stage uses 4 blocks of a window (NVFP4) or half of them (MXFP4)
+            const uint32_t sf =
+                sbase + S::OFF_SF + stage * S::kParts * SF_BYTES + (kNv ? 0u : 1024u * uint32_t(kb & 1));
+#pragma unroll
+            for (uint32_t j = 0; j < (kNv ? 4 : 2); ++j) {
+              copy_scales<kPair>(tmem_base + S::TM_SFA + 4 * j, sf + 512u * j);
+              copy_scales<kPair>(tmem_base + S::TM_SFB + (kPair ? 8 : 4) * j, sf + SF_BYTES + 512u * j);
+              if (kPair && ncols > 128)
+                copy_scales<kPair>(tmem_base + S::TM_SFB + 8 * j + 4, sf + 2 * SF_BYTES + 512u * j);
+            }
+            const uint64_t ad = sw128_desc(sbase + S::OFF_A + stage * A_BYTES, 16, 1024);
+            const uint64_t bd = sw128_desc(sbase + S::OFF_B + stage * S::B_BYTES, 16, 1024);
+#pragma unroll
+            for (uint32_t kk = 0; kk < BK / 64; ++kk) {
+              const uint32_t j = kNv ? kk : kk >> 1;
+              mma_fp4<kPair, kNv>(d_tmem, ad + 2 * kk, bd + 2 * kk,
+                                  idesc_fp4<kNv>(S::kTileW, ncols, kNv ? 0u : 2u * (kk & 1)),
+                                  tmem_base + S::TM_SFA + 4 * j, tmem_base + S::TM_SFB + (kPair ? 8 : 4) * j,
+                                  (uint32_t(kb) | kk) != 0 ? 1u : 0u);
+            }
+            commit<kPair>(empty_bar(stage));
+            if (kb == k_blocks - 1) commit<kPair>(accf_bar(acc));
+          }
+          __syncwarp();
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-      }
-      if (!ok) {
-        for (int s = 0; s < STAGES; ++s)
-          if (pend_mask >> s & 1u) drain_bar(full_bar(s), pend_par[s]);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
-    bool ok = true;
-    for (int32_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-      const GemmTile t = item_of(w);
-      const int32_t ncols = chunk_n(t);
-      if (!wait_bar(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.err)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * CHUNK;
-      for (int32_t kb = 0; kb < k_blocks; ++kb) {
-        if (!wait_bar(full_bar(stage), phase, abort_flag, p.err) ||
-            !wait_bar(turned_bar(stage), phase, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a0 = sbase + OFF_A + stage * A_BYTES;
-          const uint32_t b0 = sbase + OFF_B + stage * B_BYTES;
-          const uint32_t sf = sbase + OFF_SF + stage * 3 * SF_BYTES;
-          // a stage uses 4 blocks of a window (NVFP4) or half of them (MXFP4)
-          const int first = kNv ? 0 : 2 * (kb & 1);
-#pragma unroll
-          for (int j = 0; j < (kNv ? 4 : 2); ++j) {
-            const uint32_t blk = 512u * uint32_t(first + j);
-            copy_scales(tmem_base + TM_SFA + 4 * j, sf + blk);
-            copy_scales(tmem_base + TM_SFB + 8 * j, sf + SF_BYTES + blk);
-            if (ncols > 128) copy_scales(tmem_base + TM_SFB + 8 * j + 4, sf + 2 * SF_BYTES + blk);
-          }
-#pragma unroll
-          for (int kk = 0; kk < BK / 64; ++kk) {
-            const uint64_t ad = sw128_desc(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = sw128_desc(b0 + kk * 32, 16, 1024);
-            const int j = kNv ? kk : kk >> 1;
-            mma_fp4<kNv>(d_tmem, ad, bd, idesc_fp4<kNv>(ncols, kNv ? 0u : 2u * (kk & 1)), tmem_base + TM_SFA + 4 * j,
-                         tmem_base + TM_SFB + 8 * j, (kb | kk) != 0 ? 1u : 0u);
-          }
-          mma_commit(empty_bar(stage));
-        }
-        __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
         }
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(accf_bar(acc));
+      if (elected()) {
+        if constexpr (kPair)
+          mma_commit_pair(done_bar, 0x1);
+        else
+          mma_commit(done_bar);
+        drain_bar(done_bar, 0);
+      }
       __syncwarp();
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
     }
-    if (lane == 0) {
-      mma_commit(done_bar);
-      drain_bar(done_bar, 0);
-    }
-    __syncwarp();
-  } else if (warp >= 6) {
-    // ---------------------------------------------------------------- scales into the MMA's order
-    const int part = warp - 6;  // the weights' 128 rows, the first and the second 128 of the chunk
-    uint32_t stage = 0, phase = 0;
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- copies of scales (both CTAs)
+    uint32_t stage = 0, phase = 0, mine = 0;
     bool ok = true;
-    for (int32_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-      const bool used = part < 2 || chunk_n(item_of(w)) > 128;
+    for (int32_t w = pair; w < total && ok; w += npairs) {
+      const GemmTile t = tile_of(w);
+      const int32_t wrow = t.n_tile * S::kTileW + int32_t(rank) * BW;
+      const int32_t wrows = max(0, min(BW, p.n - wrow));
+      const uint32_t a_bytes = uint32_t(wrows) * 16u, b_bytes = uint32_t(t.row_end - t.row0) * 16u;
+      const uint8_t* a_src = p.rhs_scale + (int64_t(t.local_group) * windows * p.n + wrow) * 16;
+      const uint8_t* b_src = p.lhs_scale + int64_t(t.row0) * 16;
       for (int32_t kb = 0; kb < k_blocks; ++kb) {
-        if (!wait_bar(full_bar(stage), phase, abort_flag, p.err)) {
+        if (!wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        if (used) {
-          turn_scales(sbase + OFF_SF + stage * 3 * SF_BYTES + part * SF_BYTES, lane);
-          fence_proxy_async_smem();
+        if (elected()) {
+          const uint32_t dst = sbase + S::OFF_SF + stage * S::kParts * SF_BYTES;
+          const int64_t win = kNv ? kb : kb >> 1;
+          mbar_arrive_expect_tx(sfull_bar(stage), a_bytes + b_bytes);
+          if (wrows > 0) bulk_load(dst, a_src + win * p.n * 16, a_bytes, sfull_bar(stage));
+          bulk_load(dst + SF_BYTES, b_src + win * p.m * 16, b_bytes, sfull_bar(stage));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(turned_bar(stage));
-        if (++stage == STAGES) {
+        ++mine;
+        if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      for (uint32_t i = mine > kStages ? mine - kStages : 0u; i < mine; ++i)
+        drain_bar(sfull_bar(i % kStages), (i / kStages) & 1u);
+    }
+  } else if (warp > 10) {
+    // ---------------------------------------------------------------- scales into the MMA's order (both CTAs)
+    const int64_t stages = pair < total ? int64_t((total - 1 - pair) / npairs + 1) * k_blocks : 0;
+    const uint32_t turned0 = kPair ? mapa_shared(turned_bar(0), 0) : turned_bar(0);
+    // A warp has stages of its own: a parity wait tells a phase from the one before it only, so
+    // whoever waits on a barrier has to have seen each of its phases.
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t i0 = 0; i0 < stages && ok; i0 += kStages, phase ^= 1u) {
+      for (int32_t stage = warp - 11; stage < kStages && i0 + stage < stages; stage += kTurners) {
+        if (!wait_warp(sfull_bar(stage), phase, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        turn_scales<S::kParts>(sbase + S::OFF_SF + stage * S::kParts * SF_BYTES, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_cluster(turned0 + 8 * stage);
+          else
+            mbar_arrive(turned0 + 8 * stage);
         }
       }
     }
   } else {
-    // ---------------------------------------------------------------- epilogue
-    // TMEM lane = weight row = output column; TMEM column = row of the chunk.
-    const int quarter = warp & 3;
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    // TMEM lane = this CTA's weight row = output column; TMEM column = row of the chunk.
+    const int quarter = warp & 3, set = (warp - 2) >> 2;
+    const uint32_t buf = sbase + S::OFF_OUT + uint32_t(warp - 2) * OUT_BYTES;
+    const uint32_t acce0 = kPair ? mapa_shared(acce_bar(0), 0) : acce_bar(0);
     uint32_t acc = 0, acc_phase = 0;
-    for (int32_t w = blockIdx.x; w < total; w += gridDim.x) {
-      const GemmTile t = item_of(w);
-      const int32_t rows = chunk_rows(t), ncols = chunk_n(t);
-      const int32_t col = t.n_tile * BW + quarter * 32 + lane;
-      const bool col_ok = col < p.n;
-      float bias = 0.f, ws = 1.f;
-      if (col_ok) {
-        const int64_t bi = int64_t(t.local_group) * p.n + col;
-        if (p.bias != nullptr)
-          bias = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + bi)
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[bi]);
-        if (p.rhs_row_scale != nullptr) ws = __ldg(p.rhs_row_scale + bi);
-      }
-      if (!wait_bar(accf_bar(acc), acc_phase, abort_flag, p.err)) break;
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + acc * CHUNK;
-#pragma unroll 1
-      for (int32_t c0 = 0; c0 < ncols; c0 += 32) {
-        uint32_t v[32];
-        const float rs =
-            p.lhs_row_scale != nullptr && c0 + lane < rows ? __ldg(p.lhs_row_scale + t.row0 + c0 + lane) : 1.f;
-        tmem_ld_32cols(tbase + c0, v);
-        if (c0 + 32 >= ncols) {
-          tc_fence_before();
-          mbar_arrive(acce_bar(acc));
-        }
+    for (int32_t w = pair; w < total; w += npairs) {
+      const GemmTile t = tile_of(w);
+      const int32_t rows = t.row_end - t.row0, ncols = chunk_n(t);
+      const int32_t col0 = t.n_tile * S::kTileW + int32_t(rank) * BW + quarter * 32;
+      const int64_t w0 = int64_t(t.local_group) * p.n;
+      // bf16: this thread's weight rows are lane / 4 + 8 i; f32: weight row lane (i = 0)
+      float ws[4], bias[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float r = fmaf(__uint_as_float(v[i]) * __shfl_sync(0xffffffffu, rs, i), ws, bias);
-          if (col_ok && c0 + i < rows) {
-            const int64_t o = int64_t(t.row0 + c0 + i) * p.n + col;
-            if constexpr (kOutF32)
-              static_cast<float*>(p.out)[o] = r;
-            else
-              static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(r);
+      for (int i = 0; i < (kOutF32 ? 1 : 4); ++i) {
+        const int32_t c = col0 + (kOutF32 ? lane : lane / 4 + 8 * i);
+        ws[i] = c < p.n && p.rhs_row_scale != nullptr ? __ldg(p.rhs_row_scale + w0 + c) : 1.f;
+        bias[i] = c < p.n && p.bias != nullptr ? load_bias(p, w0 + c) : 0.f;
+      }
+      constexpr int kBlocks = (S::kChunk / 32 + 1) / 2;  // of 32 rows, for each set
+      float rs[kBlocks];
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int32_t r = 32 * (2 * i + set) + lane;
+        rs[i] = p.lhs_row_scale != nullptr && r < rows ? __ldg(p.lhs_row_scale + t.row0 + r) : 1.f;
+      }
+      if (!wait_warp(accf_bar(acc), acc_phase, abort_flag, p.err)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + acc * S::kChunk;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_cluster(acce0 + 8 * acc);
+          else
+            mbar_arrive(acce0 + 8 * acc);
+        }
+      };
+      if (32 * set >= ncols) release();
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const int32_t c0 = 32 * (2 * b + set);
+        if (c0 < ncols) {
+          const bool last = c0 + 64 >= ncols;
+          if constexpr (kOutF32) {
+            uint32_t v[32];
+            tmem_ld_32cols(tbase + c0, v);
+            if (last) release();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float r = fmaf(__uint_as_float(v[i]) * __shfl_sync(0xffffffffu, rs[b], i), ws[0], bias[0]);
+              if (col0 + lane < p.n && c0 + i < rows)
+                static_cast<float*>(p.out)[int64_t(t.row0 + c0 + i) * p.n + col0 + lane] = r;
+            }
+          } else {
+            uint32_t v[2][16];
+            tmem_ld_16x32(tbase + c0, v[0]);
+            tmem_ld_16x32(tbase + c0 + (16u << 16), v[1]);
+            tmem_wait_ld16(v[0]);
+            tmem_wait_ld16(v[1]);
+            if (last) release();
+            const uint32_t at = buf + uint32_t(8 * (lane >> 4) + (lane & 7)) * OUT_PITCH + uint32_t(lane >> 3 & 1) * 16u;
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+              float r[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                r[i] = __shfl_sync(0xffffffffu, rs[b], 8 * (g + i / 2) + 2 * (lane & 3) + (i & 1));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t m[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // matrix q: rows 8 (g + q / 2) .. and columns 16 h + 8 (q & 1) ..
+                  const int i = 4 * (g + q / 2) + 2 * (q & 1), f = 2 * h + (q & 1);
+                  m[q] = pack_bf16x2(fmaf(__uint_as_float(v[h][i]) * r[q & 2], ws[f], bias[f]),
+                                     fmaf(__uint_as_float(v[h][i + 1]) * r[(q & 2) + 1], ws[f], bias[f]));
+                }
+                stmatrix_trans(at + uint32_t(8 * g) * OUT_PITCH + uint32_t(h) * 32u, m[0], m[1], m[2], m[3]);
+              }
+            }
+            __syncwarp();
+            const int32_t c = col0 + 8 * (lane & 3);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + c0) * p.n + c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int32_t r = 8 * q + (lane >> 2);
+              const uint4 x = ld_shared_v4(buf + uint32_t(r) * OUT_PITCH + uint32_t(lane & 3) * 16u);
+              if (c < p.n && c0 + r < rows) st_global_v4(o + int64_t(r) * p.n, x.x, x.y, x.z, x.w);
+            }
+            __syncwarp();
           }
         }
       }
@@ -378,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t hi_begin = int64_t(offs[go + p.num_local_groups]) * row_bytes;
     const int64_t n_lo = lo_bytes / 16;
     const int64_t n_all = n_lo + (int64_t(p.m) * row_bytes - hi_begin) / 16;
-    const int64_t stride = int64_t(gridDim.x) * 128;
-    for (int64_t i = int64_t(blockIdx.x) * 128 + (threadIdx.x - 64); i < n_all; i += stride) {
+    const int64_t stride = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + (threadIdx.x - 64); i < n_all; i += stride) {
       const int64_t byte = i < n_lo ? i * 16 : hi_begin + (i - n_lo) * 16;
       st_global_v4(static_cast<uint8_t*>(p.out) + byte, 0u, 0u, 0u, 0u);
     }
@@ -387,20 +625,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) {
+    if (leader && warp == 0 && lane == 0 && *abort_flag) {
+      st_shared_cluster_u32(mapa_shared(sbase + S::OFF_ABORT, 1), 1u);  // the follower's waits end too
+      // stage i of the sequence belongs to the pair's (i / k_blocks)-th work item
+      pair_drain<kStages>(full_bar(0), sbase + S::OFF_REPORT, sbase + S::OFF_RWORD, issued, kWaitLimitCycles,
+                          [&](uint32_t i) {
+                            return code_bytes(lane_tile(pair + int32_t(i / uint32_t(k_blocks)) * npairs));
+                          });
+    }
+    cluster_sync();  // the leader's MMAs and every copy are done; no signal targets either CTA any more
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem_base, S::kColumns);
+    else
+      tmem_dealloc(tmem_base, S::kColumns);
   }
 }
 
-template <bool kNv, bool kOutF32>
-cudaError_t launch(const CUtensorMap& tm_lhs, const CUtensorMap& tm_rhs, const Params& p, int grid,
-                   cudaStream_t stream) {
-  auto kern = gemm_fp4_kernel<kNv, kOutF32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
+template <bool kPair, bool kNv, bool kOutF32>
+cudaError_t launch(const Maps& maps, const Params& p, int sms, cudaStream_t stream) {
+  using S = Shape<kPair>;
+  auto kern = gemm_fp4_kernel<kPair, kNv, kOutF32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM_BYTES));
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, SMEM_BYTES, stream>>>(tm_lhs, tm_rhs, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPair ? sms & ~1 : sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = kPair ? 1 : 0;
+  if (kPair) {
+    // One pair per co-resident cluster slot (persistent kernel).
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorLaunchOutOfResources;
+    if (2 * clusters < int(cfg.gridDim.x)) cfg.gridDim.x = unsigned(2 * clusters);
+  }
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <bool kPair>
+cudaError_t launch_shape(const Maps& maps, const Params& p, bool nv, bool out_f32, int sms, cudaStream_t stream) {
+  if (nv)
+    return out_f32 ? launch<kPair, true, true>(maps, p, sms, stream) : launch<kPair, true, false>(maps, p, sms, stream);
+  return out_f32 ? launch<kPair, false, true>(maps, p, sms, stream) : launch<kPair, false, false>(maps, p, sms, stream);
 }
 
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
@@ -427,7 +704,7 @@ extern "C" int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const
       num_local_groups > num_total_groups)
     return GMM_ERR_SHAPE;
   if (group_offset < 0 || group_offset > num_total_groups - num_local_groups) return GMM_ERR_GROUP_OFFSET;
-  if (((m + CHUNK - 1) / CHUNK + num_local_groups) * ((n + BW - 1) / BW) > INT32_MAX) return GMM_ERR_SHAPE;
+  if (((m + 63) / 64 + num_local_groups) * ((n + BW - 1) / BW) > INT32_MAX) return GMM_ERR_SHAPE;
   if (!aligned(lhs_codes, 16) || !aligned(lhs_block_scale, 16) || !aligned(rhs_codes, 16) ||
       !aligned(rhs_block_scale, 16) || !aligned(out, 16) || !aligned(lhs_row_scale, 4) || !aligned(rhs_row_scale, 4) ||
       !aligned(rhs_bias, bias_dtype == GMM_DTYPE_F32 ? 4 : 2) || !aligned(group_sizes, 4))
@@ -437,30 +714,30 @@ extern "C" int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const
   int sms = 0;
   if (int st = require_device(&sms)) return st;
   if (m == 0) return GMM_OK;
-  CUtensorMap tm_lhs, tm_rhs;
-  {
+  const bool pair = m >= int64_t(16) * num_total_groups;
+  Maps maps;
+  for (const auto& [map, rows] : {std::pair<CUtensorMap*, uint32_t>(&maps.lhs64, 64u), {&maps.lhs32, 32u},
+                                  {&maps.lhs16, 16u}}) {
     const uint64_t dims[2] = {uint64_t(k / 2), uint64_t(m)};
-    const uint32_t box[2] = {BK / 2, TBOX};
-    if (int st = byte_map(&tm_lhs, 2, lhs_codes, dims, box)) return st;
+    const uint32_t box[2] = {BK / 2, rows};
+    if (int st = byte_map(map, 2, lhs_codes, dims, box)) return st;
   }
   {
     const uint64_t dims[3] = {uint64_t(k / 2), uint64_t(n), uint64_t(num_local_groups)};
     const uint32_t box[3] = {BK / 2, BW, 1};
-    if (int st = byte_map(&tm_rhs, 3, rhs_codes, dims, box)) return st;
+    if (int st = byte_map(&maps.rhs, 3, rhs_codes, dims, box)) return st;
   }
   const Params p{group_sizes, num_total_groups, group_offset, num_local_groups, int32_t(m), int32_t(n), int32_t(k),
                  static_cast<const uint8_t*>(lhs_block_scale), static_cast<const uint8_t*>(rhs_block_scale),
                  lhs_row_scale, rhs_row_scale, out, rhs_bias, bias_dtype == GMM_DTYPE_F32 ? 1 : 0,
                  static_cast<uint32_t*>(workspace)};
   if (call_log_enabled())
-    std::fprintf(stderr, "libgmm: gmm_fp4 m=%lld k=%lld n=%lld groups=%d local=%d offset=%d format=%s out=%s\n",
+    std::fprintf(stderr, "libgmm: gmm_fp4 m=%lld k=%lld n=%lld groups=%d local=%d offset=%d format=%s out=%s kernel=%s\n",
                  (long long)m, (long long)k, (long long)n, num_total_groups, num_local_groups, group_offset,
-                 nv ? "nvfp4" : "mxfp4", out_dtype == GMM_DTYPE_F32 ? "f32" : "bf16");
+                 nv ? "nvfp4" : "mxfp4", out_dtype == GMM_DTYPE_F32 ? "f32" : "bf16",
+                 pair ? "pair" : "single");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f32 = out_dtype == GMM_DTYPE_F32;
-  const cudaError_t e = nv ? (f32 ? launch<true, true>(tm_lhs, tm_rhs, p, sms, s)
-                                  : launch<true, false>(tm_lhs, tm_rhs, p, sms, s))
-                           : (f32 ? launch<false, true>(tm_lhs, tm_rhs, p, sms, s)
-                                  : launch<false, false>(tm_lhs, tm_rhs, p, sms, s));
+  const cudaError_t e = pair ? launch_shape<true>(maps, p, nv, f32, sms, s) : launch_shape<false>(maps, p, nv, f32, sms, s);
   return e == cudaSuccess ? GMM_OK : record_cuda_error(e);
 }

@@ -211,6 +211,33 @@ def test_product(case, out_dtype, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("name,groups,mean,k,n", [("few rows", 64, 4, 4096, 1024), ("some rows", 32, 12, 2080, 2048),
+                                                  ("many rows", 8, 700, 4096, 4096), ("ragged", 128, 60, 1056, 1032)])
+def test_long_runs_of_tiles(name, groups, mean, k, n, out_dtype, fmt):
+    """Several tiles for every SM and many times the pipeline's stages for each, several times over."""
+    rng = np.random.default_rng(groups)
+    sizes = rng.poisson(mean * rng.exponential(1.0, groups))
+    m = int(sizes.sum()) + 3
+    x = torch.randn((m, k), device=DEV).to(torch.bfloat16)
+    wv = (0.1 * torch.randn((groups, n, k), device=DEV)).to(torch.bfloat16)
+    lhs, rhs = G.quantize_fp4(x, fmt), G.quantize_fp4(wv, fmt)
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    first = G.gmm_fp4(lhs, rhs, gs, out_dtype=out_dtype)
+    for _ in range(4):
+        assert torch.equal(G.gmm_fp4(lhs, rhs, gs, out_dtype=out_dtype), first)
+    assert G.read_device_errors() == 0
+    a, w = G.dequantize_fp4(lhs, torch.float32), G.dequantize_fp4(rhs, torch.float32)
+    at = 0
+    for g, size in enumerate(sizes.tolist()):
+        a64, w64, got = a[at:at + size].double(), w[g].double(), first[at:at + size].double()
+        ref, mag = a64 @ w64.T, a64.abs() @ w64.abs().T
+        assert ((got - ref).abs() <= (k / 16 + 8) * 2.0 ** -21 * mag + UNIT[out_dtype] * ref.abs()).all(), g
+        at += size
+    assert first[at:].abs().max() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_every_code_and_scale(fmt):
     """Each e2m1 code against each, and each finite scale byte, one block at a time (sums of one term)."""
     k = R.BLOCK[fmt] * 16
