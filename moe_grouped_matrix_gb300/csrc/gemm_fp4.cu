@@ -83,22 +83,22 @@ struct Shape {
   static constexpr uint32_t OFF_SF = OFF_B + kStages * B_BYTES;
   static constexpr uint32_t OFF_OUT = OFF_SF + kStages * kParts * SF_BYTES;
   static constexpr uint32_t OFF_CTRL = OFF_OUT + 8 * OUT_BYTES;
-  static constexpr uint32_t OFF_FULL = OFF_CTRL;                   // codes (of both CTAs, the leader's)
+  static constexpr uint32_t OFF_FULL = OFF_CTRL;                   // codes, scales turned (of both CTAs, the leader's)
   static constexpr uint32_t OFF_EMPTY = OFF_FULL + 8 * kStages;    // the MMA's commit
   static constexpr uint32_t OFF_SFULL = OFF_EMPTY + 8 * kStages;   // this CTA's scales
-  static constexpr uint32_t OFF_TURNED = OFF_SFULL + 8 * kStages;  // scales turned (in both CTAs, the leader's)
-  static constexpr uint32_t OFF_ACCF = OFF_TURNED + 8 * kStages;
+  static constexpr uint32_t OFF_ACCF = OFF_SFULL + 8 * kStages;
   static constexpr uint32_t OFF_ACCE = OFF_ACCF + 16;
   static constexpr uint32_t OFF_DONE = OFF_ACCE + 16;
   static constexpr uint32_t OFF_REPORT = OFF_DONE + 8;  // pair_report's barrier and count (leader's)
   static constexpr uint32_t OFF_RWORD = OFF_REPORT + 8;
   static constexpr uint32_t OFF_TMEM = OFF_RWORD + 4;
   static constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
+  static constexpr uint32_t OFF_SIGNAL = (OFF_ABORT + 4 + 15) / 16 * 16;  // 16 bytes, see signal_leader
   static constexpr uint32_t OFF_OFFS = OFF_CTRL + 512;
   static constexpr uint32_t OFF_TILES = OFF_OFFS + 4 * (kMaxGroups + 4);
   static constexpr uint32_t SMEM_BYTES = OFF_TILES + 4 * (kMaxGroups + 4) + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(OFF_ABORT + 4 <= OFF_OFFS && OFF_REPORT % 8 == 0, "control block overlaps the tables");
+  static_assert(OFF_SIGNAL + 16 <= OFF_OFFS && OFF_REPORT % 8 == 0, "control block overlaps the tables");
   static_assert(B_BYTES % 1024 == 0 && OFF_SF % 1024 == 0, "swizzle atoms");
   static_assert(TM_SFB + (kPair ? 32 : 16) <= kColumns, "tensor memory budget");
 };
@@ -196,6 +196,19 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// Tells the leader that this CTA's scales of a stage are turned: a copy of 16 bytes to the same place
+// there, whose arrival counts on the leader's barrier.  The copy is an operation of the async proxy,
+// ordered after the turned scales by the fence before it, as the MMA's reading of them has to be; an
+// mbarrier arrive with release at cluster scope took 1570 cycles here, this takes 140.
+constexpr uint32_t kSignalBytes = 16;
+__device__ __forceinline__ void signal_leader(uint32_t addr, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          mapa_shared(addr, 0)),
+      "r"(addr), "r"(kSignalBytes), "r"(mapa_shared(bar, 0))
+      : "memory");
+}
+
 // Turns kParts windows of 128 rows of 16 scale bytes into four 512-byte blocks each, in place (one warp).
 template <int kParts>
 __device__ __forceinline__ void turn_scales(uint32_t addr, int lane) {
@@ -266,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   auto full_bar = [&](uint32_t s) { return sbase + S::OFF_FULL + 8 * s; };
   auto empty_bar = [&](uint32_t s) { return sbase + S::OFF_EMPTY + 8 * s; };
   auto sfull_bar = [&](uint32_t s) { return sbase + S::OFF_SFULL + 8 * s; };
-  auto turned_bar = [&](uint32_t s) { return sbase + S::OFF_TURNED + 8 * s; };
   auto accf_bar = [&](uint32_t b) { return sbase + S::OFF_ACCF + 8 * b; };
   auto acce_bar = [&](uint32_t b) { return sbase + S::OFF_ACCE + 8 * b; };
   const uint32_t done_bar = sbase + S::OFF_DONE;
@@ -274,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full_bar(s), 1);             // the (leader's) expect_tx; bytes from both CTAs of a pair
+      mbar_init(full_bar(s), 2);             // the (leader's) copies armed, its scales turned; bytes of both CTAs
       mbar_init(empty_bar(s), 1);            // the MMA's commit, to both CTAs of a pair
       mbar_init(sfull_bar(s), 1);            // this CTA's expect_tx
-      mbar_init(turned_bar(s), S::kCtas);    // a turning warp of each CTA
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);             // the MMA's commit, to both CTAs of a pair
@@ -314,22 +325,37 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   const int32_t k_blocks = (p.k + BK - 1) / BK;
   const int32_t windows = (p.k + (kNv ? 255 : 511)) / (kNv ? 256 : 512);
   const int32_t total = t_tiles * n_tiles;
+  // This CTA's (pair's) items: w = pair, pair + npairs, ...
+  const int32_t items = pair < total ? (total - 1 - pair) / npairs + 1 : 0;
   // Group by group, blocks of 16 chunks meeting the n tiles in turn: each weight tile comes from
   // memory once for the block, whose rows stay in L2.  A group's units of rows are spread evenly
   // over its chunks, so that no tile is left with a few.
-  auto lane_tile = [&](int32_t w) {
-    GemmTile t = decode_gemm_tile(w, t_tiles, n_tiles, -16, tiles, offs, go, p.num_local_groups, S::kChunk);
-    const int32_t start = offs[go + t.local_group];
-    const int32_t chunks = tiles[t.local_group + 1] - tiles[t.local_group];
-    const int32_t i = (t.row0 - start) / S::kChunk;
-    const int32_t units = (t.row_end - start + S::kUnit - 1) / S::kUnit;
-    t.row0 = start + int32_t(int64_t(i) * units / chunks) * S::kUnit;
-    t.row_end = min(t.row_end, start + int32_t(int64_t(i + 1) * units / chunks) * S::kUnit);
+  auto lane_tile = [&](int32_t item) {
+    constexpr int32_t kBlock = 16;
+    const int32_t w = pair + item * npairs;
+    GemmTile t;
+    t.local_group = find_group(tiles, p.num_local_groups, w / n_tiles);
+    const int32_t g0 = tiles[t.local_group], chunks = tiles[t.local_group + 1] - g0;
+    const int32_t r = w - g0 * n_tiles;                            // item within the group
+    const int32_t b0 = r / (kBlock * n_tiles) * kBlock;            // first chunk of its block
+    const int32_t width = min(kBlock, chunks - b0), rb = r - b0 * n_tiles;
+    t.n_tile = rb / width;
+    const int32_t i = b0 + rb - t.n_tile * width;                  // chunk of the group
+    const int32_t start = offs[go + t.local_group], end = offs[go + t.local_group + 1];
+    const int32_t units = (end - start + S::kUnit - 1) / S::kUnit, base = units / chunks, more = units - base * chunks;
+    t.row0 = start + (i * base + min(i, more)) * S::kUnit;
+    t.row_end = min(end, t.row0 + (base + (i < more ? 1 : 0)) * S::kUnit);
     return t;
   };
-  auto tile_of = [&](int32_t w) {  // a whole warp's
-    const GemmTile t = lane_tile(w);
-    return GemmTile{uniform(t.local_group), uniform(t.row0), uniform(t.row_end), uniform(t.n_tile)};
+  // The tile of an item, for a whole warp that asks for one item after the other: every 32 items
+  // each lane works out one of them, which takes the divisions and the search out of each tile's
+  // way (some 100 cycles for every stage of 16).
+  GemmTile mine{};
+  auto tile_of = [&](int32_t item) {
+    const int at = item & 31;
+    if (at == 0 && item + lane < items) mine = lane_tile(item + lane);
+    return GemmTile{__shfl_sync(0xffffffffu, mine.local_group, at), __shfl_sync(0xffffffffu, mine.row0, at),
+                    __shfl_sync(0xffffffffu, mine.row_end, at), __shfl_sync(0xffffffffu, mine.n_tile, at)};
   };
   auto chunk_n = [](const GemmTile& t) { return (t.row_end - t.row0 + S::kUnit - 1) / S::kUnit * S::kUnit; };
   // bytes of one CTA's copies of codes in a stage of tile t
@@ -341,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     const uint32_t full0 = kPair ? mapa_shared(full_bar(0), 0) : full_bar(0);
-    for (int32_t w = pair; w < total && ok; w += npairs) {
-      const GemmTile t = tile_of(w);
+    for (int32_t item = 0; item < items && ok; ++item) {
+      const GemmTile t = tile_of(item);
       const int32_t rows = chunk_n(t) / S::kCtas;  // of the chunk that this CTA holds
       const int32_t trow = t.row0 + int32_t(rank) * rows;
       const int32_t wrow = t.n_tile * S::kTileW + int32_t(rank) * BW;
@@ -393,15 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     if (leader) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (int32_t w = pair; w < total && ok; w += npairs) {
-        const GemmTile t = tile_of(w);
+      for (int32_t item = 0; item < items && ok; ++item) {
+        const GemmTile t = tile_of(item);
         const int32_t ncols = chunk_n(t);
         if (!wait_warp_cluster(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.err)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * S::kChunk;
         for (int32_t kb = 0; kb < k_blocks; ++kb) {
-          if (!wait_warp_cluster(turned_bar(stage), phase, abort_flag, p.err) ||
-              !wait_warp(full_bar(stage), phase, abort_flag, p.err)) {
+          if (!wait_warp_cluster(full_bar(stage), phase, abort_flag, p.err)) {
             ok = false;
             break;
           }
@@ -454,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     // ---------------------------------------------------------------- copies of scales (both CTAs)
     uint32_t stage = 0, phase = 0, mine = 0;
     bool ok = true;
-    for (int32_t w = pair; w < total && ok; w += npairs) {
-      const GemmTile t = tile_of(w);
+    for (int32_t item = 0; item < items && ok; ++item) {
+      const GemmTile t = tile_of(item);
       const int32_t wrow = t.n_tile * S::kTileW + int32_t(rank) * BW;
       const int32_t wrows = max(0, min(BW, p.n - wrow));
       const uint32_t a_bytes = uint32_t(wrows) * 16u, b_bytes = uint32_t(t.row_end - t.row0) * 16u;
@@ -487,8 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     }
   } else if (warp > 10) {
     // ---------------------------------------------------------------- scales into the MMA's order (both CTAs)
-    const int64_t stages = pair < total ? int64_t((total - 1 - pair) / npairs + 1) * k_blocks : 0;
-    const uint32_t turned0 = kPair ? mapa_shared(turned_bar(0), 0) : turned_bar(0);
+    const int64_t stages = int64_t(items) * k_blocks;
     // A warp has stages of its own: a parity wait tells a phase from the one before it only, so
     // whoever waits on a barrier has to have seen each of its phases.
     uint32_t phase = 0;
@@ -503,10 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (kPair)
-            mbar_arrive_cluster(turned0 + 8 * stage);
+          if constexpr (!kPair)
+            mbar_arrive(full_bar(stage));
+          else if (leader)
+            mbar_arrive_expect_tx(full_bar(stage), kSignalBytes);
           else
-            mbar_arrive(turned0 + 8 * stage);
+            signal_leader(sbase + S::OFF_SIGNAL, full_bar(stage));
         }
       }
     }
@@ -517,25 +543,38 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     const uint32_t buf = sbase + S::OFF_OUT + uint32_t(warp - 2) * OUT_BYTES;
     const uint32_t acce0 = kPair ? mapa_shared(acce_bar(0), 0) : acce_bar(0);
     uint32_t acc = 0, acc_phase = 0;
-    for (int32_t w = pair; w < total; w += npairs) {
-      const GemmTile t = tile_of(w);
-      const int32_t rows = t.row_end - t.row0, ncols = chunk_n(t);
-      const int32_t col0 = t.n_tile * S::kTileW + int32_t(rank) * BW + quarter * 32;
+    constexpr int kBlocks = (S::kChunk / 32 + 1) / 2;  // of 32 rows, for each set
+    // What a tile's outputs are scaled by, loaded a tile ahead.  bf16: this thread's weight rows are
+    // lane / 4 + 8 i; f32: weight row lane (i = 0).  Row scales: block i's row `lane`.
+    struct Scales {
+      float ws[4], bias[4], rs[kBlocks];
+    } next;
+    auto col_of = [&](const GemmTile& t) { return t.n_tile * S::kTileW + int32_t(rank) * BW + quarter * 32; };
+    auto load_scales = [&](const GemmTile& t, Scales& s) {
       const int64_t w0 = int64_t(t.local_group) * p.n;
-      // bf16: this thread's weight rows are lane / 4 + 8 i; f32: weight row lane (i = 0)
-      float ws[4], bias[4];
 #pragma unroll
       for (int i = 0; i < (kOutF32 ? 1 : 4); ++i) {
-        const int32_t c = col0 + (kOutF32 ? lane : lane / 4 + 8 * i);
-        ws[i] = c < p.n && p.rhs_row_scale != nullptr ? __ldg(p.rhs_row_scale + w0 + c) : 1.f;
-        bias[i] = c < p.n && p.bias != nullptr ? load_bias(p, w0 + c) : 0.f;
+        const int32_t c = col_of(t) + (kOutF32 ? lane : lane / 4 + 8 * i);
+        s.ws[i] = c < p.n && p.rhs_row_scale != nullptr ? __ldg(p.rhs_row_scale + w0 + c) : 1.f;
+        s.bias[i] = c < p.n && p.bias != nullptr ? load_bias(p, w0 + c) : 0.f;
       }
-      constexpr int kBlocks = (S::kChunk / 32 + 1) / 2;  // of 32 rows, for each set
-      float rs[kBlocks];
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
-        const int32_t r = 32 * (2 * i + set) + lane;
-        rs[i] = p.lhs_row_scale != nullptr && r < rows ? __ldg(p.lhs_row_scale + t.row0 + r) : 1.f;
+        const int32_t r = t.row0 + 32 * (2 * i + set) + lane;
+        s.rs[i] = p.lhs_row_scale != nullptr && r < t.row_end ? __ldg(p.lhs_row_scale + r) : 1.f;
+      }
+    };
+    GemmTile t{};
+    if (items > 0) {
+      t = tile_of(0);
+      load_scales(t, next);
+    }
+    for (int32_t item = 0; item < items; ++item) {
+      const int32_t rows = t.row_end - t.row0, ncols = chunk_n(t), col0 = col_of(t), row0 = t.row0;
+      const Scales now = next;
+      if (item + 1 < items) {
+        t = tile_of(item + 1);
+        load_scales(t, next);
       }
       if (!wait_warp(accf_bar(acc), acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
@@ -562,9 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             if (last) release();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float r = fmaf(__uint_as_float(v[i]) * __shfl_sync(0xffffffffu, rs[b], i), ws[0], bias[0]);
+              const float r = fmaf(__uint_as_float(v[i]) * __shfl_sync(0xffffffffu, now.rs[b], i), now.ws[0], now.bias[0]);
               if (col0 + lane < p.n && c0 + i < rows)
-                static_cast<float*>(p.out)[int64_t(t.row0 + c0 + i) * p.n + col0 + lane] = r;
+                static_cast<float*>(p.out)[int64_t(row0 + c0 + i) * p.n + col0 + lane] = r;
             }
           } else {
             uint32_t v[2][16];
@@ -579,22 +618,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
               float r[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                r[i] = __shfl_sync(0xffffffffu, rs[b], 8 * (g + i / 2) + 2 * (lane & 3) + (i & 1));
+                r[i] = __shfl_sync(0xffffffffu, now.rs[b], 8 * (g + i / 2) + 2 * (lane & 3) + (i & 1));
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 uint32_t m[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {  // matrix q: rows 8 (g + q / 2) .. and columns 16 h + 8 (q & 1) ..
                   const int i = 4 * (g + q / 2) + 2 * (q & 1), f = 2 * h + (q & 1);
-                  m[q] = pack_bf16x2(fmaf(__uint_as_float(v[h][i]) * r[q & 2], ws[f], bias[f]),
-                                     fmaf(__uint_as_float(v[h][i + 1]) * r[(q & 2) + 1], ws[f], bias[f]));
+                  m[q] = pack_bf16x2(fmaf(__uint_as_float(v[h][i]) * r[q & 2], now.ws[f], now.bias[f]),
+                                     fmaf(__uint_as_float(v[h][i + 1]) * r[(q & 2) + 1], now.ws[f], now.bias[f]));
                 }
                 stmatrix_trans(at + uint32_t(8 * g) * OUT_PITCH + uint32_t(h) * 32u, m[0], m[1], m[2], m[3]);
               }
             }
             __syncwarp();
             const int32_t c = col0 + 8 * (lane & 3);
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + c0) * p.n + c;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + int64_t(row0 + c0) * p.n + c;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int32_t r = 8 * q + (lane >> 2);
@@ -628,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   if constexpr (kPair) {
     if (leader && warp == 0 && lane == 0 && *abort_flag) {
       st_shared_cluster_u32(mapa_shared(sbase + S::OFF_ABORT, 1), 1u);  // the follower's waits end too
-      // stage i of the sequence belongs to the pair's (i / k_blocks)-th work item
+      // stage i of the sequence belongs to the pair's (i / k_blocks)-th item
       pair_drain<kStages>(full_bar(0), sbase + S::OFF_REPORT, sbase + S::OFF_RWORD, issued, kWaitLimitCycles,
                           [&](uint32_t i) {
-                            return code_bytes(lane_tile(pair + int32_t(i / uint32_t(k_blocks)) * npairs));
+                            return code_bytes(lane_tile(int32_t(i / uint32_t(k_blocks))));
                           });
     }
     cluster_sync();  // the leader's MMAs and every copy are done; no signal targets either CTA any more
