@@ -17,8 +17,9 @@
 //          and 32 of row scales take 496 of the 512 columns of tensor memory;
 //          256 rows would leave one accumulator, and every tile would wait for
 //          the epilogue of the one before.
-//   single 128 weight rows on one SM by up to 64 rows: for groups of a few rows,
-//          where the time is the reading of the weights and stages are small.
+//   single 128 weight rows on one SM by up to 32 rows: for groups of a few rows,
+//          where the time is the reading of the weights and what counts is how much
+//          of them is on its way (64 rows and a stage less: 66.2 us against 64.2).
 //
 // Scales reach tensor memory as the MMA wants them: for every 128 rows and 4
 // bytes of scales (64 k of NVFP4, 128 k of MXFP4) lane l of 32 holds the 4 bytes
@@ -70,23 +71,26 @@ template <bool kPair>
 struct Shape {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kTileW = kCtas * BW;          // weight rows a tile
-  static constexpr int kChunk = kPair ? 224 : 64;    // most rows of a group a tile
+  static constexpr int kChunk = kPair ? 224 : 32;    // most rows of a group a tile
   static constexpr int kUnit = kPair ? 32 : 16;      // rows a chunk is a multiple of
   static constexpr int kRows = kChunk / kCtas;       // of them in a CTA's shared memory
   static constexpr int kParts = kPair ? 3 : 2;       // 128-row windows of scales: weights, rows
-  static constexpr int kStages = kPair ? 5 : 7;
+  static constexpr int kStages = kPair ? 5 : 8;   // of codes
+  static constexpr int kScales = kPair ? 7 : 8;   // of scales
   static constexpr uint32_t B_BYTES = kRows * ROW_BYTES;
   static constexpr uint32_t TM_SFA = 2 * kChunk, TM_SFB = TM_SFA + 16;
   static constexpr uint32_t kColumns = kPair ? 512 : 256;  // TM_SFB + 4 * 8 (4 * 4) columns, to a power of two
   static constexpr uint32_t OFF_A = 0;
   static constexpr uint32_t OFF_B = OFF_A + kStages * A_BYTES;
   static constexpr uint32_t OFF_SF = OFF_B + kStages * B_BYTES;
-  static constexpr uint32_t OFF_OUT = OFF_SF + kStages * kParts * SF_BYTES;
+  static constexpr uint32_t OFF_OUT = OFF_SF + kScales * kParts * SF_BYTES;
   static constexpr uint32_t OFF_CTRL = OFF_OUT + 8 * OUT_BYTES;
-  static constexpr uint32_t OFF_FULL = OFF_CTRL;                   // codes, scales turned (of both CTAs, the leader's)
+  static constexpr uint32_t OFF_FULL = OFF_CTRL;                   // codes (of both CTAs, the leader's)
   static constexpr uint32_t OFF_EMPTY = OFF_FULL + 8 * kStages;    // the MMA's commit
   static constexpr uint32_t OFF_SFULL = OFF_EMPTY + 8 * kStages;   // this CTA's scales
-  static constexpr uint32_t OFF_ACCF = OFF_SFULL + 8 * kStages;
+  static constexpr uint32_t OFF_TURNED = OFF_SFULL + 8 * kScales;  // scales turned (of both CTAs, the leader's)
+  static constexpr uint32_t OFF_SEMPTY = OFF_TURNED + 8 * kScales; // the MMA's commit
+  static constexpr uint32_t OFF_ACCF = OFF_SEMPTY + 8 * kScales;
   static constexpr uint32_t OFF_ACCE = OFF_ACCF + 16;
   static constexpr uint32_t OFF_DONE = OFF_ACCE + 16;
   static constexpr uint32_t OFF_REPORT = OFF_DONE + 8;  // pair_report's barrier and count (leader's)
@@ -140,6 +144,10 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                                   uint32_t* err) {
   return __all_sync(0xffffffffu, wait_bar_cluster(bar, parity, abort_flag, err));
+}
+
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Instruction descriptor of the block-scaled 4-bit kinds:
@@ -263,7 +271,7 @@ __device__ __forceinline__ float load_bias(const Params& p, int64_t i) {
 template <bool kPair, bool kNv, bool kOutF32>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_constant__ Maps maps, const Params p) {
   using S = Shape<kPair>;
-  constexpr int kStages = S::kStages;
+  constexpr int kStages = S::kStages, kScales = S::kScales;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -279,6 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   auto full_bar = [&](uint32_t s) { return sbase + S::OFF_FULL + 8 * s; };
   auto empty_bar = [&](uint32_t s) { return sbase + S::OFF_EMPTY + 8 * s; };
   auto sfull_bar = [&](uint32_t s) { return sbase + S::OFF_SFULL + 8 * s; };
+  auto turned_bar = [&](uint32_t s) { return sbase + S::OFF_TURNED + 8 * s; };
+  auto sempty_bar = [&](uint32_t s) { return sbase + S::OFF_SEMPTY + 8 * s; };
   auto accf_bar = [&](uint32_t b) { return sbase + S::OFF_ACCF + 8 * b; };
   auto acce_bar = [&](uint32_t b) { return sbase + S::OFF_ACCE + 8 * b; };
   const uint32_t done_bar = sbase + S::OFF_DONE;
@@ -286,9 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full_bar(s), 2);             // the (leader's) copies armed, its scales turned; bytes of both CTAs
+      mbar_init(full_bar(s), 1);             // the (leader's) expect_tx; bytes of both CTAs of a pair
       mbar_init(empty_bar(s), 1);            // the MMA's commit, to both CTAs of a pair
+    }
+    for (int s = 0; s < kScales; ++s) {
       mbar_init(sfull_bar(s), 1);            // this CTA's expect_tx
+      mbar_init(turned_bar(s), 1);           // the leader's turning warp; in a pair the follower's signal
+      mbar_init(sempty_bar(s), 1);           // the MMA's commit, to both CTAs of a pair
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);             // the MMA's commit, to both CTAs of a pair
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (leader) {
-      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int32_t item = 0; item < items && ok; ++item) {
         const GemmTile t = tile_of(item);
@@ -426,7 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * S::kChunk;
         for (int32_t kb = 0; kb < k_blocks; ++kb) {
-          if (!wait_warp_cluster(full_bar(stage), phase, abort_flag, p.err)) {
+          // both are asked at once: one latency where both have come
+          const uint32_t turned = mbar_try_wait_cluster(turned_bar(slot), slot_phase);
+          const uint32_t full = mbar_try_wait(full_bar(stage), phase);
+          if (!__all_sync(0xffffffffu, turned & full) &&
+              (!wait_warp_cluster(turned_bar(slot), slot_phase, abort_flag, p.err) ||
+               !wait_warp(full_bar(stage), phase, abort_flag, p.err))) {
             ok = false;
             break;
           }
@@ -434,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
           if (elected()) {
             // a stage uses 4 blocks of a window (NVFP4) or half of them (MXFP4)
             const uint32_t sf =
-                sbase + S::OFF_SF + stage * S::kParts * SF_BYTES + (kNv ? 0u : 1024u * uint32_t(kb & 1));
+                sbase + S::OFF_SF + slot * S::kParts * SF_BYTES + (kNv ? 0u : 1024u * uint32_t(kb & 1));
 #pragma unroll
             for (uint32_t j = 0; j < (kNv ? 4 : 2); ++j) {
               copy_scales<kPair>(tmem_base + S::TM_SFA + 4 * j, sf + 512u * j);
@@ -453,12 +472,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
                                   (uint32_t(kb) | kk) != 0 ? 1u : 0u);
             }
             commit<kPair>(empty_bar(stage));
+            commit<kPair>(sempty_bar(slot));
             if (kb == k_blocks - 1) commit<kPair>(accf_bar(acc));
           }
           __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
+          }
+          if (++slot == kScales) {
+            slot = 0;
+            slot_phase ^= 1u;
           }
         }
         if (++acc == 2) {
@@ -487,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       const uint8_t* a_src = p.rhs_scale + (int64_t(t.local_group) * windows * p.n + wrow) * 16;
       const uint8_t* b_src = p.lhs_scale + int64_t(t.row0) * 16;
       for (int32_t kb = 0; kb < k_blocks; ++kb) {
-        if (!wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+        if (!wait_warp(sempty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
@@ -500,15 +524,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         }
         __syncwarp();
         ++mine;
-        if (++stage == kStages) {
+        if (++stage == kScales) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
     if (!ok) {
-      for (uint32_t i = mine > kStages ? mine - kStages : 0u; i < mine; ++i)
-        drain_bar(sfull_bar(i % kStages), (i / kStages) & 1u);
+      for (uint32_t i = mine > kScales ? mine - kScales : 0u; i < mine; ++i)
+        drain_bar(sfull_bar(i % kScales), (i / kScales) & 1u);
     }
   } else if (warp > 10) {
     // ---------------------------------------------------------------- scales into the MMA's order (both CTAs)
@@ -517,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     // whoever waits on a barrier has to have seen each of its phases.
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t i0 = 0; i0 < stages && ok; i0 += kStages, phase ^= 1u) {
-      for (int32_t stage = warp - 11; stage < kStages && i0 + stage < stages; stage += kTurners) {
+    for (int64_t i0 = 0; i0 < stages && ok; i0 += kScales, phase ^= 1u) {
+      for (int32_t stage = warp - 11; stage < kScales && i0 + stage < stages; stage += kTurners) {
         if (!wait_warp(sfull_bar(stage), phase, abort_flag, p.err)) {
           ok = false;
           break;
@@ -528,11 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) {
           if constexpr (!kPair)
-            mbar_arrive(full_bar(stage));
+            mbar_arrive(turned_bar(stage));
           else if (leader)
-            mbar_arrive_expect_tx(full_bar(stage), kSignalBytes);
+            mbar_arrive_expect_tx(turned_bar(stage), kSignalBytes);
           else
-            signal_leader(sbase + S::OFF_SIGNAL, full_bar(stage));
+            signal_leader(sbase + S::OFF_SIGNAL, turned_bar(stage));
         }
       }
     }
@@ -579,12 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       if (!wait_warp(accf_bar(acc), acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + acc * S::kChunk;
+      // The accumulator may be overwritten: this warp's loads of it have completed (wait::ld), and
+      // nothing else is handed over, so the arrive orders no memory.  (With release at cluster scope it
+      // waits for the warp's stores to `out`, some 1500 cycles a tile.)
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if constexpr (kPair)
-            mbar_arrive_cluster(acce0 + 8 * acc);
+            mbar_arrive_relaxed_cluster(acce0 + 8 * acc);
           else
             mbar_arrive(acce0 + 8 * acc);
         }
@@ -743,7 +770,7 @@ extern "C" int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const
       num_local_groups > num_total_groups)
     return GMM_ERR_SHAPE;
   if (group_offset < 0 || group_offset > num_total_groups - num_local_groups) return GMM_ERR_GROUP_OFFSET;
-  if (((m + 63) / 64 + num_local_groups) * ((n + BW - 1) / BW) > INT32_MAX) return GMM_ERR_SHAPE;
+  if (((m + 31) / 32 + num_local_groups) * ((n + BW - 1) / BW) > INT32_MAX) return GMM_ERR_SHAPE;
   if (!aligned(lhs_codes, 16) || !aligned(lhs_block_scale, 16) || !aligned(rhs_codes, 16) ||
       !aligned(rhs_block_scale, 16) || !aligned(out, 16) || !aligned(lhs_row_scale, 4) || !aligned(rhs_row_scale, 4) ||
       !aligned(rhs_bias, bias_dtype == GMM_DTYPE_F32 ? 4 : 2) || !aligned(group_sizes, 4))
