@@ -15,12 +15,13 @@ Like the rest of the package this only marshals arguments; gradients are calls o
 from __future__ import annotations
 
 import ctypes
+import sys
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_I, _I32, _I64, _P, _SZ, _TORCH_TO_CODE, DTYPE_BF16, DTYPE_F32, SIGNATURES, _check, _dev, _stream,
-               load_library, workspace_for)
+from . import (_I, _I32, _I64, _P, _SZ, DTYPE_BF16, DTYPE_F32, SIGNATURES, GmmError, _dev, load_library,
+               workspace_for)
 
 __all__ = ["route", "route_backward", "ExpertOrder", "sort_by_expert", "dispatch", "dispatch_backward", "combine",
            "combine_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gmm_fp4", "MAX_TOPK"]
@@ -30,6 +31,7 @@ FP4_FORMATS = {"nvfp4": 0, "mxfp4": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 MAX_TOPK = 32
 
+_package = sys.modules[__package__]
 _F = ctypes.c_float
 SIGNATURES.update({
     "gmm_route": ([_P, _I, _I64, _I32, _I64, _I32, _I, _I, _F, _P, _P, _P, _P, _P], _I),
@@ -64,6 +66,25 @@ class Fp4Tensor(NamedTuple):
     format: str
 
 
+# These calls are a few microseconds of GPU work at decoding sizes, so the checks below cost as
+# little as they can: one test that holds for good arguments, and the reason only where it fails.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(device, stream):
+    """The CUDA stream handle of `stream`, or of the device's current stream."""
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+
+def _run(fn, status):
+    if status:
+        raise GmmError(fn, status)
+
+
+def _lib():
+    return _package._lib or load_library()
+
+
 def _rows(t, name):
     """A 2-D CUDA tensor whose rows are dense; returns its row pitch."""
     if not t.is_cuda:
@@ -71,29 +92,33 @@ def _rows(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     n, d = t.shape
-    if d > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if step != 1 and d > 1:
         raise ValueError(f"{name} must have dense rows")
     if n <= 1:
         return d
-    if t.stride(0) < d:
+    if pitch < d:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
+    return pitch
+
+
+_FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
 def _float_code(t, name):
-    code = _TORCH_TO_CODE.get(t.dtype)
-    if code != DTYPE_BF16 and code != DTYPE_F32:
+    code = _FLOATS.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32")
     return code
 
 
 def _want(t, name, dtype, shape):
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     _dev(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _ptr(t):
@@ -127,9 +152,9 @@ def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bia
         _want(token_mask, "token_mask", torch.uint8 if token_mask.dtype == torch.uint8 else torch.bool, (tokens,))
     weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
     chosen = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
-    _check("gmm_route", load_library().gmm_route(
+    _run("gmm_route", _lib().gmm_route(
         logits.data_ptr(), code, tokens, experts, ld, topk, _score(score), int(bool(renormalize)), float(scale),
-        _ptr(select_bias), _ptr(token_mask), weights.data_ptr(), chosen.data_ptr(), _stream(logits.device, stream)))
+        _ptr(select_bias), _ptr(token_mask), weights.data_ptr(), chosen.data_ptr(), _on(logits.device, stream)))
     return weights, chosen
 
 
@@ -145,9 +170,9 @@ def route_backward(dweights, experts, logits, score="softmax", renormalize=True,
     _want(experts, "experts", torch.int32, (tokens, topk))
     _want(dweights, "dweights", torch.float32, (tokens, topk))
     dlogits = torch.empty((tokens, n), dtype=logits.dtype, device=logits.device)
-    _check("gmm_route_backward", load_library().gmm_route_backward(
+    _run("gmm_route_backward", _lib().gmm_route_backward(
         dweights.data_ptr(), experts.data_ptr(), logits.data_ptr(), code, tokens, n, ld, topk, _score(score),
-        int(bool(renormalize)), float(scale), dlogits.data_ptr(), _stream(logits.device, stream)))
+        int(bool(renormalize)), float(scale), dlogits.data_ptr(), _on(logits.device, stream)))
     return dlogits
 
 
@@ -161,9 +186,9 @@ def sort_by_expert(experts, num_experts, stream=None):
     sizes = torch.empty((int(num_experts),), dtype=torch.int32, device=experts.device)
     rows = torch.empty((tokens, topk), dtype=torch.int32, device=experts.device)
     source = torch.empty((tokens * topk,), dtype=torch.int32, device=experts.device)
-    _check("gmm_sort_by_expert", load_library().gmm_sort_by_expert(
+    _run("gmm_sort_by_expert", _lib().gmm_sort_by_expert(
         experts.data_ptr(), tokens, topk, int(num_experts), sizes.data_ptr(), rows.data_ptr(), source.data_ptr(),
-        _stream(experts.device, stream)))
+        _on(experts.device, stream)))
     return ExpertOrder(sizes, rows, source)
 
 
@@ -185,9 +210,9 @@ def dispatch(x, order, stream=None):
     if x.shape[0] != tokens:
         raise ValueError(f"x must have {tokens} rows")
     out = torch.empty((tokens * topk, x.shape[1]), dtype=x.dtype, device=x.device)
-    _check("gmm_dispatch", load_library().gmm_dispatch(
+    _run("gmm_dispatch", _lib().gmm_dispatch(
         x.data_ptr(), code, tokens, x.shape[1], ld, topk, order.rows.data_ptr(), order.source.data_ptr(),
-        out.data_ptr(), _stream(x.device, stream)))
+        out.data_ptr(), _on(x.device, stream)))
     return out
 
 
@@ -201,9 +226,9 @@ def combine(rows, order, weights=None, stream=None):
     if weights is not None:
         _want(weights, "weights", torch.float32, (tokens, topk))
     out = torch.empty((tokens, rows.shape[1]), dtype=rows.dtype, device=rows.device)
-    _check("gmm_combine", load_library().gmm_combine(
+    _run("gmm_combine", _lib().gmm_combine(
         rows.data_ptr(), code, tokens, rows.shape[1], topk, order.rows.data_ptr(), _ptr(weights), out.data_ptr(),
-        _stream(rows.device, stream)))
+        _on(rows.device, stream)))
     return out
 
 
@@ -223,10 +248,10 @@ def combine_backward(dout, rows, order, weights, stream=None):
     _want(weights, "weights", torch.float32, (tokens, topk))
     drows = torch.empty_like(rows)
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=rows.device)
-    _check("gmm_combine_backward", load_library().gmm_combine_backward(
+    _run("gmm_combine_backward", _lib().gmm_combine_backward(
         dout.data_ptr(), rows.data_ptr(), code, tokens, rows.shape[1], topk, order.rows.data_ptr(),
         order.source.data_ptr(), weights.data_ptr(), drows.data_ptr(), dweights.data_ptr(),
-        _stream(rows.device, stream)))
+        _on(rows.device, stream)))
     return drows, dweights
 
 
@@ -268,10 +293,10 @@ def quantize_fp4(x, format="nvfp4", order=None, stream=None):
     row = torch.empty(lead + (out_rows,), dtype=torch.float32, device=x.device) if format == "nvfp4" else None
     if batch == 0:
         return Fp4Tensor(codes, scale, row, format)
-    _check("gmm_quantize_fp4", load_library().gmm_quantize_fp4(
+    _run("gmm_quantize_fp4", _lib().gmm_quantize_fp4(
         x.data_ptr(), code, batch, rows, k, ld, fmt, None if order is None else order.rows.data_ptr(),
         None if order is None else order.source.data_ptr(), topk, codes.data_ptr(), scale.data_ptr(), _ptr(row),
-        _stream(x.device, stream)))
+        _on(x.device, stream)))
     return Fp4Tensor(codes, scale, row, format)
 
 
@@ -303,9 +328,9 @@ def dequantize_fp4(q, out_dtype=torch.bfloat16, stream=None):
     out = torch.empty(tuple(q.codes.shape[:-1]) + (k,), dtype=out_dtype, device=q.codes.device)
     if batch == 0:
         return out
-    _check("gmm_dequantize_fp4", load_library().gmm_dequantize_fp4(
+    _run("gmm_dequantize_fp4", _lib().gmm_dequantize_fp4(
         q.codes.data_ptr(), q.block_scale.data_ptr(), _ptr(q.row_scale), FP4_FORMATS[q.format], batch, rows, k,
-        out.data_ptr(), _float_code(out, "out_dtype"), _stream(out.device, stream)))
+        out.data_ptr(), _float_code(out, "out_dtype"), _on(out.device, stream)))
     return out
 
 
@@ -337,9 +362,9 @@ def gmm_fp4(lhs, rhs, group_sizes, rhs_bias=None, group_offset=0, out=None, out_
     if tuple(out.shape) != (m, n):
         raise ValueError(f"out must be [{m}, {n}], got {list(out.shape)}")
     ws = workspace if workspace is not None else workspace_for(device, stream)
-    _check("gmm_fp4", load_library().gmm_fp4(
+    _run("gmm_fp4", _lib().gmm_fp4(
         lhs.codes.data_ptr(), lhs.block_scale.data_ptr(), _ptr(lhs.row_scale), m, k, rhs.codes.data_ptr(),
         rhs.block_scale.data_ptr(), _ptr(rhs.row_scale), FP4_FORMATS[lhs.format], local, n, group_sizes.data_ptr(),
         group_sizes.shape[0], int(group_offset), _ptr(rhs_bias), bias_code, out.data_ptr(),
-        _float_code(out, "out"), ws.data_ptr(), ws.numel(), _stream(device, stream)))
+        _float_code(out, "out"), ws.data_ptr(), ws.numel(), _on(device, stream)))
     return out
