@@ -38,11 +38,10 @@ __device__ __forceinline__ int32_t slot_row(const int32_t* rows, int64_t slot, i
 // expert, equal experts within a step of 32 in lane order.  So the order is
 // stable and no result hangs on the order of an atomic.  Dropped slots count as
 // one more expert after the last.
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
-// Up to this many slots one CTA alone is used: 4 steps a warp.
-constexpr int64_t kSortOneCta = 4 * kSortThreads;
+//
+// Bound by latency, not by its 12 bytes a slot: so few barriers, the counts of
+// all warps read at once before they are summed, and up to 16 CTAs.
+constexpr int kSortCluster = 16;
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -50,31 +49,44 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSortThreads)
+// kWarps a CTA; `run` slots a warp, a multiple of 32.
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps)
     sort_kernel(const int32_t* __restrict__ experts, int32_t slots, int32_t num_experts, int32_t run,
                 int32_t* __restrict__ group_sizes, int32_t* __restrict__ rows, int32_t* __restrict__ source,
                 int32_t ctas) {
-  extern __shared__ uint32_t table[];  // [kSortWarps][bins], then [bins] of the CTA's sums
-  __shared__ uint32_t warp_sums[32];
+  constexpr int kThreads = 32 * kWarps;
+  extern __shared__ uint32_t table[];  // [kWarps][bins], then the CTA's sums [bins] and first places [bins]
+  __shared__ uint32_t warp_sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bins = num_experts + 1;
   uint32_t* mine = table + warp * bins;
-  uint32_t* total = table + kSortWarps * bins;
+  uint32_t* total = table + kWarps * bins;
+  uint32_t* place = total + bins;
   const int32_t rank = ctas > 1 ? int32_t(cluster_ctarank()) : 0;
-  const int64_t first = int64_t(rank * kSortWarps + warp) * run;
+  const int64_t first = int64_t(rank * kWarps + warp) * run;
   const int32_t lo = int32_t(first < slots ? first : slots);
   const int32_t hi = int32_t(first + run < slots ? first + run : slots);
-  for (int i = tid; i < kSortWarps * bins; i += kSortThreads) table[i] = 0;
-  __syncthreads();
+  // the run's first four steps stay in registers
+  int32_t held[4];
   auto bin_of = [&](int32_t e) { return e >= 0 && e < num_experts ? e : num_experts; };
-  for (int32_t s = lo + lane; s < hi; s += 32) atomicAdd(mine + bin_of(__ldg(experts + s)), 1u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) held[i] = lo + 32 * i + lane < hi ? bin_of(__ldg(experts + lo + 32 * i + lane)) : -1;
+  for (int b = lane; b < bins; b += 32) mine[b] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (held[i] >= 0) atomicAdd(mine + held[i], 1u);
+  for (int32_t s = lo + 128 + lane; s < hi; s += 32) atomicAdd(mine + bin_of(__ldg(experts + s)), 1u);
   __syncthreads();
-  for (int b = tid; b < bins; b += kSortThreads) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = table[w * bins + b];
+  for (int b = tid; b < bins; b += kThreads) {
+    uint32_t c[kWarps], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) c[w] = table[w * bins + b];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
       table[w * bins + b] = sum;
-      sum += c;
+      sum += c[w];
     }
     total[b] = sum;
   }
@@ -82,21 +94,33 @@ __global__ void __launch_bounds__(kSortThreads)
     cluster_sync();
   else
     __syncthreads();
-  // each expert's rows over all CTAs, and those of the CTAs before this one
-  uint32_t all = 0, before = 0;
-  if (tid < num_experts) {
-    if (ctas > 1) {
-      for (int r = 0; r < ctas; ++r) {
-        const uint32_t c = ld_cluster_u32(mapa_shared(smem_u32(total + tid), uint32_t(r)));
-        all += c;
-        before += r < rank ? c : 0u;
+  // Each expert's rows over all CTAs, those of the CTAs before this one, and the experts before: the
+  // threads take kPer consecutive bins each.
+  constexpr int kPer = (GMM_MAX_GROUPS + 1 + kThreads - 1) / kThreads;
+  uint32_t all[kPer], before[kPer], sum = 0;
+  const int b0 = tid * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    all[i] = before[i] = 0;
+    if (b0 + i < bins) {
+      if (ctas > 1) {
+        uint32_t c[kSortCluster];
+#pragma unroll
+        for (int r = 0; r < kSortCluster; ++r)
+          c[r] = r < ctas ? ld_cluster_u32(mapa_shared(smem_u32(total + b0 + i), uint32_t(r))) : 0u;
+#pragma unroll
+        for (int r = 0; r < kSortCluster; ++r) {
+          all[i] += c[r];
+          before[i] += r < rank ? c[r] : 0u;
+        }
+      } else {
+        all[i] = total[b0 + i];
       }
-    } else {
-      all = total[tid];
+      if (rank == 0 && b0 + i < num_experts) group_sizes[b0 + i] = int32_t(all[i]);
     }
-    if (rank == 0) group_sizes[tid] = int32_t(all);
+    sum += all[i];
   }
-  uint32_t incl = all;
+  uint32_t incl = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
@@ -104,28 +128,19 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  uint32_t start = incl - all, end = 0;
-  for (int w = 0; w < kSortWarps; ++w) {
-    const uint32_t s = warp_sums[w];
-    if (w < warp) start += s;
-    end += s;
-  }
-  if (tid < num_experts)
-    for (int w = 0; w < kSortWarps; ++w) table[w * bins + tid] += start + before;
-  if (tid == 0) {
-    uint32_t gone = 0;  // dropped slots of the CTAs before
-    if (ctas > 1)
-      for (int r = 0; r < rank; ++r) gone += ld_cluster_u32(mapa_shared(smem_u32(total + num_experts), uint32_t(r)));
-    for (int w = 0; w < kSortWarps; ++w) table[w * bins + num_experts] += end + gone;
+  uint32_t start = incl - sum;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) start += w < warp ? warp_sums[w] : 0u;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (b0 + i < bins) place[b0 + i] = start + before[i];
+    start += all[i];
   }
   __syncthreads();
-  for (int32_t s0 = lo; s0 < hi; s0 += 32) {
-    const int32_t s = s0 + lane;
-    const int32_t b = s < hi ? bin_of(__ldg(experts + s)) : -1;
+  auto put = [&](int32_t s, int32_t b) {  // a step of 32 slots, b the bin of slot s or -1
     const uint32_t same = __match_any_sync(0xffffffffu, b);
     const int ahead = __popc(same & ((1u << lane) - 1u));
-    uint32_t at = 0;
-    if (b >= 0) at = mine[b] + uint32_t(ahead);
+    const uint32_t at = b >= 0 ? place[b] + mine[b] + uint32_t(ahead) : 0u;
     __syncwarp();
     if (b >= 0) {
       if (ahead == 0) mine[b] += uint32_t(__popc(same));
@@ -133,23 +148,29 @@ __global__ void __launch_bounds__(kSortThreads)
       source[at] = b < num_experts ? s : -1;
     }
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lo + 32 * i < hi) put(lo + 32 * i + lane, held[i]);
+  for (int32_t s0 = lo + 128; s0 < hi; s0 += 32)
+    put(s0 + lane, s0 + lane < hi ? bin_of(__ldg(experts + s0 + lane)) : -1);
   if (ctas > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
-cudaError_t launch_sort(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
-                        int32_t* rows, int32_t* source, cudaStream_t stream) {
-  const size_t smem = size_t(kSortWarps + 1) * (num_experts + 1) * sizeof(uint32_t);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
-  const int ctas = slots <= kSortOneCta ? 1 : kSortCluster;
-  const int64_t warps = int64_t(ctas) * kSortWarps;
+template <int kWarps>
+cudaError_t launch_sort_as(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
+                           int32_t* rows, int32_t* source, int ctas, cudaStream_t stream) {
+  const size_t smem = size_t(kWarps + 2) * (num_experts + 1) * sizeof(uint32_t);
+  auto kern = sort_kernel<kWarps>;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = int64_t(ctas) * kWarps;
   const int32_t run = int32_t(((slots + warps - 1) / warps + 31) / 32 * 32);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
@@ -158,8 +179,17 @@ cudaError_t launch_sort(const int32_t* experts, int32_t slots, int32_t num_exper
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, sort_kernel, experts, slots, num_experts, run, group_sizes, rows, source,
-                            int32_t(ctas));
+  return cudaLaunchKernelEx(&cfg, kern, experts, slots, num_experts, run, group_sizes, rows, source, int32_t(ctas));
+}
+
+// Up to 512 slots: one CTA of 8 warps; up to 4096 (four steps a warp): one CTA of 32; up to 32768
+// eight CTAs (portable), above that sixteen.
+cudaError_t launch_sort(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
+                        int32_t* rows, int32_t* source, cudaStream_t stream) {
+  if (slots <= 512)
+    return launch_sort_as<8>(experts, slots, num_experts, group_sizes, rows, source, 1, stream);
+  const int ctas = slots <= 4096 ? 1 : slots <= 32768 ? 8 : kSortCluster;
+  return launch_sort_as<32>(experts, slots, num_experts, group_sizes, rows, source, ctas, stream);
 }
 
 // ------------------------------------------------------------------ rows of any width
@@ -190,6 +220,12 @@ struct Unit {
 };
 
 constexpr int kThreads = 128;
+
+// Units a lane moves at a time: `bytes` of them whatever their width.
+template <class U>
+constexpr int units_of(int bytes) {
+  return int(sizeof(U)) > bytes ? 1 : bytes / int(sizeof(U));
+}
 
 template <class U>
 __device__ __forceinline__ U zero_unit() {
@@ -230,7 +266,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <class U, class T, int kPer>
+template <class U, class T, int kPer, int kBatch>
 __global__ void __launch_bounds__(kThreads)
     combine_kernel(const U* __restrict__ in, int64_t tokens, int64_t units, int32_t topk, int64_t parts,
                    const int32_t* __restrict__ rows, const float* __restrict__ weights, U* __restrict__ out) {
@@ -247,32 +283,40 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < kPer; ++i)
 #pragma unroll
     for (int n = 0; n < N; ++n) acc[i][n] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < topk; ++j) {
-    const int32_t from = __shfl_sync(0xffffffffu, r, j);
-    const float gj = __shfl_sync(0xffffffffu, g, j);
-    if (from >= 0) {
+  // kBatch rows are on their way before the first is used
+  for (int j0 = 0; j0 < topk; j0 += kBatch) {
+    U got[kBatch][kPer];
+    float gj[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int32_t from = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);  // -1 past the last slot
+      gj[q] = __shfl_sync(0xffffffffu, g, (j0 + q) & 31);
+      const bool there = j0 + q < topk && from >= 0;
+      gj[q] = there ? gj[q] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        got[q][i] = there && c0 + 32 * i < units ? __ldg(in + from * units + c0 + 32 * i) : zero_unit<U>();
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (c0 + 32 * i < units) {
-          float f[N];
-          Unit<U, T>::unpack(__ldg(in + from * units + c0 + 32 * i), f);
+        float f[N];
+        Unit<U, T>::unpack(got[q][i], f);
 #pragma unroll
-          for (int n = 0; n < N; ++n) acc[i][n] = fmaf(gj, f[n], acc[i][n]);
-        }
+        for (int n = 0; n < N; ++n) acc[i][n] = fmaf(gj[q], f[n], acc[i][n]);
       }
-    }
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (c0 + 32 * i < units) out[t * units + c0 + 32 * i] = Unit<U, T>::pack(acc[i]);
 }
 
-constexpr int kBackThreads = 256;
+constexpr int kBackThreads = 512;
 
 // One CTA for each token: its warps share the row's columns; their parts of the
 // dot products are summed in warp order.
-template <class U, class T, int kPer>
+template <class U, class T, int kPer, int kBatch>
 __global__ void __launch_bounds__(kBackThreads)
     combine_backward_kernel(const U* __restrict__ dout, const U* __restrict__ in, int64_t tokens, int64_t units,
                             int32_t topk,
@@ -287,48 +331,64 @@ __global__ void __launch_bounds__(kBackThreads)
   const float g = lane < topk ? __ldg(weights + t * topk + lane) : 0.f;
   part[warp][lane] = 0.f;
   __syncwarp();
-  for (int64_t base = 0; base < units; base += kBackThreads * kPer) {
+  const int threads = blockDim.x;
+  for (int64_t base = 0; base < units; base += threads * kPer) {
     const int64_t c0 = base + threadIdx.x;
     float d[kPer][N];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (c0 + kBackThreads * i < units) {
-        Unit<U, T>::unpack(__ldg(dout + t * units + c0 + kBackThreads * i), d[i]);
+      if (c0 + threads * i < units) {
+        Unit<U, T>::unpack(__ldg(dout + t * units + c0 + threads * i), d[i]);
       } else {
 #pragma unroll
         for (int n = 0; n < N; ++n) d[i][n] = 0.f;
       }
     }
-    for (int j = 0; j < topk; ++j) {
-      const int32_t row = __shfl_sync(0xffffffffu, r, j);
-      const float gj = __shfl_sync(0xffffffffu, g, j);
-      if (row >= 0) {
-        float sum = 0.f;
+    for (int j0 = 0; j0 < topk; j0 += kBatch) {
+      U got[kBatch][kPer];
+      int32_t row[kBatch];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (c0 + kBackThreads * i < units) {
-            float f[N], o[N];
-            Unit<U, T>::unpack(__ldg(in + row * units + c0 + kBackThreads * i), f);
-#pragma unroll
-            for (int n = 0; n < N; ++n) sum = fmaf(d[i][n], f[n], sum), o[n] = gj * d[i][n];
-            din[row * units + c0 + kBackThreads * i] = Unit<U, T>::pack(o);
-          }
-        }
-#pragma unroll
-        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        if (lane == 0) part[warp][j] += sum;
-      }
-      if (__shfl_sync(0xffffffffu, s, j) < 0) {
+      for (int q = 0; q < kBatch; ++q) {
+        const int32_t from = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
+        row[q] = j0 + q < topk ? from : -1;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (c0 + kBackThreads * i < units) din[(t * topk + j) * units + c0 + kBackThreads * i] = zero_unit<U>();
+          got[q][i] = row[q] >= 0 && c0 + threads * i < units ? __ldg(in + row[q] * units + c0 + threads * i)
+                                                              : zero_unit<U>();
+      }
+      float sum[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const float gj = __shfl_sync(0xffffffffu, g, (j0 + q) & 31);
+        const bool gone = __shfl_sync(0xffffffffu, s, (j0 + q) & 31) < 0 && j0 + q < topk;
+        sum[q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          float f[N], o[N];
+          Unit<U, T>::unpack(got[q][i], f);
+#pragma unroll
+          for (int n = 0; n < N; ++n) sum[q] = fmaf(d[i][n], f[n], sum[q]), o[n] = gj * d[i][n];
+          if (c0 + threads * i < units) {
+            if (row[q] >= 0) din[row[q] * units + c0 + threads * i] = Unit<U, T>::pack(o);
+            if (gone) din[(t * topk + j0 + q) * units + c0 + threads * i] = zero_unit<U>();
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1)
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], k);
+      if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+          if (row[q] >= 0) part[warp][j0 + q] += sum[q];
       }
     }
   }
   __syncthreads();
   if (int(threadIdx.x) < topk) {
     float sum = 0.f;
-    for (int w = 0; w < kBackThreads / 32; ++w) sum += part[w][threadIdx.x];
+    for (int w = 0; w < threads / 32; ++w) sum += part[w][threadIdx.x];
     dweights[t * topk + threadIdx.x] = sum;
   }
 }
@@ -370,10 +430,13 @@ cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, con
     } else {
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
       int64_t parts;
-      const unsigned grid = row_grid(tokens, units, 2, &parts);
+      constexpr int kPer = units_of<U>(32);
+      const unsigned grid = row_grid(tokens, units, kPer, &parts);
       if (grid == 0) return cudaErrorInvalidConfiguration;
-      combine_kernel<U, T, 2><<<grid, kThreads, 0, s>>>(static_cast<const U*>(in), tokens, units, topk, parts, rows,
-                                                       weights, static_cast<U*>(out));
+      // rows on their way at once, by how many a token has
+      auto kern = topk <= 2 ? combine_kernel<U, T, kPer, 2> : combine_kernel<U, T, kPer, 4>;
+      kern<<<grid, kThreads, 0, s>>>(static_cast<const U*>(in), tokens, units, topk, parts, rows, weights,
+                                     static_cast<U*>(out));
       return cudaGetLastError();
     }
   });
@@ -388,9 +451,17 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
     if constexpr (sizeof(U) < sizeof(T)) {
       return cudaErrorInvalidValue;
     } else {
-      combine_backward_kernel<U, T, 2><<<unsigned(tokens), kBackThreads, 0, s>>>(
-          static_cast<const U*>(dout), static_cast<const U*>(in), tokens, d * int64_t(sizeof(T)) / int64_t(sizeof(U)), topk,
-          rows, source, weights, static_cast<U*>(din), dweights);
+      const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
+      // 32 bytes a thread and 4 rows at once; 16 and 2 where units are narrow, whose many registers
+      // would leave few threads (3001 tokens, 5 rows of 1027 f32: 33 us, with 32 and 4 49 us;
+      // 8192 tokens, 2 rows of 4096 bf16: 59 us, with 16 and 2 66 us)
+      constexpr bool kWide = sizeof(U) == 16;
+      constexpr int kPer = units_of<U>(kWide ? 32 : 16);
+      const int64_t lanes = (units + kPer - 1) / kPer;
+      const int threads = lanes >= kBackThreads ? kBackThreads : int((lanes + 31) / 32 * 32);
+      auto kern = kWide && topk > 2 ? combine_backward_kernel<U, T, kPer, 4> : combine_backward_kernel<U, T, kPer, 2>;
+      kern<<<unsigned(tokens), threads, 0, s>>>(static_cast<const U*>(dout), static_cast<const U*>(in), tokens, units,
+                                                topk, rows, source, weights, static_cast<U*>(din), dweights);
       return cudaGetLastError();
     }
   });
@@ -428,9 +499,10 @@ extern "C" int gmm_dispatch(const void* x, int dtype, int64_t tokens, int64_t d,
     using U = decltype(unit);
     const int64_t units = d * int64_t(el) / int64_t(sizeof(U));
     int64_t parts;
-    const unsigned grid = row_grid(tokens, units, 4, &parts);
+    constexpr int kPer = units_of<U>(32);
+    const unsigned grid = row_grid(tokens, units, kPer, &parts);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    dispatch_kernel<U, 4><<<grid, kThreads, 0, s>>>(static_cast<const U*>(x), tokens, units,
+    dispatch_kernel<U, kPer><<<grid, kThreads, 0, s>>>(static_cast<const U*>(x), tokens, units,
                                                    x_ld * int64_t(el) / int64_t(sizeof(U)), topk, parts, rows, source,
                                                    static_cast<U*>(out));
     return cudaGetLastError();
