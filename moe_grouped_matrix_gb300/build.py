@@ -1,8 +1,10 @@
-"""Builds libgmm.so in-tree for sm_103a with nvcc (no cmake, no torch extension).
+"""Builds libgmm.so in-tree for sm_103a with nvcc (no cmake), and the host-side calls of the binding.
 
 Each .cu file is compiled to an object in parallel, then linked into
 ``moe_grouped_matrix_gb300/libgmm.so``.  Objects live in ``_build/`` next to
-this file and are rebuilt when any source or header is newer.
+this file and are rebuilt when any source or header is newer.  Beside them g++
+compiles ``csrc/host_calls.cpp`` (no device code) against the installed
+PyTorch's headers into ``moe_grouped_matrix_gb300/_host_calls.so``.
 """
 
 from __future__ import annotations
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libgmm.so")
+HOST_CALLS = os.path.join(CSRC, "host_calls.cpp")
+HOST_CALLS_PATH = os.path.join(HERE, "_host_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -46,6 +51,18 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _host_calls_command(out: str):
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(at, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"],
+               os.path.join(ROOT, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{d}" for d in include], HOST_CALLS, "-o", out, "-L" + os.path.join(at, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compiles every kernel source and links libgmm.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -60,11 +77,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd[1:1] = ["-Xptxas", "-v"]
             jobs.append((cmd, obj))
 
+    if force or _stale(HOST_CALLS_PATH, [HOST_CALLS] + headers):
+        tmp_calls = HOST_CALLS_PATH + f".tmp{os.getpid()}"
+        jobs.append((_host_calls_command(tmp_calls), tmp_calls))
+
     def run(job):
         cmd, obj = job
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {obj}:\n{res.stdout}\n{res.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {obj}:\n{res.stdout}\n{res.stderr}")
+        if cmd[0] == "g++":
+            os.replace(obj, HOST_CALLS_PATH)
         return res.stdout + res.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:

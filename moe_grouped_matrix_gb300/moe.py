@@ -9,12 +9,17 @@ expert and brought back, and microscaled 4-bit floating point.
     q = quantize_fp4(x, "nvfp4", order=order)      # the same rows in 4 bits, for gmm_fp4()
 
 Like the rest of the package this only marshals arguments; gradients are calls of their own
-(``route_backward``, ``dispatch_backward``, ``combine_backward``).
+(``route_backward``, ``dispatch_backward``, ``combine_backward``).  Arguments that are right as they
+stand go to the library through ``_host_calls.so`` (``csrc/host_calls.cpp``) in one step; all others
+are looked at here, one by one, and called through ctypes or refused.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import sys
 from typing import NamedTuple, Optional
 
@@ -30,6 +35,7 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 FP4_FORMATS = {"nvfp4": 0, "mxfp4": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 MAX_TOPK = 32
+_OUT_F32 = {torch.bfloat16: 0, torch.float32: 1}
 
 _package = sys.modules[__package__]
 _F = ctypes.c_float
@@ -77,12 +83,34 @@ def _on(device, stream):
 
 
 def _run(fn, status):
+    """Raises for a status that is not 0 (None: there is none)."""
     if status:
         raise GmmError(fn, status)
 
 
 def _lib():
     return _package._lib or load_library()
+
+
+_calls = None
+
+
+def _bind():
+    """Loads _host_calls.so and gives it the loaded library's functions."""
+    global _calls
+    lib = load_library()
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_host_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m moe_grouped_matrix_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._host_calls", path)
+    spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
+    calls = importlib.util.module_from_spec(spec)
+    loader.exec_module(calls)
+    names = ("gmm_route", "gmm_route_backward", "gmm_sort_by_expert", "gmm_dispatch", "gmm_combine",
+             "gmm_combine_backward", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_fp4")
+    calls.bind(*[ctypes.cast(getattr(lib, n), _P).value for n in names])
+    _calls = calls
+    return calls
 
 
 def _rows(t, name):
@@ -140,6 +168,12 @@ def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bia
     scale * softmax (over all experts) or scale * sigmoid of the logits, divided by their sum over
     the chosen experts with renormalize.  Tokens whose token_mask (bool or uint8 [tokens]) is 0,
     and slots past the experts that can be chosen, have expert -1 and weight 0."""
+    if stream is None:
+        got = (_calls or _bind()).route(logits, topk, SCORES.get(score), 1 if renormalize else 0, scale, select_bias,
+                                        token_mask)
+        if got.__class__ is tuple:
+            return got
+        _run("gmm_route", got)
     ld = _rows(logits, "logits")
     code = _float_code(logits, "logits")
     tokens, experts = logits.shape
@@ -161,6 +195,12 @@ def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bia
 def route_backward(dweights, experts, logits, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of route()'s weights with respect to the logits, [tokens, experts] of the logits'
     dtype, from dweights float32 [tokens, topk] and the experts that route() chose."""
+    if stream is None:
+        got = (_calls or _bind()).route_backward(dweights, experts, logits, SCORES.get(score),
+                                                 1 if renormalize else 0, scale)
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_route_backward", got)
     ld = _rows(logits, "logits")
     code = _float_code(logits, "logits")
     tokens, n = logits.shape
@@ -179,6 +219,11 @@ def route_backward(dweights, experts, logits, score="softmax", renormalize=True,
 def sort_by_expert(experts, num_experts, stream=None):
     """The stable order of the slots of experts int32 [tokens, topk] by expert, as an ExpertOrder.
     Slots whose expert is outside [0, num_experts) are dropped."""
+    if stream is None:
+        got = (_calls or _bind()).sort_by_expert(experts, num_experts)
+        if got.__class__ is tuple:
+            return ExpertOrder._make(got)
+        _run("gmm_sort_by_expert", got)
     if experts.dim() != 2:
         raise ValueError("experts must be [tokens, topk]")
     tokens, topk = experts.shape
@@ -204,6 +249,11 @@ def _order(order):
 def dispatch(x, order, stream=None):
     """The rows of x [tokens, d] (bfloat16 or float32, rows may have a pitch) in expert order:
     [tokens * topk, d], zeros past the groups."""
+    if stream is None:
+        got = (_calls or _bind()).dispatch(x, order.rows, order.source)
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_dispatch", got)
     ld = _rows(x, "x")
     code = _float_code(x, "x")
     tokens, topk = _order(order)
@@ -219,6 +269,11 @@ def dispatch(x, order, stream=None):
 def combine(rows, order, weights=None, stream=None):
     """Token order again: out[t] = sum over t's slots of weights[t, j] * rows[order.rows[t, j]], in
     fp32, rounded once; weights float32 [tokens, topk], or None for ones.  rows [tokens * topk, d]."""
+    if stream is None:
+        got = (_calls or _bind()).combine(rows, order.rows, order.source, weights)
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_combine", got)
     code = _float_code(_dev(rows, "rows"), "rows")
     tokens, topk = _order(order)
     if rows.dim() != 2 or rows.shape[0] != tokens * topk:
@@ -240,6 +295,11 @@ def dispatch_backward(drows, order, stream=None):
 def combine_backward(dout, rows, order, weights, stream=None):
     """Gradients of combine(): (drows [tokens * topk, d] of the rows' dtype, dweights float32
     [tokens, topk]) from dout [tokens, d] of the rows' dtype."""
+    if stream is None:
+        got = (_calls or _bind()).combine_backward(dout, rows, order.rows, order.source, weights)
+        if got.__class__ is tuple:
+            return got
+        _run("gmm_combine_backward", got)
     code = _float_code(_dev(rows, "rows"), "rows")
     tokens, topk = _order(order)
     if rows.dim() != 2 or rows.shape[0] != tokens * topk:
@@ -271,6 +331,12 @@ def quantize_fp4(x, format="nvfp4", order=None, stream=None):
     [rows, k] (rows may have a pitch) or a dense [batch, rows, k], the experts' weights for
     gmm_fp4(); k must be a multiple of 32.  With order, x [tokens, k] gives the rows of
     dispatch(x, order), each token quantised once."""
+    if stream is None:
+        got = (_calls or _bind()).quantize_fp4(x, FP4_FORMATS.get(format), None if order is None else order.rows,
+                                               None if order is None else order.source)
+        if got.__class__ is tuple:
+            return Fp4Tensor(*got, format)
+        _run("gmm_quantize_fp4", got)
     fmt = _fp4_format(format)
     code = _float_code(x, "x")
     if x.dim() == 3:
@@ -320,6 +386,12 @@ def _fp4_args(q, name, lead):
 
 def dequantize_fp4(q, out_dtype=torch.bfloat16, stream=None):
     """The values an Fp4Tensor stands for, [.., rows, k] of out_dtype (bfloat16 or float32)."""
+    if stream is None:
+        got = (_calls or _bind()).dequantize_fp4(q.codes, q.block_scale, q.row_scale, FP4_FORMATS.get(q.format),
+                                                 _OUT_F32.get(out_dtype))
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_dequantize_fp4", got)
     lead = q.codes.dim() - 2
     if lead not in (0, 1):
         raise ValueError("codes must be [rows, k / 2] or [batch, rows, k / 2]")
@@ -340,6 +412,17 @@ def gmm_fp4(lhs, rhs, group_sizes, rhs_bias=None, group_offset=0, out=None, out_
     NT layout: lhs an Fp4Tensor [m, k], rhs an Fp4Tensor [G_local, n, k] of the same format, on the
     block-scaled 4-bit tensor cores.  k must be a multiple of 32 and n of 8; rhs_bias
     [G_local, 1, n] bfloat16 or float32."""
+    if stream is None and rhs_bias is None and out is None and lhs.format == rhs.format and lhs.codes.is_cuda:
+        ws = workspace
+        if ws is None:
+            index = lhs.codes.device.index
+            ws = _package._workspaces.get((index, _raw_stream(index)))  # workspace_for()'s
+        got = (_calls or _bind()).gmm_fp4(lhs.codes, lhs.block_scale, lhs.row_scale, rhs.codes, rhs.block_scale,
+                                          rhs.row_scale, FP4_FORMATS.get(lhs.format), group_sizes, group_offset,
+                                          _OUT_F32.get(out_dtype), ws)
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_fp4", got)
     m, k = _fp4_args(lhs, "lhs", 0)
     n, kr = _fp4_args(rhs, "rhs", 1)
     if kr != k:
@@ -362,6 +445,7 @@ def gmm_fp4(lhs, rhs, group_sizes, rhs_bias=None, group_offset=0, out=None, out_
     if tuple(out.shape) != (m, n):
         raise ValueError(f"out must be [{m}, {n}], got {list(out.shape)}")
     ws = workspace if workspace is not None else workspace_for(device, stream)
+    _dev(ws, "workspace")
     _run("gmm_fp4", _lib().gmm_fp4(
         lhs.codes.data_ptr(), lhs.block_scale.data_ptr(), _ptr(lhs.row_scale), m, k, rhs.codes.data_ptr(),
         rhs.block_scale.data_ptr(), _ptr(rhs.row_scale), FP4_FORMATS[lhs.format], local, n, group_sizes.data_ptr(),
