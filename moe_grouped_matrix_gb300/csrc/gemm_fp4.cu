@@ -37,7 +37,16 @@
 // uniform registers: with one lane's own loop each tensor-core instruction and
 // each copy took some 80 cycles to issue, a stage over 1300 for 420 cycles of
 // MMA.  For the same reason a warp turns the whole of a stage, and has stages of
-// its own.
+// its own.  Codes and scales have rings of their own: a window of scales is ready
+// later than the codes copied with it, and is cheap to hold (prefill with one
+// ring of 5 for both 658 us, with 7 windows 617, with 8 or 9 the same, with 4 767).
+//
+// Measured (L2 cold): 8 experts, 16384 rows, 4096 -> 28672: NVFP4 618 us, 6.2
+// PFLOP/s; MXFP4 574 us.  128 experts, 32768 rows, 2048 -> 2048: 83 us for 456 MB
+// (67 us at the copy rate).  Decoding, 64 experts, 256 rows, 4096 -> 2048: 52 us
+// for 303 MB (45 us).  What bounds the first is the issuing of a stage's 16
+// instructions beside its waits, about 600 cycles for 420 of MMA; for seconds on
+// end the power cap (1740 MHz, 736 us before the last two steps).
 //
 // Roles (512 threads): warp 0 copies codes; warp 1 tensor memory and MMA (the
 // leader's in a pair); warps 2-9 epilogue, each set of four every other 32 rows;
@@ -65,7 +74,7 @@ constexpr uint32_t ROW_BYTES = BK / 2;
 constexpr uint32_t A_BYTES = BW * ROW_BYTES;
 constexpr uint32_t SF_BYTES = 128 * 16;  // a window of 128 rows' scales
 constexpr uint32_t OUT_PITCH = 80;       // of 32 bf16 columns in an epilogue warp's buffer: no bank conflicts
-constexpr uint32_t OUT_BYTES = 32 * OUT_PITCH;
+constexpr uint32_t OUT_BYTES = 16 * OUT_PITCH;
 
 template <bool kPair>
 struct Shape {
@@ -433,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     if (leader) {
       uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
+      const bool one = elected();
+      const uint64_t a_desc = sw128_desc(sbase + S::OFF_A, 16, 1024), b_desc = sw128_desc(sbase + S::OFF_B, 16, 1024);
       for (int32_t item = 0; item < items && ok; ++item) {
         const GemmTile t = tile_of(item);
         const int32_t ncols = chunk_n(t);
@@ -440,9 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * S::kChunk;
         for (int32_t kb = 0; kb < k_blocks; ++kb) {
-          // both are asked at once: one latency where both have come
-          const uint32_t turned = mbar_try_wait_cluster(turned_bar(slot), slot_phase);
-          const uint32_t full = mbar_try_wait(full_bar(stage), phase);
+          // Both are asked at once, by the test that does not suspend: this warp's own work for a stage is
+          // as long as the stage's MMAs, and each cycle of it counts (prefill: 662 us with suspending
+          // waits, 632 so, 618 with the lane elected and the descriptors made outside the loop too).
+          const uint32_t turned = mbar_test_wait_cluster(turned_bar(slot), slot_phase);
+          const uint32_t full = mbar_test_wait_cluster(full_bar(stage), phase);
           if (!__all_sync(0xffffffffu, turned & full) &&
               (!wait_warp_cluster(turned_bar(slot), slot_phase, abort_flag, p.err) ||
                !wait_warp(full_bar(stage), phase, abort_flag, p.err))) {
@@ -450,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             break;
           }
           tc_fence_after();
-          if (elected()) {
+          if (one) {
             // a stage uses 4 blocks of a window (NVFP4) or half of them (MXFP4)
             const uint32_t sf =
                 sbase + S::OFF_SF + slot * S::kParts * SF_BYTES + (kNv ? 0u : 1024u * uint32_t(kb & 1));
@@ -461,8 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
               if (kPair && ncols > 128)
                 copy_scales<kPair>(tmem_base + S::TM_SFB + 8 * j + 4, sf + 2 * SF_BYTES + 512u * j);
             }
-            const uint64_t ad = sw128_desc(sbase + S::OFF_A + stage * A_BYTES, 16, 1024);
-            const uint64_t bd = sw128_desc(sbase + S::OFF_B + stage * S::B_BYTES, 16, 1024);
+            const uint64_t ad = a_desc + uint64_t(stage * (A_BYTES >> 4)), bd = b_desc + uint64_t(stage * (S::B_BYTES >> 4));
 #pragma unroll
             for (uint32_t kk = 0; kk < BK / 64; ++kk) {
               const uint32_t j = kNv ? kk : kk >> 1;
@@ -475,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             commit<kPair>(sempty_bar(slot));
             if (kb == k_blocks - 1) commit<kPair>(accf_bar(acc));
           }
-          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
           acc_phase ^= 1u;
         }
       }
-      if (elected()) {
+      if (one) {
         if constexpr (kPair)
           mma_commit_pair(done_bar, 0x1);
         else
@@ -640,8 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             tmem_wait_ld16(v[1]);
             if (last) release();
             const uint32_t at = buf + uint32_t(8 * (lane >> 4) + (lane & 7)) * OUT_PITCH + uint32_t(lane >> 3 & 1) * 16u;
+            const int32_t c = col0 + 8 * (lane & 3);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + int64_t(row0 + c0) * p.n + c;
 #pragma unroll
-            for (int g = 0; g < 4; g += 2) {
+            for (int g = 0; g < 4; g += 2) {  // 16 rows at a time
               float r[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -655,19 +668,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
                   m[q] = pack_bf16x2(fmaf(__uint_as_float(v[h][i]) * r[q & 2], now.ws[f], now.bias[f]),
                                      fmaf(__uint_as_float(v[h][i + 1]) * r[(q & 2) + 1], now.ws[f], now.bias[f]));
                 }
-                stmatrix_trans(at + uint32_t(8 * g) * OUT_PITCH + uint32_t(h) * 32u, m[0], m[1], m[2], m[3]);
+                stmatrix_trans(at + uint32_t(h) * 32u, m[0], m[1], m[2], m[3]);
               }
-            }
-            __syncwarp();
-            const int32_t c = col0 + 8 * (lane & 3);
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + int64_t(row0 + c0) * p.n + c;
+              __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int32_t r = 8 * q + (lane >> 2);
-              const uint4 x = ld_shared_v4(buf + uint32_t(r) * OUT_PITCH + uint32_t(lane & 3) * 16u);
-              if (c < p.n && c0 + r < rows) st_global_v4(o + int64_t(r) * p.n, x.x, x.y, x.z, x.w);
+              for (int q = 0; q < 2; ++q) {
+                const int32_t w = 8 * q + (lane >> 2), row = 8 * g + w;
+                const uint4 x = ld_shared_v4(buf + uint32_t(w) * OUT_PITCH + uint32_t(lane & 3) * 16u);
+                if (c < p.n && c0 + row < rows) st_global_v4(o + int64_t(row) * p.n, x.x, x.y, x.z, x.w);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }
