@@ -111,7 +111,7 @@ def test_turning_warps_without_slots_of_their_own_are_caught(pair):
     they have not seen every phase, and pass on the phase before."""
     _, n_scales, turners = depths(pair)
     assert n_scales % turners
-    found = []
-    for seed in range(25):
-        found += model.run(roles(tiles(seed), pair, turner_of=lambda s: s % turners), seed)
-    assert any("passed at" in e for e in found), found[:3]
+    for seed in range(400):
+        if any("passed at" in e for e in model.run(roles([16] * 6, pair, turner_of=lambda s: s % turners), seed)):
+            return
+    pytest.fail("no schedule showed it")
