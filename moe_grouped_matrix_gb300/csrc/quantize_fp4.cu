@@ -319,60 +319,50 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   }
 }
 
-// 16 codes times s times rs.
-template <class T>
-__device__ __forceinline__ void write_values(T* out, uint2 c, float s, float rs) {
-  float v[16];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 q = e2m1x2_values((j < 4 ? c.x : c.y) >> (8 * (j % 4)));
-    v[2 * j] = q.x * s * rs, v[2 * j + 1] = q.y * s * rs;
-  }
-  if constexpr (sizeof(T) == 4) {
-    float4* o = reinterpret_cast<float4*>(out);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-    uint32_t h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      memcpy(&h[j], &q, 4);
-    }
-    uint4* o = reinterpret_cast<uint4*>(out);
-    o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    o[1] = make_uint4(h[4], h[5], h[6], h[7]);
-  }
-}
-
-// A CTA for each row.
+// A CTA for each row; a thread writes 16 bytes at a time (8 bf16 or 4 f32 values), so that a warp's
+// store is whole lines, and has four such pieces on their way.
 template <class T, bool kNv>
 __global__ void __launch_bounds__(kMaxThreads) dequantize_fp4_kernel(const DequantParams p) {
-  const int32_t units = int32_t(p.k / 16);
+  constexpr int kVals = 16 / int(sizeof(T)), kAtOnce = 4;
+  constexpr int kBlockPieces = (kNv ? 16 : 32) / kVals;
+  const int32_t pieces = int32_t(p.k / kVals);
   const int64_t row = blockIdx.x;
   const int64_t batch = row / p.rows_per_batch, r = row - batch * p.rows_per_batch;
   const int64_t windows = (p.k + (kNv ? 255 : 511)) / (kNv ? 256 : 512);
   const uint8_t* scale = p.scale + (batch * windows * p.rows_per_batch + r) * 16;
-  const uint2* codes = reinterpret_cast<const uint2*>(p.codes + row * (p.k / 2));
+  const uint8_t* codes = p.codes + row * (p.k / 2);
   const float rs = kNv ? __ldg(p.row_scale + row) : 1.f;
-  T* out = static_cast<T*>(p.out) + row * p.k;
-  // two units on their way at once
-  for (int32_t u0 = threadIdx.x; u0 < units; u0 += 2 * blockDim.x) {
-    uint32_t byte[2];
-    uint2 c[2];
+  uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.k);
+  for (int32_t u0 = threadIdx.x; u0 < pieces; u0 += kAtOnce * blockDim.x) {
+    uint32_t byte[kAtOnce], c[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const int32_t u = u0 + i * int32_t(blockDim.x);
-      if (u < units) {
-        const int32_t b = kNv ? u : u / 2;
+      if (u < pieces) {
+        const int32_t b = u / kBlockPieces;
         byte[i] = __ldg(scale + int64_t(b / 16) * p.rows_per_batch * 16 + b % 16);
-        c[i] = __ldg(codes + u);
+        c[i] = kVals == 8 ? __ldg(reinterpret_cast<const uint32_t*>(codes) + u)
+                          : uint32_t(__ldg(reinterpret_cast<const uint16_t*>(codes) + u));
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const int32_t u = u0 + i * int32_t(blockDim.x);
-      if (u < units) write_values(out + 16 * int64_t(u), c[i], scale_value<kNv>(byte[i]), rs);
+      if (u >= pieces) continue;
+      const float s = scale_value<kNv>(byte[i]);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < kVals / 2; ++j) {
+        const float2 q = e2m1x2_values(c[i] >> (8 * j));
+        const float x = q.x * s * rs, y = q.y * s * rs;
+        if constexpr (sizeof(T) == 4) {
+          w[2 * j] = __float_as_uint(x), w[2 * j + 1] = __float_as_uint(y);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+          memcpy(&w[j], &h, 4);
+        }
+      }
+      out[u] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -465,7 +455,8 @@ extern "C" int gmm_dequantize_fp4(const void* codes, const void* block_scale, co
   if (all_rows > INT32_MAX) return GMM_ERR_SHAPE;
   const DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(block_scale), row_scale,
                         rows_per_batch, k, out};
-  const int threads = int(k / 32 >= kMaxThreads ? kMaxThreads : (k / 32 + 31) / 32 * 32);  // two units each
+  const int64_t lanes = (k / (out_dtype == GMM_DTYPE_F32 ? 4 : 8) + 3) / 4;  // four pieces each
+  const int threads = int(lanes >= kMaxThreads ? kMaxThreads : (lanes + 31) / 32 * 32);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned grid = unsigned(all_rows);
   if (out_dtype == GMM_DTYPE_F32) {
