@@ -60,7 +60,7 @@ def _host_calls_command(out: str):
                os.path.join(ROOT, "include")]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f"-I{d}" for d in include], HOST_CALLS, "-o", out, "-L" + os.path.join(at, "lib"), "-ltorch_python",
-            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(32 * kWarps)
                 int32_t* __restrict__ group_sizes, int32_t* __restrict__ rows, int32_t* __restrict__ source,
                 int32_t ctas) {
   constexpr int kThreads = 32 * kWarps;
+  griddep_begin();
+  experts = after_begin(experts);
   extern __shared__ uint32_t table[];  // [kWarps][bins], then the CTA's sums [bins] and first places [bins]
   __shared__ uint32_t warp_sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -168,18 +170,8 @@ cudaError_t launch_sort_as(const int32_t* experts, int32_t slots, int32_t num_ex
   if (e != cudaSuccess) return e;
   const int64_t warps = int64_t(ctas) * kWarps;
   const int32_t run = int32_t(((slots + warps - 1) / warps + 31) / 32 * 32);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(ctas);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, experts, slots, num_experts, run, group_sizes, rows, source, int32_t(ctas));
+  return launch_dependent(kern, unsigned(ctas), 32 * kWarps, smem, stream, ctas, experts, slots, num_experts, run,
+                          group_sizes, rows, source, int32_t(ctas));
 }
 
 // Up to 512 slots: one CTA of 8 warps (256 slots: 2.3 us in a graph); up to 1024 one CTA of 32
@@ -241,6 +233,8 @@ __global__ void __launch_bounds__(kThreads)
     dispatch_kernel(const U* __restrict__ x, int64_t tokens, int64_t units, int64_t x_units, int32_t topk,
                     int64_t parts, const int32_t* __restrict__ rows, const int32_t* __restrict__ source,
                     U* __restrict__ out) {
+  griddep_begin();
+  x = after_begin(x), rows = after_begin(rows), source = after_begin(source);
   const int lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / parts;
@@ -271,6 +265,8 @@ template <class U, class T, int kPer, int kBatch>
 __global__ void __launch_bounds__(kThreads)
     combine_kernel(const U* __restrict__ in, int64_t tokens, int64_t units, int32_t topk, int64_t parts,
                    const int32_t* __restrict__ rows, const float* __restrict__ weights, U* __restrict__ out) {
+  griddep_begin();
+  in = after_begin(in), rows = after_begin(rows), weights = after_begin(weights);
   constexpr int N = Unit<U, T>::kN;
   const int lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -323,6 +319,9 @@ __global__ void __launch_bounds__(kBackThreads)
                             int32_t topk,
                             const int32_t* __restrict__ rows, const int32_t* __restrict__ source,
                             const float* __restrict__ weights, U* __restrict__ din, float* __restrict__ dweights) {
+  griddep_begin();
+  dout = after_begin(dout), in = after_begin(in), rows = after_begin(rows), source = after_begin(source);
+  weights = after_begin(weights);
   constexpr int N = Unit<U, T>::kN;
   __shared__ float part[kBackThreads / 32][GMM_MAX_TOPK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -436,9 +435,8 @@ cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, con
       if (grid == 0) return cudaErrorInvalidConfiguration;
       // rows on their way at once, by how many a token has
       auto kern = topk <= 2 ? combine_kernel<U, T, kPer, 2> : combine_kernel<U, T, kPer, 4>;
-      kern<<<grid, kThreads, 0, s>>>(static_cast<const U*>(in), tokens, units, topk, parts, rows, weights,
-                                     static_cast<U*>(out));
-      return cudaGetLastError();
+      return launch_dependent(kern, grid, kThreads, 0, s, 1, static_cast<const U*>(in), tokens, units, topk, parts, rows,
+                              weights, static_cast<U*>(out));
     }
   });
 }
@@ -461,9 +459,9 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
       const int64_t lanes = (units + kPer - 1) / kPer;
       const int threads = lanes >= kBackThreads ? kBackThreads : int((lanes + 31) / 32 * 32);
       auto kern = kWide && topk > 2 ? combine_backward_kernel<U, T, kPer, 4> : combine_backward_kernel<U, T, kPer, 2>;
-      kern<<<unsigned(tokens), threads, 0, s>>>(static_cast<const U*>(dout), static_cast<const U*>(in), tokens, units,
-                                                topk, rows, source, weights, static_cast<U*>(din), dweights);
-      return cudaGetLastError();
+      return launch_dependent(kern, unsigned(tokens), threads, 0, s, 1, static_cast<const U*>(dout),
+                              static_cast<const U*>(in), tokens, units, topk, rows, source, weights,
+                              static_cast<U*>(din), dweights);
     }
   });
 }
@@ -503,10 +501,8 @@ extern "C" int gmm_dispatch(const void* x, int dtype, int64_t tokens, int64_t d,
     constexpr int kPer = units_of<U>(32);
     const unsigned grid = row_grid(tokens, units, kPer, &parts);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    dispatch_kernel<U, kPer><<<grid, kThreads, 0, s>>>(static_cast<const U*>(x), tokens, units,
-                                                   x_ld * int64_t(el) / int64_t(sizeof(U)), topk, parts, rows, source,
-                                                   static_cast<U*>(out));
-    return cudaGetLastError();
+    return launch_dependent(dispatch_kernel<U, kPer>, grid, kThreads, 0, s, 1, static_cast<const U*>(x), tokens, units,
+                            x_ld * int64_t(el) / int64_t(sizeof(U)), topk, parts, rows, source, static_cast<U*>(out));
   }));
 }
 

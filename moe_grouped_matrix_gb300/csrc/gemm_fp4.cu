@@ -278,7 +278,7 @@ __device__ __forceinline__ float load_bias(const Params& p, int64_t i) {
 }
 
 template <bool kPair, bool kNv, bool kOutF32>
-__global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_constant__ Maps maps, const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_constant__ Maps maps, Params p) {
   using S = Shape<kPair>;
   constexpr int kStages = S::kStages, kScales = S::kScales;
   extern __shared__ uint8_t smem_raw[];
@@ -333,6 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       tmem_relinquish();
     }
   }
+  griddep_begin();
+  p.group_sizes = after_begin(p.group_sizes), p.bias = after_begin(p.bias);
+  p.lhs_row_scale = after_begin(p.lhs_row_scale), p.rhs_row_scale = after_begin(p.rhs_row_scale);
   if (warp == 2) {
     build_group_offsets(p.group_sizes, p.num_total_groups, p.m, offs, p.err);
     build_tile_prefix(offs, go, p.num_local_groups, S::kChunk, tiles);
@@ -728,26 +731,26 @@ cudaError_t launch(const Maps& maps, const Params& p, int sms, cudaStream_t stre
   auto kern = gemm_fp4_kernel<kPair, kNv, kOutF32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM_BYTES));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kPair ? sms & ~1 : sms);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = kPair ? 1 : 0;
+  unsigned grid = unsigned(kPair ? sms & ~1 : sms);
   if (kPair) {
     // One pair per co-resident cluster slot (persistent kernel).
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     int clusters = 0;
     e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorLaunchOutOfResources;
-    if (2 * clusters < int(cfg.gridDim.x)) cfg.gridDim.x = unsigned(2 * clusters);
+    if (2 * clusters < int(grid)) grid = unsigned(2 * clusters);
   }
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+  return launch_dependent(kern, grid, kThreads, S::SMEM_BYTES, stream, S::kCtas, maps, p);
 }
 
 template <bool kPair>

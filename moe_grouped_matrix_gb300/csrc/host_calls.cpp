@@ -2,7 +2,7 @@
 // they stand (dense CUDA tensors of the expected types and sizes, the current
 // stream) one call from Python checks them, allocates the results and calls the C
 // ABI.  At decoding sizes an operator is a few microseconds on the GPU, and this
-// work done in Python costs more: combine() of 64 tokens 10 us in Python, 5 here.
+// work done in Python costs more: combine() takes the host 10 us in Python, 3 here.
 //
 // Every function returns None for any other arguments, and moe.py then goes
 // through them one by one and says what is wrong or handles the case; an int is
@@ -10,7 +10,7 @@
 // that the binding has loaded, by address.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -57,8 +57,9 @@ int64_t pitch(const Tensor* t) {
   return t->stride(0) >= d ? t->stride(0) : -1;
 }
 
+// The CUDA allocation itself, without at::empty()'s way through the dispatcher (0.7 us a tensor).
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }

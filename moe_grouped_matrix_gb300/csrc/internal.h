@@ -8,6 +8,27 @@
 
 namespace gmmk {
 
+// Launches a kernel that begins with griddep_begin() (ptx.cuh) as the programmatic dependent of what is
+// ahead of it on the stream: its launch overlaps that work's end.  cluster > 1: in clusters of so many CTAs.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t stream,
+                             int cluster, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = unsigned(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Forward grouped matmul with bf16 operands (NT or NN weight layout).
 struct GemmLaunch {
   CUtensorMap tm_lhs;  // lhs [m, k], box {64, 128}, 128-byte swizzle

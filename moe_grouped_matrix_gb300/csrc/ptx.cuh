@@ -105,6 +105,21 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The start of a kernel that is launched so (launch_dependent in internal.h): the next kernel may be
+// set up from here on, and nothing is read or written before the kernels ahead have completed.
+__device__ __forceinline__ void griddep_begin() {
+  griddep_launch_dependents();
+  griddep_wait();
+}
+
+// A pointer that no load can be moved ahead of: read-only loads (__ldg, or of const __restrict__) count
+// as free to move, across griddep_begin() too, unless their address comes after it.
+template <class T>
+__device__ __forceinline__ T* after_begin(T* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

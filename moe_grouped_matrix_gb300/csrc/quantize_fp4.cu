@@ -29,6 +29,7 @@
 
 #include "../../include/libgmm_moe.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace gmmk {
 namespace {
@@ -165,7 +166,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // kUnits > 0: a thread's units, all in registers; 0: any number, read again
 // for the codes.
 template <class T, bool kNv, int kThreads, int kUnits, bool kOrder>
-__global__ void __launch_bounds__(kThreads == 32 ? 128 : kThreads) quantize_fp4_kernel(const QuantParams p, bool wide) {
+__global__ void __launch_bounds__(kThreads == 32 ? 128 : kThreads) quantize_fp4_kernel(QuantParams p, bool wide) {
+  griddep_begin();
+  p.x = after_begin(p.x), p.rows = after_begin(p.rows), p.source = after_begin(p.source);
   constexpr int kRows = kThreads == 32 ? 4 : 1;  // rows a CTA
   __shared__ uint32_t warp_max[kThreads / 32];
   const int lane = threadIdx.x & 31;
@@ -322,7 +325,9 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 // A CTA for each row; a thread writes 16 bytes at a time (8 bf16 or 4 f32 values), so that a warp's
 // store is whole lines, and has four such pieces on their way.
 template <class T, bool kNv>
-__global__ void __launch_bounds__(kMaxThreads) dequantize_fp4_kernel(const DequantParams p) {
+__global__ void __launch_bounds__(kMaxThreads) dequantize_fp4_kernel(DequantParams p) {
+  griddep_begin();
+  p.codes = after_begin(p.codes), p.scale = after_begin(p.scale), p.row_scale = after_begin(p.row_scale);
   constexpr int kVals = 16 / int(sizeof(T)), kAtOnce = 4;
   constexpr int kBlockPieces = (kNv ? 16 : 32) / kVals;
   const int32_t pieces = int32_t(p.k / kVals);
@@ -372,11 +377,9 @@ cudaError_t quantize_as(const QuantParams& p, bool wide, cudaStream_t s) {
   const int64_t blocks = kThreads == 32 ? (p.in_rows + 3) / 4 : p.in_rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   constexpr int kBlock = kThreads == 32 ? 128 : kThreads;
-  if (p.rows != nullptr)
-    quantize_fp4_kernel<T, kNv, kThreads, kUnits, true><<<unsigned(blocks), kBlock, 0, s>>>(p, wide);
-  else
-    quantize_fp4_kernel<T, kNv, kThreads, kUnits, false><<<unsigned(blocks), kBlock, 0, s>>>(p, wide);
-  return cudaGetLastError();
+  auto kern = p.rows != nullptr ? quantize_fp4_kernel<T, kNv, kThreads, kUnits, true>
+                                : quantize_fp4_kernel<T, kNv, kThreads, kUnits, false>;
+  return launch_dependent(kern, unsigned(blocks), kBlock, 0, s, 1, p, wide);
 }
 
 // Threads a row and units a thread that cover a row's whole windows.  With many rows a thread takes
@@ -459,13 +462,9 @@ extern "C" int gmm_dequantize_fp4(const void* codes, const void* block_scale, co
   const int threads = int(lanes >= kMaxThreads ? kMaxThreads : (lanes + 31) / 32 * 32);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned grid = unsigned(all_rows);
-  if (out_dtype == GMM_DTYPE_F32) {
-    if (nv) dequantize_fp4_kernel<float, true><<<grid, threads, 0, s>>>(p);
-    else dequantize_fp4_kernel<float, false><<<grid, threads, 0, s>>>(p);
-  } else {
-    if (nv) dequantize_fp4_kernel<__nv_bfloat16, true><<<grid, threads, 0, s>>>(p);
-    else dequantize_fp4_kernel<__nv_bfloat16, false><<<grid, threads, 0, s>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  auto kern = out_dtype == GMM_DTYPE_F32
+                  ? (nv ? dequantize_fp4_kernel<float, true> : dequantize_fp4_kernel<float, false>)
+                  : (nv ? dequantize_fp4_kernel<__nv_bfloat16, true> : dequantize_fp4_kernel<__nv_bfloat16, false>);
+  const cudaError_t e = launch_dependent(kern, grid, threads, 0, s, 1, p);
   return e == cudaSuccess ? GMM_OK : record_cuda_error(e);
 }

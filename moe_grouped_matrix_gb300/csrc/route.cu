@@ -22,6 +22,7 @@
 
 #include "../../include/libgmm_moe.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace gmmk {
 namespace {
@@ -91,7 +92,9 @@ struct RouteParams {
 };
 
 template <int V, class T>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
+  griddep_begin();
+  p.logits = after_begin(p.logits), p.bias = after_begin(p.bias), p.mask = after_begin(p.mask);
   const int lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
@@ -183,7 +186,9 @@ struct RouteBackParams {
 //   sigmoid        dl_j = w'_j (1 - sigmoid(l_j)) g_j
 // and dl_j = dv_j (1 - sigmoid(l_j)) for the renormalised sigmoid.
 template <int V, class T>
-__global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const RouteBackParams p) {
+__global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(RouteBackParams p) {
+  griddep_begin();
+  p.dweights = after_begin(p.dweights), p.chosen = after_begin(p.chosen), p.logits = after_begin(p.logits);
   const int lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
@@ -283,8 +288,7 @@ cudaError_t route(const RouteParams& p, cudaStream_t stream) {
     constexpr int V = decltype(v)::value;
     RouteParams q = p;
     q.wide = p.experts % V == 0 && p.ld * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
-    route_kernel<V, T><<<unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0, stream>>>(q);
-    return cudaGetLastError();
+    return launch_dependent(route_kernel<V, T>, unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0, stream, 1, q);
   });
 }
 
@@ -295,8 +299,8 @@ cudaError_t route_backward(const RouteBackParams& p, cudaStream_t stream) {
     RouteBackParams q = p;
     q.wide = p.experts % V == 0 && p.ld * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
              p.experts * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0;
-    route_backward_kernel<V, T><<<unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0, stream>>>(q);
-    return cudaGetLastError();
+    return launch_dependent(route_backward_kernel<V, T>, unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0,
+                            stream, 1, q);
   });
 }
 
