@@ -33,38 +33,37 @@ __device__ __forceinline__ int32_t slot_row(const int32_t* rows, int64_t slot, i
 // ------------------------------------------------------------------ the sort
 // One cluster of CTAs.  Every warp owns a run of consecutive slots: it counts its
 // experts in its own row of a table in shared memory, the table is summed down
-// the warps and (through distributed shared memory) across the CTAs, and then
-// the warp walks its run again and gives each slot the next place of its
-// expert, equal experts within a step of 32 in lane order.  So the order is
-// stable and no result hangs on the order of an atomic.  Dropped slots count as
-// one more expert after the last.
+// the warps and across the CTAs (each CTA writes its sums into all of them, so
+// that one barrier of the cluster is all they wait for), and then the warp walks
+// its run again and gives each slot the next place of its expert, equal experts
+// within a step of 32 in lane order.  So the order is stable and no result hangs
+// on the order of an atomic.  Dropped slots count as one more expert after the
+// last.
 //
-// Bound by latency, not by its 12 bytes a slot: so few barriers, the counts of
-// all warps read at once before they are summed, and up to 16 CTAs.
+// Bound by latency, not by its 12 bytes a slot: 32768 slots of 128 experts take
+// 6.6 us in a graph, 12000 cycles, of which 4000 are the three barriers of the
+// cluster and the sums between them and 4000 the last walk, whose stores are
+// scattered.  There lanes with equal experts find each other by a ballot for each
+// bit of the expert's number (with __match_any_sync, and the sums read from the
+// other CTAs instead of written into them, 7.6 us).
 constexpr int kSortCluster = 16;
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-// kWarps a CTA; `run` slots a warp, a multiple of 32.
+// kWarps a CTA; `run` slots a warp, a multiple of 32; 2^bits > num_experts.
 template <int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
-    sort_kernel(const int32_t* __restrict__ experts, int32_t slots, int32_t num_experts, int32_t run,
+    sort_kernel(const int32_t* __restrict__ experts, int32_t slots, int32_t num_experts, int32_t bits, int32_t run,
                 int32_t* __restrict__ group_sizes, int32_t* __restrict__ rows, int32_t* __restrict__ source,
                 int32_t ctas) {
   constexpr int kThreads = 32 * kWarps;
   griddep_begin();
   experts = after_begin(experts);
-  extern __shared__ uint32_t table[];  // [kWarps][bins], then the CTA's sums [bins] and first places [bins]
+  extern __shared__ uint32_t table[];  // [kWarps][bins]; each CTA's sums [ctas][bins]; first places [bins]
   __shared__ uint32_t warp_sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bins = num_experts + 1;
   uint32_t* mine = table + warp * bins;
-  uint32_t* total = table + kWarps * bins;
-  uint32_t* place = total + bins;
+  uint32_t* sums = table + kWarps * bins;
+  uint32_t* place = sums + ctas * bins;
   const int32_t rank = ctas > 1 ? int32_t(cluster_ctarank()) : 0;
   const int64_t first = int64_t(rank * kWarps + warp) * run;
   const int32_t lo = int32_t(first < slots ? first : slots);
@@ -81,6 +80,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (held[i] >= 0) atomicAdd(mine + held[i], 1u);
   for (int32_t s = lo + 128 + lane; s < hi; s += 32) atomicAdd(mine + bin_of(__ldg(experts + s)), 1u);
   __syncthreads();
+  if (ctas > 1) cluster_sync();  // every CTA has started: its shared memory can be written
   for (int b = tid; b < bins; b += kThreads) {
     uint32_t c[kWarps], sum = 0;
 #pragma unroll
@@ -90,35 +90,32 @@ __global__ void __launch_bounds__(32 * kWarps)
       table[w * bins + b] = sum;
       sum += c[w];
     }
-    total[b] = sum;
+    if (ctas > 1) {
+      const uint32_t to = smem_u32(sums + rank * bins + b);
+      for (int r = 0; r < ctas; ++r) st_shared_cluster_u32(mapa_shared(to, uint32_t(r)), sum);
+    } else {
+      sums[b] = sum;
+    }
   }
   if (ctas > 1)
     cluster_sync();
   else
     __syncthreads();
-  // Each expert's rows over all CTAs, those of the CTAs before this one, and the experts before: the
-  // threads take kPer consecutive bins each.
-  constexpr int kPer = (GMM_MAX_GROUPS + 1 + kThreads - 1) / kThreads;
+  // Each expert's rows over all CTAs, those of the CTAs before this one, and the experts before: a
+  // thread takes kPer consecutive experts.
+  constexpr int kPer = GMM_MAX_GROUPS / kThreads;
   uint32_t all[kPer], before[kPer], sum = 0;
   const int b0 = tid * kPer;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     all[i] = before[i] = 0;
-    if (b0 + i < bins) {
-      if (ctas > 1) {
-        uint32_t c[kSortCluster];
-#pragma unroll
-        for (int r = 0; r < kSortCluster; ++r)
-          c[r] = r < ctas ? ld_cluster_u32(mapa_shared(smem_u32(total + b0 + i), uint32_t(r))) : 0u;
-#pragma unroll
-        for (int r = 0; r < kSortCluster; ++r) {
-          all[i] += c[r];
-          before[i] += r < rank ? c[r] : 0u;
-        }
-      } else {
-        all[i] = total[b0 + i];
+    if (b0 + i < num_experts) {
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t c = sums[r * bins + b0 + i];
+        all[i] += c;
+        before[i] += r < rank ? c : 0u;
       }
-      if (rank == 0 && b0 + i < num_experts) group_sizes[b0 + i] = int32_t(all[i]);
+      if (rank == 0) group_sizes[b0 + i] = int32_t(all[i]);
     }
     sum += all[i];
   }
@@ -130,17 +127,29 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  uint32_t start = incl - sum;
+  uint32_t start = incl - sum, kept = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) start += w < warp ? warp_sums[w] : 0u;
+  for (int w = 0; w < kWarps; ++w) {
+    start += w < warp ? warp_sums[w] : 0u;
+    kept += warp_sums[w];
+  }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (b0 + i < bins) place[b0 + i] = start + before[i];
+    if (b0 + i < num_experts) place[b0 + i] = start + before[i];
     start += all[i];
+  }
+  if (tid == kThreads - 1) {  // the dropped ones
+    for (int r = 0; r < rank; ++r) kept += sums[r * bins + num_experts];
+    place[num_experts] = kept;
   }
   __syncthreads();
   auto put = [&](int32_t s, int32_t b) {  // a step of 32 slots, b the bin of slot s or -1
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
+    uint32_t same = __ballot_sync(0xffffffffu, b >= 0);
+    for (int i = 0; i < bits; ++i) {
+      const bool set = (b >> i) & 1;
+      const uint32_t with = __ballot_sync(0xffffffffu, set);
+      same &= set ? with : ~with;
+    }
     const int ahead = __popc(same & ((1u << lane) - 1u));
     const uint32_t at = b >= 0 ? place[b] + mine[b] + uint32_t(ahead) : 0u;
     __syncwarp();
@@ -156,13 +165,14 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (lo + 32 * i < hi) put(lo + 32 * i + lane, held[i]);
   for (int32_t s0 = lo + 128; s0 < hi; s0 += 32)
     put(s0 + lane, s0 + lane < hi ? bin_of(__ldg(experts + s0 + lane)) : -1);
-  if (ctas > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 template <int kWarps>
 cudaError_t launch_sort_as(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
                            int32_t* rows, int32_t* source, int ctas, cudaStream_t stream) {
-  const size_t smem = size_t(kWarps + 2) * (num_experts + 1) * sizeof(uint32_t);
+  const size_t smem = size_t(kWarps + ctas + 1) * (num_experts + 1) * sizeof(uint32_t);
+  int bits = 1;
+  while ((1 << bits) <= num_experts) ++bits;
   auto kern = sort_kernel<kWarps>;
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -170,18 +180,18 @@ cudaError_t launch_sort_as(const int32_t* experts, int32_t slots, int32_t num_ex
   if (e != cudaSuccess) return e;
   const int64_t warps = int64_t(ctas) * kWarps;
   const int32_t run = int32_t(((slots + warps - 1) / warps + 31) / 32 * 32);
-  return launch_dependent(kern, unsigned(ctas), 32 * kWarps, smem, stream, ctas, experts, slots, num_experts, run,
-                          group_sizes, rows, source, int32_t(ctas));
+  return launch_dependent(kern, unsigned(ctas), 32 * kWarps, smem, stream, ctas, experts, slots, num_experts, bits,
+                          run, group_sizes, rows, source, int32_t(ctas));
 }
 
-// Up to 512 slots: one CTA of 8 warps (256 slots: 2.3 us in a graph); up to 1024 one CTA of 32
-// (a step a warp); up to 8192 eight CTAs (the portable cluster), above that sixteen: 4096 slots 6.1 us
-// with eight and 7.8 with one, 32768 slots 7.6 us with sixteen and 9.3 with eight.
+// Up to 1024 slots: one CTA of 8 warps (256 slots 2.4 us in a graph, 1024 slots 3.2; with 32 warps
+// 4.1); up to 2048 one CTA of 32 (4.7 us, with eight CTAs 5.2); up to 8192 eight CTAs (the portable
+// cluster; 4096 slots 5.4 us, with one 6.1), above that sixteen (32768 slots 6.6 us, with eight 7.3).
 cudaError_t launch_sort(const int32_t* experts, int32_t slots, int32_t num_experts, int32_t* group_sizes,
                         int32_t* rows, int32_t* source, cudaStream_t stream) {
-  if (slots <= 512)
+  if (slots <= 1024)
     return launch_sort_as<8>(experts, slots, num_experts, group_sizes, rows, source, 1, stream);
-  const int ctas = slots <= 1024 ? 1 : slots <= 8192 ? 8 : kSortCluster;
+  const int ctas = slots <= 2048 ? 1 : slots <= 8192 ? 8 : kSortCluster;
   return launch_sort_as<32>(experts, slots, num_experts, group_sizes, rows, source, ctas, stream);
 }
 
