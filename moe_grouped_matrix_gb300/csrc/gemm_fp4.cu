@@ -41,12 +41,12 @@
 // later than the codes copied with it, and is cheap to hold (prefill with one
 // ring of 5 for both 658 us, with 7 windows 617, with 8 or 9 the same, with 4 767).
 //
-// Measured (L2 cold): 8 experts, 16384 rows, 4096 -> 28672: NVFP4 618 us, 6.2
-// PFLOP/s; MXFP4 574 us.  128 experts, 32768 rows, 2048 -> 2048: 83 us for 456 MB
+// Measured (L2 cold): 8 experts, 16384 rows, 4096 -> 28672: NVFP4 605 us, 6.4
+// PFLOP/s; MXFP4 562 us.  128 experts, 32768 rows, 2048 -> 2048: 83 us for 456 MB
 // (67 us at the copy rate).  Decoding, 64 experts, 256 rows, 4096 -> 2048: 52 us
-// for 303 MB (45 us).  What bounds the first is the issuing of a stage's 16
-// instructions beside its waits, about 600 cycles for 420 of MMA; for seconds on
-// end the power cap (1740 MHz, 736 us before the last two steps).
+// for 303 MB (45 us), 46 back to back with the rows' quantisation.  What bounds
+// the first is the issuing of a stage's 16 instructions beside its waits, about
+// 600 cycles for 420 of MMA; for seconds on end the power cap (700 us).
 //
 // Roles (512 threads): warp 0 copies codes; warp 1 tensor memory and MMA (the
 // leader's in a pair); warps 2-9 epilogue, each set of four every other 32 rows;
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
               if (kPair && ncols > 128)
                 copy_scales<kPair>(tmem_base + S::TM_SFB + 8 * j + 4, sf + 2 * SF_BYTES + 512u * j);
             }
+            commit<kPair>(sempty_bar(slot));  // the window is free once it is copied
             const uint64_t ad = a_desc + uint64_t(stage * (A_BYTES >> 4)), bd = b_desc + uint64_t(stage * (S::B_BYTES >> 4));
 #pragma unroll
             for (uint32_t kk = 0; kk < BK / 64; ++kk) {
@@ -487,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
                                   (uint32_t(kb) | kk) != 0 ? 1u : 0u);
             }
             commit<kPair>(empty_bar(stage));
-            commit<kPair>(sempty_bar(slot));
             if (kb == k_blocks - 1) commit<kPair>(accf_bar(acc));
           }
           if (++stage == kStages) {
