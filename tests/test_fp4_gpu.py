@@ -393,3 +393,18 @@ def test_refusals():
         G.gmm_fp4(lhs, rhs, gs, out=torch.zeros((4, 8), device=DEV))
     with pytest.raises(ValueError, match="rhs_bias"):
         G.gmm_fp4(lhs, rhs, gs, rhs_bias=torch.zeros((2, 16), device=DEV))
+
+
+@pytest.mark.parametrize("groups,first,count", [(1024, 0, 1024), (1000, 37, 500), (33, 1, 32), (5, 4, 1)])
+def test_many_groups(groups, first, count):
+    """As many groups as there can be, most of them of a few rows or none, and slices of them."""
+    rng = np.random.default_rng(groups)
+    sizes = rng.integers(0, 4, groups)
+    sizes[rng.integers(0, groups, 3)] = 70
+    k, n, m = 64, 32, int(sizes.sum())
+    lhs, a = operand((m, k), "mxfp4", 14)
+    rhs, w = operand((count, n, k), "mxfp4", 15)
+    out = G.gmm_fp4(lhs, rhs, torch.tensor(sizes, dtype=torch.int32, device=DEV), group_offset=first,
+                    out_dtype=torch.float32)
+    assert G.read_device_errors() == 0
+    check_product(out, a, w, sizes, first, None, k)
