@@ -440,7 +440,9 @@ cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, con
     } else {
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
       int64_t parts;
-      constexpr int kPer = units_of<U>(32);
+      // 24 bytes a lane where units are narrow: 8192 tokens, 8 rows of 1027 bf16 37 us, with 32 bytes 49
+      // and 8 39; 3001 tokens, 5 rows of 1027 f32 12.5 us, with 32 bytes 13.1 and 16 14.6
+      constexpr int kPer = units_of<U>(sizeof(U) == 16 ? 32 : 24);
       const unsigned grid = row_grid(tokens, units, kPer, &parts);
       if (grid == 0) return cudaErrorInvalidConfiguration;
       // rows on their way at once, by how many a token has
@@ -463,9 +465,10 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
       // 32 bytes a thread and 4 rows at once; 16 and 2 where units are narrow, whose many registers
       // would leave few threads (3001 tokens, 5 rows of 1027 f32: 33 us, with 32 and 4 49 us;
-      // 8192 tokens, 2 rows of 4096 bf16: 59 us, with 16 and 2 66 us)
+      // 8192 tokens, 2 rows of 4096 bf16: 59 us, with 16 and 2 66 us); 12 of the narrowest (8 rows of
+      // 1027 bf16: 106 us, with 16 111 and with 4 175)
       constexpr bool kWide = sizeof(U) == 16;
-      constexpr int kPer = units_of<U>(kWide ? 32 : 16);
+      constexpr int kPer = units_of<U>(kWide ? 32 : sizeof(U) == 2 ? 12 : 16);
       const int64_t lanes = (units + kPer - 1) / kPer;
       const int threads = lanes >= kBackThreads ? kBackThreads : int((lanes + 31) / 32 * 32);
       auto kern = kWide && topk > 2 ? combine_backward_kernel<U, T, kPer, 4> : combine_backward_kernel<U, T, kPer, 2>;
