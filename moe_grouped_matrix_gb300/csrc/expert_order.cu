@@ -208,16 +208,18 @@ struct Unit {
     for (int i = 0; i < kN; ++i) f[i] = float(t[i]);
   }
   static __device__ __forceinline__ U pack(const float (&f)[kN]) {
-    T t[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if constexpr (std::is_same<T, float>::value)
-        t[i] = f[i];
-      else
-        t[i] = __float2bfloat16_rn(f[i]);
-    }
     U u;
-    memcpy(&u, t, sizeof(U));
+    if constexpr (std::is_same<T, float>::value) {
+      memcpy(&u, f, sizeof(U));
+    } else if constexpr (kN == 1) {
+      const T t = __float2bfloat16_rn(f[0]);
+      memcpy(&u, &t, sizeof(U));
+    } else {
+      __nv_bfloat162 t[kN / 2];
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) t[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      memcpy(&u, t, sizeof(U));
+    }
     return u;
   }
 };
@@ -319,41 +321,51 @@ __global__ void __launch_bounds__(kThreads)
     if (c0 + 32 * i < units) out[t * units + c0 + 32 * i] = Unit<U, T>::pack(acc[i]);
 }
 
-constexpr int kBackThreads = 512;
+// The sums over the warp of two values, a's in the lower half of the lanes and b's in the upper: the halves
+// exchange what they do not go on with.
+__device__ __forceinline__ float warp_sums(float a, float b, int lane) {
+  const bool high = lane & 16;
+  float v = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+  for (int k = 8; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+  return v;
+}
 
-// One CTA for each token: its warps share the row's columns; their parts of the
-// dot products are summed in warp order.
-template <class U, class T, int kPer, int kBatch>
-__global__ void __launch_bounds__(kBackThreads)
-    combine_backward_kernel(const U* __restrict__ dout, const U* __restrict__ in, int64_t tokens, int64_t units,
+// One CTA for each token: its warps share the row's columns, 32 * kPer consecutive
+// ones at a time; their parts of the dot products are summed in warp order.  Two
+// of the token's rows are on their way at once.  Bound by memory and, of narrow
+// units, by the instructions a unit takes: columns that are all there are not
+// asked for one by one (8192 tokens, 2 rows of 4096 bf16: 53 us for 50; with 512
+// threads, and four rows at once of more than two, 59; 4096 tokens, 8 rows of
+// 2048: 45 for 42, with those 50; 2000 tokens, 6 rows of 7168: 60 for 55, with
+// those 85; 3001 tokens, 5 rows of 1027 f32: 29 for 20, with those 32).
+template <class U, class T, int kPer, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps)
+    combine_backward_kernel(const U* __restrict__ dout, const U* __restrict__ in, int64_t tokens, uint32_t units,
                             int32_t topk,
                             const int32_t* __restrict__ rows, const int32_t* __restrict__ source,
                             const float* __restrict__ weights, U* __restrict__ din, float* __restrict__ dweights) {
   griddep_begin();
   dout = after_begin(dout), in = after_begin(in), rows = after_begin(rows), source = after_begin(source);
   weights = after_begin(weights);
-  constexpr int N = Unit<U, T>::kN;
-  __shared__ float part[kBackThreads / 32][GMM_MAX_TOPK];
+  constexpr int N = Unit<U, T>::kN, kBatch = 2;
+  __shared__ float part[kWarps][GMM_MAX_TOPK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x;
   const int32_t r = lane < topk ? slot_row(rows, t * topk + lane, tokens * topk) : -1;
   const int32_t s = lane < topk ? __ldg(source + t * topk + lane) : 0;
   const float g = lane < topk ? __ldg(weights + t * topk + lane) : 0.f;
+  const uint32_t gone = __ballot_sync(0xffffffffu, s < 0);  // rows of these numbers are past the groups
   part[warp][lane] = 0.f;
   __syncwarp();
-  const int threads = blockDim.x;
-  for (int64_t base = 0; base < units; base += threads * kPer) {
-    const int64_t c0 = base + threadIdx.x;
+  // A warp's 32 * kPer columns from c0 - lane on, all of them the row's (kFull) or not.
+  auto columns = [&](uint32_t c0, auto full) {
+    constexpr bool kFull = decltype(full)::value;
     float d[kPer][N];
+    const U* pd = dout + t * units + c0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (c0 + threads * i < units) {
-        Unit<U, T>::unpack(__ldg(dout + t * units + c0 + threads * i), d[i]);
-      } else {
-#pragma unroll
-        for (int n = 0; n < N; ++n) d[i][n] = 0.f;
-      }
-    }
+    for (int i = 0; i < kPer; ++i)
+      Unit<U, T>::unpack(kFull || c0 + 32 * i < units ? __ldg(pd + 32 * i) : zero_unit<U>(), d[i]);
     for (int j0 = 0; j0 < topk; j0 += kBatch) {
       U got[kBatch][kPer];
       int32_t row[kBatch];
@@ -361,45 +373,48 @@ __global__ void __launch_bounds__(kBackThreads)
       for (int q = 0; q < kBatch; ++q) {
         const int32_t from = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
         row[q] = j0 + q < topk ? from : -1;
+        const U* p = in + int64_t(row[q]) * units + c0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          got[q][i] = row[q] >= 0 && c0 + threads * i < units ? __ldg(in + row[q] * units + c0 + threads * i)
-                                                              : zero_unit<U>();
+          got[q][i] = row[q] >= 0 && (kFull || c0 + 32 * i < units) ? __ldg(p + 32 * i) : zero_unit<U>();
       }
       float sum[kBatch];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const float gj = __shfl_sync(0xffffffffu, g, (j0 + q) & 31);
-        const bool gone = __shfl_sync(0xffffffffu, s, (j0 + q) & 31) < 0 && j0 + q < topk;
         sum[q] = 0.f;
+        U* p = din + int64_t(row[q]) * units + c0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           float f[N], o[N];
           Unit<U, T>::unpack(got[q][i], f);
 #pragma unroll
           for (int n = 0; n < N; ++n) sum[q] = fmaf(d[i][n], f[n], sum[q]), o[n] = gj * d[i][n];
-          if (c0 + threads * i < units) {
-            if (row[q] >= 0) din[row[q] * units + c0 + threads * i] = Unit<U, T>::pack(o);
-            if (gone) din[(t * topk + j0 + q) * units + c0 + threads * i] = zero_unit<U>();
-          }
+          if (row[q] >= 0 && (kFull || c0 + 32 * i < units)) p[32 * i] = Unit<U, T>::pack(o);
         }
       }
-#pragma unroll
-      for (int k = 16; k; k >>= 1)
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], k);
-      if (lane == 0) {
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-          if (row[q] >= 0) part[warp][j0 + q] += sum[q];
-      }
+      const float all = warp_sums(sum[0], sum[1], lane);
+      const int j = j0 + lane / 16;
+      if (lane % 16 == 0 && j < topk) part[warp][j] += all;
     }
+    for (uint32_t left = gone; left != 0; left &= left - 1) {
+      U* p = din + (t * topk + __ffs(left) - 1) * units + c0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kFull || c0 + 32 * i < units) p[32 * i] = zero_unit<U>();
+    }
+  };
+  for (uint32_t c0 = warp * (32 * kPer); c0 < units; c0 += blockDim.x * kPer) {
+    if (c0 + 32 * kPer <= units)
+      columns(c0 + lane, std::true_type{});
+    else
+      columns(c0 + lane, std::false_type{});
   }
   __syncthreads();
   if (int(threadIdx.x) < topk) {
     float sum = 0.f;
-    for (int w = 0; w < threads / 32; ++w) sum += part[w][threadIdx.x];
-    dweights[t * topk + threadIdx.x] = sum;
+    for (uint32_t w = 0; w < blockDim.x / 32; ++w) sum += part[w][threadIdx.x];
+    dweights[t * topk + threadIdx.x] = r >= 0 ? sum : 0.f;  // r is this slot's row; a dropped one's sum may be 0 * inf
   }
 }
 
@@ -463,18 +478,18 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
       return cudaErrorInvalidValue;
     } else {
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
-      // 32 bytes a thread and 4 rows at once; 16 and 2 where units are narrow, whose many registers
-      // would leave few threads (3001 tokens, 5 rows of 1027 f32: 33 us, with 32 and 4 49 us;
-      // 8192 tokens, 2 rows of 4096 bf16: 59 us, with 16 and 2 66 us); 12 of the narrowest (8 rows of
-      // 1027 bf16: 106 us, with 16 111 and with 4 175)
-      constexpr bool kWide = sizeof(U) == 16;
-      constexpr int kPer = units_of<U>(kWide ? 32 : sizeof(U) == 2 ? 12 : 16);
-      const int64_t lanes = (units + kPer - 1) / kPer;
-      const int threads = lanes >= kBackThreads ? kBackThreads : int((lanes + 31) / 32 * 32);
-      auto kern = kWide && topk > 2 ? combine_backward_kernel<U, T, kPer, 4> : combine_backward_kernel<U, T, kPer, 2>;
-      return launch_dependent(kern, unsigned(tokens), threads, 0, s, 1, static_cast<const U*>(dout),
-                              static_cast<const U*>(in), tokens, units, topk, rows, source, weights,
-                              static_cast<U*>(din), dweights);
+      // 32 bytes a thread, 16 where units are narrow (8192 tokens, 8 rows of 1030 bf16: 63 us, with 12 bytes
+      // 75 and with 24 69)
+      constexpr int kPer = units_of<U>(sizeof(U) == 16 ? 32 : 16);
+      // 4 warps a token leave the fewest idle at a token's ends; tokens that do not fill the SMs with them
+      // (8 CTAs of each of 152) have as many as the row has columns for, up to 16 (8 rows of 7168 bf16:
+      // 64 tokens 6 us, with four warps 14; 608 tokens 24, with four 29; 1216 tokens 49 with either)
+      const bool few = tokens <= 1216;
+      const int64_t warps = (units + 32 * kPer - 1) / (32 * kPer), most = few ? 16 : 4;
+      auto kern = few ? combine_backward_kernel<U, T, kPer, 16> : combine_backward_kernel<U, T, kPer, 4>;
+      return launch_dependent(kern, unsigned(tokens), 32 * unsigned(warps < most ? warps : most), 0, s, 1,
+                              static_cast<const U*>(dout), static_cast<const U*>(in), tokens, uint32_t(units), topk,
+                              rows, source, weights, static_cast<U*>(din), dweights);
     }
   });
 }

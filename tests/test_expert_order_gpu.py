@@ -241,3 +241,40 @@ def test_refusals():
         G.combine_backward(x.bfloat16(), rows, order, torch.zeros((4, 2), device=DEV))
     with pytest.raises(ValueError, match="contiguous"):
         G.combine(torch.zeros((8, 16), device=DEV)[:, :8], order)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,topk,experts,d", [(7, 3, 4, 20001), (40, 8, 16, 7168), (300, 2, 8, 515),
+                                                   (1216, 5, 8, 1026), (1217, 5, 8, 1027), (1300, 3, 8, 1028),
+                                                   (1500, 2, 8, 2056), (2000, 1, 8, 64), (2500, 7, 8, 129)])
+def test_gradients_of_few_and_of_many_tokens(tokens, topk, experts, d, dtype):
+    """A gradient row is w * dout rounded once; dweights within their bound, 0 for a dropped slot."""
+    e = choice(tokens, topk, experts, d, 0.1)
+    order = G.sort_by_expert(e.to(DEV), experts)
+    gen = torch.Generator(DEV).manual_seed(d)
+    rows = torch.randn((tokens * topk, d), generator=gen, device=DEV).to(dtype)
+    dout = torch.randn((tokens, d), generator=gen, device=DEV).to(dtype)
+    w = torch.rand((tokens, topk), generator=gen, device=DEV)
+    drows, dw = G.combine_backward(dout, rows, order, w)
+    kept = order.rows >= 0
+    want = torch.zeros_like(rows)
+    want[order.rows[kept].long()] = (w[..., None] * dout.float()[:, None])[kept].to(dtype)
+    assert torch.equal(drows, want)
+    at = order.rows.long().clamp_min(0)
+    for j in range(topk):
+        prod = dout.double() * rows[at[:, j]].double() * kept[:, j, None]
+        assert ((dw[:, j].double() - prod.sum(1)).abs() <= (d + 8) * 2.0 ** -24 * prod.abs().sum(1)).all()
+
+
+@pytest.mark.parametrize("d", [64, 99, 1030])
+def test_dropped_slots_have_no_gradient_whatever_dout_holds(d):
+    e = torch.full((4, 3), -1, dtype=torch.int32)
+    e[:, 1] = torch.tensor([0, 1, 1, 2])
+    order = G.sort_by_expert(e.to(DEV), 3)
+    rows = torch.ones((12, d), device=DEV)
+    dout = torch.ones((4, d), device=DEV)
+    dout[0, 0], dout[1, d - 1], dout[2, d // 2] = float("nan"), float("inf"), -float("inf")
+    drows, dw = G.combine_backward(dout, rows, order, torch.ones((4, 3), device=DEV))
+    assert (dw[:, [0, 2]] == 0).all()
+    assert torch.equal(dw[1:, 1], torch.tensor([float("inf"), -float("inf"), float(d)], device=DEV))
+    assert dw[0, 1].isnan() and (drows[4:] == 0).all()
