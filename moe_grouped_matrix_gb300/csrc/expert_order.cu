@@ -273,15 +273,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <class U, class T, int kPer, int kBatch>
-__global__ void __launch_bounds__(kThreads)
+template <class U, class T, int kPer, int kBatch, int kCta>
+__global__ void __launch_bounds__(kCta)
     combine_kernel(const U* __restrict__ in, int64_t tokens, int64_t units, int32_t topk, int64_t parts,
                    const int32_t* __restrict__ rows, const float* __restrict__ weights, U* __restrict__ out) {
   griddep_begin();
   in = after_begin(in), rows = after_begin(rows), weights = after_begin(weights);
   constexpr int N = Unit<U, T>::kN;
   const int lane = threadIdx.x & 31;
-  const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t w = int64_t(blockIdx.x) * (kCta / 32) + (threadIdx.x >> 5);
   const int64_t t = w / parts;
   if (t >= tokens) return;
   const int64_t c0 = (w - t * parts) * (32 * kPer) + lane;
@@ -436,10 +436,10 @@ int check(int dtype, int64_t tokens, int64_t d, int32_t topk) {
   return GMM_OK;
 }
 
-// Warps of `per` units a lane over every token's row, as a grid of kThreads-blocks; 0: too large.
-unsigned row_grid(int64_t tokens, int64_t units, int per, int64_t* parts) {
+// Warps of `per` units a lane over every token's row, as a grid of CTAs of so many threads; 0: too large.
+unsigned row_grid(int64_t tokens, int64_t units, int per, int threads, int64_t* parts) {
   *parts = (units + 32 * per - 1) / (32 * per);
-  const int64_t blocks = (tokens * *parts + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t blocks = (tokens * *parts + threads / 32 - 1) / (threads / 32);
   return blocks <= INT32_MAX ? unsigned(blocks) : 0u;
 }
 
@@ -455,15 +455,28 @@ cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, con
     } else {
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
       int64_t parts;
-      // 24 bytes a lane where units are narrow: 8192 tokens, 8 rows of 1027 bf16 37 us, with 32 bytes 49
-      // and 8 39; 3001 tokens, 5 rows of 1027 f32 12.5 us, with 32 bytes 13.1 and 16 14.6
-      constexpr int kPer = units_of<U>(sizeof(U) == 16 ? 32 : 24);
-      const unsigned grid = row_grid(tokens, units, kPer, &parts);
-      if (grid == 0) return cudaErrorInvalidConfiguration;
-      // rows on their way at once, by how many a token has
-      auto kern = topk <= 2 ? combine_kernel<U, T, kPer, 2> : combine_kernel<U, T, kPer, 4>;
-      return launch_dependent(kern, grid, kThreads, 0, s, 1, static_cast<const U*>(in), tokens, units, topk, parts, rows,
-                              weights, static_cast<U*>(out));
+      // Wide units: 32 bytes a lane, four rows at once of more than two; where the sums are many, 64 bytes, two
+      // rows and CTAs of two warps (8192 tokens, 2 rows of 4096 bf16 31.5 us, with 128 threads 33.5, as few
+      // tokens 34; 64 tokens, 4 rows of 2048 2.0 us in a graph, as many tokens 2.2; 8 MB lie between what
+      // gains and what loses).  Narrow units: 24 bytes, 128 threads (8192 tokens, 8 rows of 1027 bf16 37 us,
+      // with 32 bytes 49 and with 8 39; 3001 tokens, 5 rows of 1027 f32 12.5 us, with 32 bytes 13.1 and with
+      // 16 14.6; 8192 tokens, 2 rows of 2047 f32 32 us, with 64 threads 48).
+      auto go = [&](auto per, auto batch, auto threads) -> cudaError_t {
+        const unsigned grid = row_grid(tokens, units, per, threads, &parts);
+        if (grid == 0) return cudaErrorInvalidConfiguration;
+        return launch_dependent(combine_kernel<U, T, per, batch, threads>, grid, threads, 0, s, 1,
+                                static_cast<const U*>(in), tokens, units, topk, parts, rows, weights,
+                                static_cast<U*>(out));
+      };
+      constexpr std::integral_constant<int, units_of<U>(sizeof(U) == 16 ? 32 : 24)> per;
+      constexpr std::integral_constant<int, kThreads> threads;
+      constexpr std::integral_constant<int, 2> two;
+      constexpr std::integral_constant<int, 4> four;
+      if constexpr (sizeof(U) == 16) {
+        if (tokens * units >= (8 << 20) / 16)
+          return go(std::integral_constant<int, units_of<U>(64)>{}, two, std::integral_constant<int, 64>{});
+      }
+      return topk <= 2 ? go(per, two, threads) : go(per, four, threads);
     }
   });
 }
@@ -527,7 +540,7 @@ extern "C" int gmm_dispatch(const void* x, int dtype, int64_t tokens, int64_t d,
     const int64_t units = d * int64_t(el) / int64_t(sizeof(U));
     int64_t parts;
     constexpr int kPer = units_of<U>(32);
-    const unsigned grid = row_grid(tokens, units, kPer, &parts);
+    const unsigned grid = row_grid(tokens, units, kPer, kThreads, &parts);
     if (grid == 0) return cudaErrorInvalidConfiguration;
     return launch_dependent(dispatch_kernel<U, kPer>, grid, kThreads, 0, s, 1, static_cast<const U*>(x), tokens, units,
                             x_ld * int64_t(el) / int64_t(sizeof(U)), topk, parts, rows, source, static_cast<U*>(out));

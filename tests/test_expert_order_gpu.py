@@ -278,3 +278,24 @@ def test_dropped_slots_have_no_gradient_whatever_dout_holds(d):
     assert (dw[:, [0, 2]] == 0).all()
     assert torch.equal(dw[1:, 1], torch.tensor([float("inf"), -float("inf"), float(d)], device=DEV))
     assert dw[0, 1].isnan() and (drows[4:] == 0).all()
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("tokens,topk,d,dtype", [(2048, 3, 2048, torch.bfloat16), (2047, 3, 2048, torch.bfloat16),
+                                                 (2049, 1, 2056, torch.bfloat16), (6000, 5, 520, torch.float32),
+                                                 (1025, 6, 2052, torch.float32)])
+def test_sums_of_many_rows(tokens, topk, d, dtype, weighted):
+    """Around the size from which combine() takes longer runs of a row: a token's sum is the same chain,
+    to the bit, as in a call of few tokens."""
+    e = choice(tokens, topk, 16, d, 0.1)
+    order = G.sort_by_expert(e.to(DEV), 16)
+    gen = torch.Generator(DEV).manual_seed(d)
+    rows = torch.randn((tokens * topk, d), generator=gen, device=DEV).to(dtype)
+    w = torch.rand((tokens, topk), generator=gen, device=DEV) if weighted else None
+    got = G.combine(rows, order, w)
+    for t0 in (0, tokens // 2, tokens - 100):
+        few = G.sort_by_expert(e[t0:t0 + 100].to(DEV), 16)
+        kept = few.rows >= 0
+        part = torch.full((100 * topk, d), float("nan"), device=DEV, dtype=dtype)
+        part[few.rows[kept].long()] = rows[order.rows[t0:t0 + 100][kept].long()]
+        assert torch.equal(got[t0:t0 + 100], G.combine(part, few, w[t0:t0 + 100] if weighted else None))
