@@ -2,7 +2,11 @@
 against the layer of the values that its 4-bit operands stand for.
 
 Bounds.  The training step rounds to bf16 (2^-9 of a value) at each of its half a dozen intermediate
-tensors: 2^-5 of a gradient's norm is several times their sum.  The serving step's two quantisations
+tensors: 2^-5 of a gradient's norm is several times their sum.  The router's gradient is a difference,
+w_j (dw_j - sum_i w_i dw_i), which may all but cancel (of one token in particular); its roundings are
+those of its terms: each slot's dw is off by some 2^-9 of |dy o_j|, o_j the slot's output and the
+product taken by element, so there 2^-5 is of w_j (|dy o_j| + sum_i w_i |dy o_i|) times |x|, the root of
+the sum of its squares over slots and tokens.  The serving step's two quantisations
 of rows are those of the reference here except where an intermediate's rounding to bf16 moves a value
 across a code's half way: 2^-5 of the norm again."""
 
@@ -16,6 +20,11 @@ import moe_grouped_matrix_gb300 as G
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(autouse=True)
+def same_inputs():
+    torch.manual_seed(1)
 
 
 @pytest.fixture(scope="module")
@@ -43,8 +52,21 @@ def reference(x, router, wi, wo, experts, mask=None):
     return y
 
 
-def near(got, want, what):
-    off = (got.double() - want).norm() / want.norm()
+def router_size(x, router, wi, wo, experts, dy):
+    """The size of the terms that the router's gradient is the difference of (no slot dropped)."""
+    at = experts.long()
+    w = torch.softmax((x @ router.T).gather(1, at), dim=1)
+    s = torch.zeros_like(w)
+    for e in range(wi.shape[0]):
+        t, j = torch.nonzero(experts == e, as_tuple=True)
+        gate, up = (x[t] @ wi[e].T).chunk(2, dim=1)
+        s[t, j] = (dy[t] * ((torch.nn.functional.silu(gate) * up) @ wo[e].T)).norm(dim=1)
+    size = w * (s + (w * s).sum(1, keepdim=True))
+    return (size.square().sum(1) * x.square().sum(1)).sum().sqrt()
+
+
+def near(got, want, what, size=None):
+    off = (got.double() - want).norm() / (want.norm() if size is None else size)
     assert off < 2.0 ** -5, (what, float(off))
 
 
@@ -62,8 +84,11 @@ def test_training_step(example, tokens, experts, d, f, topk):
     want = reference(*leaves, saved[3])
     near(y, want.detach(), "y")
     want.backward(dy.double())
-    for got, leaf, what in zip((dx, grads["router"], grads["wi"], grads["wo"]), leaves, ("dx", "router", "wi", "wo")):
+    for got, leaf, what in zip((dx, grads["wi"], grads["wo"]), (leaves[0], *leaves[2:]), ("dx", "wi", "wo")):
         near(got, leaf.grad, what)
+    kept = mask.nonzero()[:, 0]
+    size = router_size(leaves[0].detach()[kept], *(t.detach() for t in leaves[1:]), saved[3][kept], dy.double()[kept])
+    near(grads["router"], leaves[1].grad, "router", size)
     assert G.read_device_errors() == 0
 
 
