@@ -321,25 +321,27 @@ __global__ void __launch_bounds__(kCta)
     if (c0 + 32 * i < units) out[t * units + c0 + 32 * i] = Unit<U, T>::pack(acc[i]);
 }
 
-// The sums over the warp of two values, a's in the lower half of the lanes and b's in the upper: the halves
-// exchange what they do not go on with.
-__device__ __forceinline__ float warp_sums(float a, float b, int lane) {
-  const bool high = lane & 16;
-  float v = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+// The sums over the warp of one or two values: of two, the first in the lower half of the lanes and the
+// second in the upper, as the halves exchange what they do not go on with.
+template <int kBatch>
+__device__ __forceinline__ float warp_sums(const float (&sum)[kBatch], int lane) {
+  static_assert(kBatch == 1 || kBatch == 2);
+  const bool high = kBatch == 2 && (lane & 16);
+  float v = (high ? sum[kBatch - 1] : sum[0]) + __shfl_xor_sync(0xffffffffu, high ? sum[0] : sum[kBatch - 1], 16);
 #pragma unroll
   for (int k = 8; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
   return v;
 }
 
 // One CTA for each token: its warps share the row's columns, 32 * kPer consecutive
-// ones at a time; their parts of the dot products are summed in warp order.  Two
-// of the token's rows are on their way at once.  Bound by memory and, of narrow
-// units, by the instructions a unit takes: columns that are all there are not
-// asked for one by one (8192 tokens, 2 rows of 4096 bf16: 53 us for 50; with 512
-// threads, and four rows at once of more than two, 59; 4096 tokens, 8 rows of
-// 2048: 45 for 42, with those 50; 2000 tokens, 6 rows of 7168: 60 for 55, with
-// those 85; 3001 tokens, 5 rows of 1027 f32: 29 for 20, with those 32).
-template <class U, class T, int kPer, int kWarps>
+// ones at a time; their parts of the dot products are summed in warp order.
+// kBatch of the token's rows are on their way at once.  Bound by memory and, of
+// narrow units, by the instructions a unit takes: columns that are all there are
+// not asked for one by one (8192 tokens, 2 rows of 4096 bf16: 53 us for 50; 4096
+// tokens, 8 rows of 2048: 45 for 42; 2000 tokens, 6 rows of 7168: 60 for 55; 3001
+// tokens, 5 rows of 1027 f32: 27 for 20; a first form, 512 threads with strided
+// columns, took 59, 50, 85 and 32).
+template <class U, class T, int kPer, int kBatch, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
     combine_backward_kernel(const U* __restrict__ dout, const U* __restrict__ in, int64_t tokens, uint32_t units,
                             int32_t topk,
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   griddep_begin();
   dout = after_begin(dout), in = after_begin(in), rows = after_begin(rows), source = after_begin(source);
   weights = after_begin(weights);
-  constexpr int N = Unit<U, T>::kN, kBatch = 2;
+  constexpr int N = Unit<U, T>::kN;
   __shared__ float part[kWarps][GMM_MAX_TOPK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x;
@@ -393,9 +395,9 @@ __global__ void __launch_bounds__(32 * kWarps)
           if (row[q] >= 0 && (kFull || c0 + 32 * i < units)) p[32 * i] = Unit<U, T>::pack(o);
         }
       }
-      const float all = warp_sums(sum[0], sum[1], lane);
-      const int j = j0 + lane / 16;
-      if (lane % 16 == 0 && j < topk) part[warp][j] += all;
+      const float all = warp_sums<kBatch>(sum, lane);
+      const int j = j0 + lane / (32 / kBatch);
+      if (lane % (32 / kBatch) == 0 && j < topk) part[warp][j] += all;
     }
     for (uint32_t left = gone; left != 0; left &= left - 1) {
       U* p = din + (t * topk + __ffs(left) - 1) * units + c0;
@@ -491,15 +493,21 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
       return cudaErrorInvalidValue;
     } else {
       const int64_t units = d * int64_t(sizeof(T)) / int64_t(sizeof(U));
-      // 32 bytes a thread, 16 where units are narrow (8192 tokens, 8 rows of 1030 bf16: 63 us, with 12 bytes
-      // 75 and with 24 69)
-      constexpr int kPer = units_of<U>(sizeof(U) == 16 ? 32 : 16);
+      // 32 bytes a thread, two rows at once where there are two (8192 tokens, 2 rows of 4096 bf16 53 us, one
+      // at once 54.5; 2000 tokens, 6 rows of 7168 60 and 67; 8192 tokens, one row of 2048 21 and 19).  Narrow
+      // units: one row, 24 bytes, 16 of 2-byte units (8192 tokens, 8 rows of 1030 bf16 50 us, with 16 bytes
+      // 66, with 32 68, two rows of 16 63; 8 rows of 1027 72, with 32 bytes 81, two rows of 16 83).
+      constexpr bool kWide = sizeof(U) == 16;
+      constexpr int kPer = units_of<U>(kWide ? 32 : sizeof(U) == 2 ? 16 : 24);
       // 4 warps a token leave the fewest idle at a token's ends; tokens that do not fill the SMs with them
       // (8 CTAs of each of 152) have as many as the row has columns for, up to 16 (8 rows of 7168 bf16:
       // 64 tokens 6 us, with four warps 14; 608 tokens 24, with four 29; 1216 tokens 49 with either)
       const bool few = tokens <= 1216;
       const int64_t warps = (units + 32 * kPer - 1) / (32 * kPer), most = few ? 16 : 4;
-      auto kern = few ? combine_backward_kernel<U, T, kPer, 16> : combine_backward_kernel<U, T, kPer, 4>;
+      auto kern = few ? combine_backward_kernel<U, T, kPer, 1, 16> : combine_backward_kernel<U, T, kPer, 1, 4>;
+      if constexpr (kWide) {
+        if (topk > 1) kern = few ? combine_backward_kernel<U, T, kPer, 2, 16> : combine_backward_kernel<U, T, kPer, 2, 4>;
+      }
       return launch_dependent(kern, unsigned(tokens), 32 * unsigned(warps < most ? warps : most), 0, s, 1,
                               static_cast<const U*>(dout), static_cast<const U*>(in), tokens, uint32_t(units), topk,
                               rows, source, weights, static_cast<U*>(din), dweights);
