@@ -175,7 +175,12 @@ cudaError_t launch_sort_as(const int32_t* experts, int32_t slots, int32_t num_ex
   while ((1 << bits) <= num_experts) ++bits;
   auto kern = sort_kernel<kWarps>;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // A launch may use 48 KB unasked, its static shared memory (under 1 KB here) among them.  The setting is
+  // the kernel's, not the launch's: always the most that any call needs, so that no call takes from another
+  // thread's what that one has just been allowed.
+  constexpr size_t kMost = size_t(kWarps + kSortCluster + 1) * (GMM_MAX_GROUPS + 1) * sizeof(uint32_t);
+  static_assert(kMost <= 226 * 1024, "shared memory budget");
+  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
   if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   const int64_t warps = int64_t(ctas) * kWarps;
