@@ -102,16 +102,17 @@ struct Shape {
   static constexpr uint32_t OFF_ACCF = OFF_SEMPTY + 8 * kScales;
   static constexpr uint32_t OFF_ACCE = OFF_ACCF + 16;
   static constexpr uint32_t OFF_DONE = OFF_ACCE + 16;
-  static constexpr uint32_t OFF_REPORT = OFF_DONE + 8;  // pair_report's barrier and count (leader's)
-  static constexpr uint32_t OFF_RWORD = OFF_REPORT + 8;
-  static constexpr uint32_t OFF_TMEM = OFF_RWORD + 4;
+  static constexpr uint32_t OFF_TMEM = OFF_DONE + 8;
   static constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
-  static constexpr uint32_t OFF_SIGNAL = (OFF_ABORT + 4 + 15) / 16 * 16;  // 16 bytes, see signal_leader
+  static constexpr uint32_t OFF_UNWIND = OFF_ABORT + 4;  // the follower's: the leader has given up
+  static constexpr uint32_t OFF_ISSUED = OFF_UNWIND + 4; // stages whose codes this CTA's copies were issued for
+  static constexpr uint32_t OFF_TURNS = OFF_ISSUED + 4;  // times each window of scales has been turned
+  static constexpr uint32_t OFF_SIGNAL = (OFF_TURNS + 4 * kScales + 15) / 16 * 16;  // 16 bytes, see signal_leader
   static constexpr uint32_t OFF_OFFS = OFF_CTRL + 512;
   static constexpr uint32_t OFF_TILES = OFF_OFFS + 4 * (kMaxGroups + 4);
   static constexpr uint32_t SMEM_BYTES = OFF_TILES + 4 * (kMaxGroups + 4) + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(OFF_SIGNAL + 16 <= OFF_OFFS && OFF_REPORT % 8 == 0, "control block overlaps the tables");
+  static_assert(OFF_SIGNAL + 16 <= OFF_OFFS, "control block overlaps the tables");
   static_assert(B_BYTES % 1024 == 0 && OFF_SF % 1024 == 0, "swizzle atoms");
   static_assert(TM_SFB + (kPair ? 32 : 16) <= kColumns, "tensor memory budget");
 };
@@ -290,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   const bool leader = rank == 0;
   const int32_t pair = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int32_t npairs = kPair ? gridDim.x >> 1 : gridDim.x;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_ABORT);
+  auto word = [&](uint32_t off) { return reinterpret_cast<volatile uint32_t*>(smem + off); };
+  volatile uint32_t* abort_flag = word(S::OFF_ABORT);
   int32_t* offs = reinterpret_cast<int32_t*>(smem + S::OFF_OFFS);
   int32_t* tiles = reinterpret_cast<int32_t*>(smem + S::OFF_TILES);
   auto full_bar = [&](uint32_t s) { return sbase + S::OFF_FULL + 8 * s; };
@@ -318,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       mbar_init(acce_bar(b), 8 * S::kCtas);  // one lane of each epilogue warp
     }
     mbar_init(done_bar, 1);
-    mbar_init(sbase + S::OFF_REPORT, 1);
     *abort_flag = 0u;
+    *word(S::OFF_UNWIND) = 0u;
+    for (int s = 0; s < kScales; ++s) word(S::OFF_TURNS)[s] = 0u;
     fence_mbar_init();
     tma_prefetch(&maps.rhs);
     tma_prefetch(&maps.lhs16);
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
-  const uint32_t tmem_base = uniform(*reinterpret_cast<volatile uint32_t*>(smem + S::OFF_TMEM));
+  const uint32_t tmem_base = uniform(*word(S::OFF_TMEM));
 
   const int32_t t_tiles = uniform(tiles[p.num_local_groups]);
   const int32_t n_tiles = (p.n + S::kTileW - 1) / S::kTileW;
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   // bytes of one CTA's copies of codes in a stage of tile t
   auto code_bytes = [&](const GemmTile& t) { return A_BYTES + uint32_t(chunk_n(t) / S::kCtas) * ROW_BYTES; };
 
-  uint32_t issued = 0;  // codes: stages of the sequence this CTA issued (leader: armed)
+  uint32_t issued = 0;  // warps that copy: stages of the sequence whose copies were issued (and armed)
   if (warp == 0) {
     // ---------------------------------------------------------------- copies of codes (both CTAs)
     uint32_t stage = 0, phase = 0;
@@ -434,12 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         }
       }
     }
-    if constexpr (kPair) {
-      if (!leader && lane == 0) pair_report(sbase + S::OFF_REPORT, sbase + S::OFF_RWORD, issued);
-    } else if (!ok) {  // the copies in flight: the last kStages at most
-      for (uint32_t i = issued > kStages ? issued - kStages : 0u; i < issued; ++i)
-        drain_bar(full_bar(i % kStages), (i / kStages) & 1u);
-    }
+    if (kPair && lane == 0) *word(S::OFF_ISSUED) = issued;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (leader) {
@@ -515,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- copies of scales (both CTAs)
-    uint32_t stage = 0, phase = 0, mine = 0;
+    uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int32_t item = 0; item < items && ok; ++item) {
       const GemmTile t = tile_of(item);
@@ -537,25 +535,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
           bulk_load(dst + SF_BYTES, b_src + win * p.m * 16, b_bytes, sfull_bar(stage));
         }
         __syncwarp();
-        ++mine;
+        ++issued;
         if (++stage == kScales) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    if (!ok) {
-      for (uint32_t i = mine > kScales ? mine - kScales : 0u; i < mine; ++i)
-        drain_bar(sfull_bar(i % kScales), (i / kScales) & 1u);
-    }
   } else if (warp > 10) {
     // ---------------------------------------------------------------- scales into the MMA's order (both CTAs)
     const int64_t stages = int64_t(items) * k_blocks;
     // A warp has stages of its own: a parity wait tells a phase from the one before it only, so
     // whoever waits on a barrier has to have seen each of its phases.
-    uint32_t phase = 0;
+    uint32_t phase = 0, turns = 0;
     bool ok = true;
     for (int64_t i0 = 0; i0 < stages && ok; i0 += kScales, phase ^= 1u) {
+      ++turns;
       for (int32_t stage = warp - 11; stage < kScales && i0 + stage < stages; stage += kTurners) {
         if (!wait_warp(sfull_bar(stage), phase, abort_flag, p.err)) {
           ok = false;
@@ -571,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             mbar_arrive_expect_tx(turned_bar(stage), kSignalBytes);
           else
             signal_leader(sbase + S::OFF_SIGNAL, turned_bar(stage));
+          if (kPair) word(S::OFF_TURNS)[stage] = turns;
         }
       }
     }
@@ -705,16 +701,44 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) {
-    if (leader && warp == 0 && lane == 0 && *abort_flag) {
-      st_shared_cluster_u32(mapa_shared(sbase + S::OFF_ABORT, 1), 1u);  // the follower's waits end too
-      // stage i of the sequence belongs to the pair's (i / k_blocks)-th item
-      pair_drain<kStages>(full_bar(0), sbase + S::OFF_REPORT, sbase + S::OFF_RWORD, issued, kWaitLimitCycles,
-                          [&](uint32_t i) {
-                            return code_bytes(lane_tile(int32_t(i / uint32_t(k_blocks))));
-                          });
+  // Every role has ended.  If a wait of this CTA gave up, copies may be in flight that nobody waited for, its
+  // own producers' or not: the last kScales of scales, which are this CTA's affair alone, and the last kStages
+  // of codes.  (Where none gave up, each copy has been waited for by the warp that it was made for.)
+  const bool gave_up = *abort_flag != 0u;
+  if (gave_up && warp == 10 && lane == 0) {
+    for (uint32_t i = issued > kScales ? issued - kScales : 0u; i < issued; ++i)
+      drain_bar(sfull_bar(i % kScales), (i / kScales) & 1u);
+  }
+  if constexpr (!kPair) {
+    if (gave_up && warp == 0 && lane == 0) {
+      for (uint32_t i = issued > kStages ? issued - kStages : 0u; i < issued; ++i)
+        drain_bar(full_bar(i % kStages), (i / kStages) & 1u);
     }
-    cluster_sync();  // the leader's MMAs and every copy are done; no signal targets either CTA any more
+  } else {
+    if (leader && gave_up && threadIdx.x == 0) {
+      st_shared_cluster_u32(mapa_shared(sbase + S::OFF_UNWIND, 1), 1u);
+      st_shared_cluster_u32(mapa_shared(sbase + S::OFF_ABORT, 1), 1u);  // the follower's waits end too
+    }
+    cluster_sync();  // the roles of both CTAs have ended, the leader's MMAs are done, and both know of `unwind`
+    // A follower that gave up leaves the leader's MMA warp a stage, or an accumulator that it asks for, short
+    // unless that one is done, so the leader's giving up is what counts.  Then the codes of both CTAs and the
+    // follower's signals are settled at the leader's barriers before either CTA may end.
+    if (leader ? gave_up : *word(S::OFF_UNWIND) != 0u) {
+      if (leader && threadIdx.x == 0) {
+        auto peer = [&](uint32_t off) { return ld_shared_cluster_u32(mapa_shared(sbase + off, 1)); };
+        // stage i of the sequence belongs to the pair's (i / k_blocks)-th item
+        pair_settle<kStages>(full_bar(0), peer(S::OFF_ISSUED), issued, [&](uint32_t i) {
+          return code_bytes(lane_tile(int32_t(i / uint32_t(k_blocks))));
+        });
+        for (uint32_t s = 0; s < kScales; ++s) {
+          // The follower is a turn ahead at most: the next needs an MMA after the leader's.
+          const uint32_t turns = peer(S::OFF_TURNS + 4 * s);
+          if (turns > word(S::OFF_TURNS)[s]) mbar_arrive_expect_tx(turned_bar(s), kSignalBytes);
+          if (turns > 0) drain_bar(turned_bar(s), (turns - 1) & 1u);
+        }
+      }
+      cluster_sync();
+    }
   }
   if (warp == 1) {
     tc_fence_after();

@@ -483,6 +483,13 @@ __device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v)
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// 4-byte load of the same.
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Takes `bytes` off the transaction count of this CTA's mbarrier, as if copies of
 // that many bytes had landed.
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
@@ -510,8 +517,24 @@ __device__ __forceinline__ void pair_report(uint32_t report_bar, uint32_t report
   mbar_arrive_cluster(mapa_shared(report_bar, 0));  // release: the count is visible first
 }
 
-// `follower_bytes(i)`: the bytes the follower's copies of stage i of the sequence
-// carry (i counts from 0); `armed`: stages the leader armed.
+// Settles them, once both counts are known.  `issued`: stages the follower issued;
+// `armed`: stages the leader armed; `follower_bytes(i)`: the bytes the follower's
+// copies of stage i of the sequence carry (i counts from 0).
+template <int kStages, class FollowerBytes>
+__device__ __forceinline__ void pair_settle(uint32_t full_bar0, uint32_t issued, uint32_t armed,
+                                            FollowerBytes follower_bytes) {
+  const uint32_t hi = armed > issued ? armed : issued;
+  for (uint32_t i = hi > uint32_t(kStages) ? hi - kStages : 0u; i < hi; ++i) {
+    const uint32_t bar = full_bar0 + 8u * (i % kStages);
+    if (i >= armed)
+      mbar_arrive_expect_tx(bar, follower_bytes(i));
+    else if (i >= issued)
+      mbar_complete_tx(bar, follower_bytes(i));
+    drain_bar(bar, (i / kStages) & 1u);
+  }
+}
+
+// Takes the follower's report and settles.
 template <int kStages, class FollowerBytes>
 __device__ __forceinline__ void pair_drain(uint32_t full_bar0, uint32_t report_bar, uint32_t report_word,
                                            uint32_t armed, long long limit, FollowerBytes follower_bytes) {
@@ -522,15 +545,7 @@ __device__ __forceinline__ void pair_drain(uint32_t full_bar0, uint32_t report_b
   }
   if (mbar_test_wait_cluster(report_bar, 0))
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(issued) : "r"(report_word) : "memory");
-  const uint32_t hi = armed > issued ? armed : issued;
-  for (uint32_t i = hi > uint32_t(kStages) ? hi - kStages : 0u; i < hi; ++i) {
-    const uint32_t bar = full_bar0 + 8u * (i % kStages);
-    if (i >= armed)
-      mbar_arrive_expect_tx(bar, follower_bytes(i));
-    else if (i >= issued)
-      mbar_complete_tx(bar, follower_bytes(i));
-    drain_bar(bar, (i / kStages) & 1u);
-  }
+  pair_settle<kStages>(full_bar0, issued, armed, follower_bytes);
 }
 
 // ------------------------------------------------------------------ misc
