@@ -232,8 +232,8 @@ typedef struct gmm_options {
  *   rhs_bias     NULL or device [num_local_groups, 1, n] of bias_dtype (BF16 or F32).
  *   out          [m, n] of out_dtype (BF16 or F32).
  *   Sizes: m >= 0, k >= 8, n >= 8, k % 8 == 0, n % 8 == 0 (16-byte rows); lhs, rhs,
- *   out and bias 16-byte aligned (E2M1 rhs 32-byte aligned).  Row counts and offsets must fit
- *   in int32.
+ *   out and bias 16-byte aligned (E2M1 rhs 32-byte aligned).  m, k and n are at most
+ *   2^31 - 1024.
  *   Returns GMM_OK or an error status above.
  */
 int gmm(const void* lhs, int lhs_dtype, int64_t m, int64_t k, const void* rhs, int rhs_dtype,
@@ -358,7 +358,8 @@ int gmm_ex(const void* lhs, int lhs_dtype, const float* lhs_scale, int32_t num_l
  *
  *   lhs    [m, k] BF16;  dout [m, n] BF16;  out [num_groups, k, n] F32 or BF16.
  *   group_sizes device int32 [num_groups], 1 <= num_groups <= GMM_MAX_GROUPS.
- *   Sizes: m >= 0, k % 8 == 0, n % 8 == 0, k, n >= 8; pointers 16-byte aligned.
+ *   Sizes: m >= 0, k % 8 == 0, n % 8 == 0, k, n >= 8, each at most 2^31 - 1024; pointers
+ *   16-byte aligned.
  *   Two kernels give the same results within the bound: one SM per 128 x 256
  *   output tile (default) and SM pairs on 256 x 256 tiles (tgmm_ex() with
  *   options.tgmm_kernel chooses).

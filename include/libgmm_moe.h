@@ -155,7 +155,8 @@ int gmm_dequantize_fp4(const void* codes, const void* block_scale, const float* 
  * with fp32 sums and one rounding to out_dtype; every other row of out is zero, as in gmm().
  * Both operands have the same format.
  *   lhs_*      [m, k] quantised rows;  rhs_*  [num_local_groups][n, k] quantised weights
- *   k % 32 == 0, n % 8 == 0; codes, block scales and out 16-byte aligned
+ *   k % 32 == 0, n % 8 == 0; m, k and n at most 2^31 - 1024; codes, block scales and out
+ *   16-byte aligned
  *   group_sizes, group offset, bias, workspace and stream as in gmm().
  */
 int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const float* lhs_row_scale, int64_t m, int64_t k,

@@ -21,9 +21,6 @@
 namespace gmmk {
 namespace {
 
-// Slots of an order: a step past the last still fits in int32.
-constexpr int64_t kMaxSlots = int64_t(INT32_MAX) - 1023;
-
 // The row of a slot as a call is given it; anything that is no row of the order counts as dropped.
 __device__ __forceinline__ int32_t slot_row(const int32_t* rows, int64_t slot, int64_t slots) {
   const int32_t r = __ldg(rows + slot);
@@ -438,7 +435,7 @@ uint64_t address(const void* p) { return uint64_t(reinterpret_cast<uintptr_t>(p)
 
 int check(int dtype, int64_t tokens, int64_t d, int32_t topk) {
   if (dtype != GMM_DTYPE_BF16 && dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
-  if (tokens < 0 || d < 1 || d > INT32_MAX || topk < 1 || topk > GMM_MAX_TOPK || tokens > kMaxSlots / topk)
+  if (tokens < 0 || d < 1 || d > INT32_MAX || topk < 1 || topk > GMM_MAX_TOPK || tokens > kMaxSize / topk)
     return GMM_ERR_SHAPE;
   return GMM_OK;
 }

@@ -802,7 +802,7 @@ extern "C" int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const
   const bool nv = format == GMM_FP4_NVFP4;
   if (out_dtype != GMM_DTYPE_BF16 && out_dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
   if (rhs_bias != nullptr && bias_dtype != GMM_DTYPE_BF16 && bias_dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
-  if (m < 0 || m > INT32_MAX || k < 32 || k > INT32_MAX || k % 32 != 0 || n < 8 || n > INT32_MAX || n % 8 != 0)
+  if (m < 0 || m > kMaxSize || k < 32 || k > kMaxSize || k % 32 != 0 || n < 8 || n > kMaxSize || n % 8 != 0)
     return GMM_ERR_SHAPE;
   if (num_total_groups < 1 || num_total_groups > GMM_MAX_GROUPS || num_local_groups < 1 ||
       num_local_groups > num_total_groups)

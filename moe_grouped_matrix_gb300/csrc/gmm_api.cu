@@ -142,7 +142,7 @@ int make_map_e2m1(CUtensorMap* map, const void* base, int64_t k, int64_t n, int6
   return GMM_OK;
 }
 
-bool fits_i32(int64_t v) { return v >= 0 && v <= INT32_MAX; }
+bool size_ok(int64_t v) { return v >= 0 && v <= gmmk::kMaxSize; }
 
 // The bf16 forward kernels:
 //   kPair     256 x 256 tiles of rows x n on SM pairs: the fastest per MMA, but
@@ -335,7 +335,7 @@ int gmm_impl(const void* lhs, int lhs_dtype, int64_t m, int64_t k, const void* r
   const bool quantized = rhs_dtype != GMM_DTYPE_BF16;
   const bool packed4 = rhs_dtype == GMM_DTYPE_INT4 || rhs_dtype == GMM_DTYPE_UINT4 || rhs_dtype == GMM_DTYPE_E2M1;
   if (quantized && !transpose_rhs) return GMM_ERR_DTYPE;
-  if (!fits_i32(m) || !fits_i32(k) || !fits_i32(n) || k < 8 || n < 8 || k % 8 != 0 || n % 8 != 0)
+  if (!size_ok(m) || !size_ok(k) || !size_ok(n) || k < 8 || n < 8 || k % 8 != 0 || n % 8 != 0)
     return GMM_ERR_SHAPE;
   if (num_total_groups < 1 || num_total_groups > GMM_MAX_GROUPS || num_local_groups < 1 ||
       num_local_groups > num_total_groups)
@@ -779,7 +779,7 @@ int tgmm_ex(const void* lhs, int lhs_dtype, const void* dout, int dout_dtype, in
   if (lhs == nullptr || dout == nullptr || group_sizes == nullptr || out == nullptr) return GMM_ERR_NULL;
   if (lhs_dtype != GMM_DTYPE_BF16 || dout_dtype != GMM_DTYPE_BF16) return GMM_ERR_DTYPE;
   if (out_dtype != GMM_DTYPE_BF16 && out_dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
-  if (!fits_i32(m) || !fits_i32(k) || !fits_i32(n) || k < 8 || n < 8 || k % 8 != 0 || n % 8 != 0)
+  if (!size_ok(m) || !size_ok(k) || !size_ok(n) || k < 8 || n < 8 || k % 8 != 0 || n % 8 != 0)
     return GMM_ERR_SHAPE;
   if (num_total_groups < 1 || num_total_groups > GMM_MAX_GROUPS || num_local_groups < 1 ||
       num_local_groups > num_total_groups)

@@ -8,6 +8,9 @@
 
 namespace gmmk {
 
+// Rows, columns and depth that the kernels take: their int32 indexes may run a tile past the last.
+constexpr int64_t kMaxSize = int64_t(INT32_MAX) - 1023;
+
 // Launches a kernel that begins with griddep_begin() (ptx.cuh) as the programmatic dependent of what is
 // ahead of it on the stream: its launch overlaps that work's end.  cluster > 1: in clusters of so many CTAs.
 template <class... P, class... A>
