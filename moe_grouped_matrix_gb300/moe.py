@@ -9,7 +9,9 @@ expert and brought back, and microscaled 4-bit floating point.
     q = quantize_fp4(x, "nvfp4", order=order)      # the same rows in 4 bits, for gmm_fp4()
 
 Like the rest of the package this only marshals arguments; gradients are calls of their own
-(``route_backward``, ``dispatch_backward``, ``combine_backward``).  Arguments that are right as they
+(``route_backward``, ``dispatch_backward``, ``combine_backward``).  A call with ``stream=`` runs on
+that stream and its results belong to it, as if it were made under ``torch.cuda.stream(stream)``;
+its inputs are the caller's to keep ready and alive for it.  Arguments that are right as they
 stand go to the library through ``_host_calls.so`` (``csrc/host_calls.cpp``) in one step; all others
 are looked at here, one by one, and called through ctypes or refused.
 """
@@ -25,7 +27,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_I, _I32, _I64, _P, _SZ, DTYPE_BF16, DTYPE_F32, SIGNATURES, GmmError, _dev, load_library,
+from . import (_I, _I32, _I64, _P, _SZ, DTYPE_BF16, DTYPE_F32, SIGNATURES, GmmError, _dev, _on_stream, load_library,
                workspace_for)
 
 __all__ = ["route", "route_backward", "ExpertOrder", "sort_by_expert", "dispatch", "dispatch_backward", "combine",
@@ -184,8 +186,9 @@ def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bia
         _want(select_bias, "select_bias", torch.float32, (experts,))
     if token_mask is not None:
         _want(token_mask, "token_mask", torch.uint8 if token_mask.dtype == torch.uint8 else torch.bool, (tokens,))
-    weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
-    chosen = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+    with _on_stream(stream):
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+        chosen = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
     _run("gmm_route", _lib().gmm_route(
         logits.data_ptr(), code, tokens, experts, ld, topk, _score(score), int(bool(renormalize)), float(scale),
         _ptr(select_bias), _ptr(token_mask), weights.data_ptr(), chosen.data_ptr(), _on(logits.device, stream)))
@@ -209,7 +212,8 @@ def route_backward(dweights, experts, logits, score="softmax", renormalize=True,
     topk = experts.shape[1]
     _want(experts, "experts", torch.int32, (tokens, topk))
     _want(dweights, "dweights", torch.float32, (tokens, topk))
-    dlogits = torch.empty((tokens, n), dtype=logits.dtype, device=logits.device)
+    with _on_stream(stream):
+        dlogits = torch.empty((tokens, n), dtype=logits.dtype, device=logits.device)
     _run("gmm_route_backward", _lib().gmm_route_backward(
         dweights.data_ptr(), experts.data_ptr(), logits.data_ptr(), code, tokens, n, ld, topk, _score(score),
         int(bool(renormalize)), float(scale), dlogits.data_ptr(), _on(logits.device, stream)))
@@ -228,9 +232,10 @@ def sort_by_expert(experts, num_experts, stream=None):
         raise ValueError("experts must be [tokens, topk]")
     tokens, topk = experts.shape
     _want(experts, "experts", torch.int32, (tokens, topk))
-    sizes = torch.empty((int(num_experts),), dtype=torch.int32, device=experts.device)
-    rows = torch.empty((tokens, topk), dtype=torch.int32, device=experts.device)
-    source = torch.empty((tokens * topk,), dtype=torch.int32, device=experts.device)
+    with _on_stream(stream):
+        sizes = torch.empty((int(num_experts),), dtype=torch.int32, device=experts.device)
+        rows = torch.empty((tokens, topk), dtype=torch.int32, device=experts.device)
+        source = torch.empty((tokens * topk,), dtype=torch.int32, device=experts.device)
     _run("gmm_sort_by_expert", _lib().gmm_sort_by_expert(
         experts.data_ptr(), tokens, topk, int(num_experts), sizes.data_ptr(), rows.data_ptr(), source.data_ptr(),
         _on(experts.device, stream)))
@@ -259,7 +264,8 @@ def dispatch(x, order, stream=None):
     tokens, topk = _order(order)
     if x.shape[0] != tokens:
         raise ValueError(f"x must have {tokens} rows")
-    out = torch.empty((tokens * topk, x.shape[1]), dtype=x.dtype, device=x.device)
+    with _on_stream(stream):
+        out = torch.empty((tokens * topk, x.shape[1]), dtype=x.dtype, device=x.device)
     _run("gmm_dispatch", _lib().gmm_dispatch(
         x.data_ptr(), code, tokens, x.shape[1], ld, topk, order.rows.data_ptr(), order.source.data_ptr(),
         out.data_ptr(), _on(x.device, stream)))
@@ -280,7 +286,8 @@ def combine(rows, order, weights=None, stream=None):
         raise ValueError(f"rows must be [{tokens * topk}, d]")
     if weights is not None:
         _want(weights, "weights", torch.float32, (tokens, topk))
-    out = torch.empty((tokens, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    with _on_stream(stream):
+        out = torch.empty((tokens, rows.shape[1]), dtype=rows.dtype, device=rows.device)
     _run("gmm_combine", _lib().gmm_combine(
         rows.data_ptr(), code, tokens, rows.shape[1], topk, order.rows.data_ptr(), _ptr(weights), out.data_ptr(),
         _on(rows.device, stream)))
@@ -306,8 +313,9 @@ def combine_backward(dout, rows, order, weights, stream=None):
         raise ValueError(f"rows must be [{tokens * topk}, d]")
     _want(dout, "dout", rows.dtype, (tokens, rows.shape[1]))
     _want(weights, "weights", torch.float32, (tokens, topk))
-    drows = torch.empty_like(rows)
-    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=rows.device)
+    with _on_stream(stream):
+        drows = torch.empty_like(rows)
+        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=rows.device)
     _run("gmm_combine_backward", _lib().gmm_combine_backward(
         dout.data_ptr(), rows.data_ptr(), code, tokens, rows.shape[1], topk, order.rows.data_ptr(),
         order.source.data_ptr(), weights.data_ptr(), drows.data_ptr(), dweights.data_ptr(),
@@ -354,9 +362,10 @@ def quantize_fp4(x, format="nvfp4", order=None, stream=None):
         out_rows = tokens * topk
     if k % 32:
         raise ValueError("k must be a multiple of 32")
-    codes = torch.empty(lead + (out_rows, k // 2), dtype=torch.uint8, device=x.device)
-    scale = torch.empty(lead + (_windows(k, format), out_rows, 16), dtype=torch.uint8, device=x.device)
-    row = torch.empty(lead + (out_rows,), dtype=torch.float32, device=x.device) if format == "nvfp4" else None
+    with _on_stream(stream):
+        codes = torch.empty(lead + (out_rows, k // 2), dtype=torch.uint8, device=x.device)
+        scale = torch.empty(lead + (_windows(k, format), out_rows, 16), dtype=torch.uint8, device=x.device)
+        row = torch.empty(lead + (out_rows,), dtype=torch.float32, device=x.device) if format == "nvfp4" else None
     if batch == 0:
         return Fp4Tensor(codes, scale, row, format)
     _run("gmm_quantize_fp4", _lib().gmm_quantize_fp4(
@@ -397,7 +406,8 @@ def dequantize_fp4(q, out_dtype=torch.bfloat16, stream=None):
         raise ValueError("codes must be [rows, k / 2] or [batch, rows, k / 2]")
     rows, k = _fp4_args(q, "q", lead)
     batch = q.codes.shape[0] if lead else 1
-    out = torch.empty(tuple(q.codes.shape[:-1]) + (k,), dtype=out_dtype, device=q.codes.device)
+    with _on_stream(stream):
+        out = torch.empty(tuple(q.codes.shape[:-1]) + (k,), dtype=out_dtype, device=q.codes.device)
     if batch == 0:
         return out
     _run("gmm_dequantize_fp4", _lib().gmm_dequantize_fp4(
@@ -440,7 +450,8 @@ def gmm_fp4(lhs, rhs, group_sizes, rhs_bias=None, group_offset=0, out=None, out_
     else:
         bias_code = DTYPE_BF16
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=device)
+        with _on_stream(stream):
+            out = torch.empty((m, n), dtype=out_dtype, device=device)
     _dev(out, "out")
     if tuple(out.shape) != (m, n):
         raise ValueError(f"out must be [{m}, {n}], got {list(out.shape)}")
