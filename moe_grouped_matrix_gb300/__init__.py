@@ -220,9 +220,20 @@ def _on_stream(stream):
     return _OnStream(stream) if stream.device_index == torch._C._cuda_getDevice() else torch.cuda.stream(stream)
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _here(t: torch.Tensor, name: str) -> None:
+    """The library launches on the current device, so that is where every tensor of a call has to be."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}")
+
+
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    _here(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -43,6 +44,15 @@ const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_U
 
 bool dense(const Tensor* t, at::ScalarType type, at::IntArrayRef shape) {
   return t != nullptr && t->is_cuda() && t->scalar_type() == type && t->sizes() == shape && t->is_contiguous();
+}
+
+// Whether the tensors (NULL: none given) are the current device's: the C ABI launches there.
+bool here(std::initializer_list<const Tensor*> all) {
+  c10::DeviceIndex now = -1;
+  if (c10::cuda::GetDevice(&now) != cudaSuccess) return false;
+  for (const Tensor* t : all)
+    if (t != nullptr && t->get_device() != now) return false;
+  return true;
 }
 
 int code_of(const Tensor& t) { return t.scalar_type() == kF32 ? GMM_DTYPE_F32 : GMM_DTYPE_BF16; }
@@ -128,7 +138,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t score = integer(a[2], 0, 1, &ok), renormalize = integer(a[3], 0, 1, &ok);
     ok = ok && (a[5] == Py_None || dense(bias, kF32, {experts}));
     ok = ok && (a[6] == Py_None || dense(mask, at::kBool, {tokens}) || dense(mask, kU8, {tokens}));
-    if (!ok) return no_answer();
+    if (!ok || !here({logits, bias, mask})) return no_answer();
     Tensor weights = empty({tokens, topk}, kF32, *logits), chosen = empty({tokens, topk}, kI32, *logits);
     const int st = g_calls.route(logits->data_ptr(), code_of(*logits), tokens, int32_t(experts), ld, int32_t(topk),
                                  int(score), int(renormalize), float(PyFloat_AS_DOUBLE(a[4])),
@@ -148,7 +158,9 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = logits->size(0), experts = logits->size(1), topk = chosen->size(1);
     bool ok = experts <= GMM_MAX_GROUPS && topk >= 1 && topk <= GMM_MAX_TOPK && topk <= experts;
     const int64_t score = integer(a[3], 0, 1, &ok), renormalize = integer(a[4], 0, 1, &ok);
-    if (!ok || !dense(chosen, kI32, {tokens, topk}) || !dense(dweights, kF32, {tokens, topk})) return no_answer();
+    if (!ok || !dense(chosen, kI32, {tokens, topk}) || !dense(dweights, kF32, {tokens, topk}) ||
+        !here({dweights, chosen, logits}))
+      return no_answer();
     Tensor dlogits = empty({tokens, experts}, logits->scalar_type(), *logits);
     const int st = g_calls.route_backward(ptr<float>(*dweights), ptr<int32_t>(*chosen), logits->data_ptr(),
                                           code_of(*logits), tokens, int32_t(experts), ld, int32_t(topk), int(score),
@@ -167,7 +179,7 @@ PyObject* sort_by_expert(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = experts->size(0), topk = experts->size(1);
     bool ok = dense(experts, kI32, {tokens, topk}) && topk >= 1 && topk <= GMM_MAX_TOPK;
     const int64_t num = integer(a[1], 1, GMM_MAX_GROUPS, &ok);
-    if (!ok) return no_answer();
+    if (!ok || !here({experts})) return no_answer();
     Tensor sizes = empty({num}, kI32, *experts), rows = empty({tokens, topk}, kI32, *experts),
            source = empty({tokens * topk}, kI32, *experts);
     const int st = g_calls.sort(ptr<int32_t>(*experts), tokens, int32_t(topk), int32_t(num), ptr<int32_t>(sizes),
@@ -191,7 +203,8 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *x = tensor(a[0]), *rows = tensor(a[1]), *source = tensor(a[2]);
     const int64_t ld = pitch(x);
     int64_t tokens, topk;
-    if (ld < 0 || !order_of(rows, source, &tokens, &topk) || x->size(0) != tokens) return no_answer();
+    if (ld < 0 || !order_of(rows, source, &tokens, &topk) || x->size(0) != tokens || !here({x, rows, source}))
+      return no_answer();
     const int64_t d = x->size(1);
     Tensor out = empty({tokens * topk, d}, x->scalar_type(), *x);
     const int st = g_calls.dispatch(x->data_ptr(), code_of(*x), tokens, d, ld, int32_t(topk), ptr<int32_t>(*rows),
@@ -210,7 +223,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return no_answer();
     const int64_t d = in->size(1);
     if (!dense(in, in->scalar_type(), {tokens * topk, d}) ||
-        (a[3] != Py_None && !dense(weights, kF32, {tokens, topk})))
+        (a[3] != Py_None && !dense(weights, kF32, {tokens, topk})) || !here({in, rows, source, weights}))
       return no_answer();
     Tensor out = empty({tokens, d}, in->scalar_type(), *in);
     const int st = g_calls.combine(in->data_ptr(), code_of(*in), tokens, d, int32_t(topk), ptr<int32_t>(*rows),
@@ -230,7 +243,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return no_answer();
     const int64_t d = in->size(1);
     if (!dense(in, in->scalar_type(), {tokens * topk, d}) || !dense(dout, in->scalar_type(), {tokens, d}) ||
-        !dense(weights, kF32, {tokens, topk}))
+        !dense(weights, kF32, {tokens, topk}) || !here({dout, in, rows, source, weights}))
       return no_answer();
     Tensor din = empty({tokens * topk, d}, in->scalar_type(), *in), dweights = empty({tokens, topk}, kF32, *in);
     const int st = g_calls.combine_backward(dout->data_ptr(), in->data_ptr(), code_of(*in), tokens, d, int32_t(topk),
@@ -256,7 +269,7 @@ PyObject* quantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t format = integer(a[1], 0, 1, &ok), tokens = x->size(0), k = x->size(1);
     int64_t order_tokens = tokens, topk = 1;
     if (a[2] != Py_None) ok = ok && order_of(rows, source, &order_tokens, &topk) && order_tokens == tokens;
-    if (!ok || k < 32 || k % 32 != 0) return no_answer();
+    if (!ok || k < 32 || k % 32 != 0 || !here({x, rows, source})) return no_answer();
     const int64_t out_rows = tokens * topk;
     Tensor codes = empty({out_rows, k / 2}, kU8, *x), scale = empty({windows_of(k, format), out_rows, 16}, kU8, *x), row;
     if (format == GMM_FP4_NVFP4) row = empty({out_rows}, kF32, *x);
@@ -290,7 +303,8 @@ PyObject* dequantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bool ok = true;
     const int64_t format = integer(a[3], 0, 1, &ok), f32 = integer(a[4], 0, 1, &ok);
     int64_t batch, rows, k;
-    if (!ok || !fp4_of(codes, scale, row, a[2] != Py_None, format, 0, &batch, &rows, &k)) return no_answer();
+    if (!ok || !fp4_of(codes, scale, row, a[2] != Py_None, format, 0, &batch, &rows, &k) || !here({codes, scale, row}))
+      return no_answer();
     Tensor out = empty({rows, k}, f32 ? kF32 : kBF16, *codes);
     const int st = g_calls.dequantize(codes->data_ptr(), scale->data_ptr(), ptr_or_null<float>(row), int(format), 1,
                                       rows, k, out.data_ptr(), code_of(out), stream_of(*codes));
@@ -312,7 +326,8 @@ PyObject* gmm_fp4_call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ok = ok && fp4_of(lc, ls, lr, a[2] != Py_None, format, 0, &one, &m, &k) &&
          fp4_of(rc, rs, rr, a[5] != Py_None, format, 1, &local, &nn, &kr) && k == kr;
     if (!ok || sizes == nullptr || sizes->dim() != 1 || !dense(sizes, kI32, {sizes->size(0)}) ||
-        sizes->size(0) > GMM_MAX_GROUPS || local > GMM_MAX_GROUPS)
+        sizes->size(0) > GMM_MAX_GROUPS || local > GMM_MAX_GROUPS ||
+        !here({lc, ls, lr, rc, rs, rr, sizes, ws}))
       return no_answer();
     Tensor out = empty({m, nn}, f32 ? kF32 : kBF16, *lc);
     const int st = g_calls.fp4(lc->data_ptr(), ls->data_ptr(), ptr_or_null<float>(lr), m, k, rc->data_ptr(),

@@ -27,8 +27,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_I, _I32, _I64, _P, _SZ, DTYPE_BF16, DTYPE_F32, SIGNATURES, GmmError, _dev, _on_stream, load_library,
-               workspace_for)
+from . import (_I, _I32, _I64, _P, _SZ, DTYPE_BF16, DTYPE_F32, SIGNATURES, GmmError, _dev, _here, _on_stream,
+               load_library, workspace_for)
 
 __all__ = ["route", "route_backward", "ExpertOrder", "sort_by_expert", "dispatch", "dispatch_backward", "combine",
            "combine_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gmm_fp4", "MAX_TOPK"]
@@ -119,6 +119,7 @@ def _rows(t, name):
     """A 2-D CUDA tensor whose rows are dense; returns its row pitch."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    _here(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     n, d = t.shape
@@ -143,9 +144,9 @@ def _float_code(t, name):
 
 
 def _want(t, name, dtype, shape):
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return
     _dev(t, name)
+    if t.dtype is dtype and t.shape == shape:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
