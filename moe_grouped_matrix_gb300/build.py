@@ -4,7 +4,8 @@ Each .cu file is compiled to an object in parallel, then linked into
 ``moe_grouped_matrix_gb300/libgmm.so``.  Objects live in ``_build/`` next to
 this file and are rebuilt when any source or header is newer.  Beside them g++
 compiles ``csrc/host_calls.cpp`` (no device code) against the installed
-PyTorch's headers into ``moe_grouped_matrix_gb300/_host_calls.so``.
+PyTorch's headers; the name of the result says which PyTorch and Python it is
+for, so another one finds no file of its own instead of one that does not fit.
 """
 
 from __future__ import annotations
@@ -23,7 +24,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libgmm.so")
 HOST_CALLS = os.path.join(CSRC, "host_calls.cpp")
-HOST_CALLS_PATH = os.path.join(HERE, "_host_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -49,6 +49,14 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def host_calls_path() -> str:
+    """The host-side calls built for this PyTorch and this Python."""
+    import torch
+
+    abi = f"torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_host_calls.{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _host_calls_command(out: str):
@@ -77,8 +85,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd[1:1] = ["-Xptxas", "-v"]
             jobs.append((cmd, obj))
 
-    if force or _stale(HOST_CALLS_PATH, [HOST_CALLS] + headers):
-        tmp_calls = HOST_CALLS_PATH + f".tmp{os.getpid()}"
+    host_calls = host_calls_path()
+    if force or _stale(host_calls, [HOST_CALLS] + headers):
+        tmp_calls = host_calls + f".tmp{os.getpid()}"
         jobs.append((_host_calls_command(tmp_calls), tmp_calls))
 
     def run(job):
@@ -87,7 +96,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if res.returncode != 0:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {obj}:\n{res.stdout}\n{res.stderr}")
         if cmd[0] == "g++":
-            os.replace(obj, HOST_CALLS_PATH)
+            os.replace(obj, host_calls)
         return res.stdout + res.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:

@@ -12,7 +12,7 @@ Like the rest of the package this only marshals arguments; gradients are calls o
 (``route_backward``, ``dispatch_backward``, ``combine_backward``).  A call with ``stream=`` runs on
 that stream and its results belong to it, as if it were made under ``torch.cuda.stream(stream)``;
 its inputs are the caller's to keep ready and alive for it.  Arguments that are right as they
-stand go to the library through ``_host_calls.so`` (``csrc/host_calls.cpp``) in one step; all others
+stand go to the library through ``csrc/host_calls.cpp`` in one step; all others
 are looked at here, one by one, and called through ctypes or refused.
 """
 
@@ -21,8 +21,8 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
-import os
 import sys
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -97,20 +97,32 @@ def _lib():
 _calls = None
 
 
+class _NoCalls:
+    """Stands for host-side calls that are not there: none takes any arguments."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _bind():
-    """Loads _host_calls.so and gives it the loaded library's functions."""
+    """Loads the host-side calls built for this PyTorch and gives them the loaded library's functions;
+    without them every call goes through the checks below and ctypes."""
     global _calls
+    from .build import host_calls_path
+
     lib = load_library()
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_host_calls.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with `python -m moe_grouped_matrix_gb300.build`")
+    path = host_calls_path()
     loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._host_calls", path)
-    spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
-    calls = importlib.util.module_from_spec(spec)
-    loader.exec_module(calls)
-    names = ("gmm_route", "gmm_route_backward", "gmm_sort_by_expert", "gmm_dispatch", "gmm_combine",
-             "gmm_combine_backward", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_fp4")
-    calls.bind(*[ctypes.cast(getattr(lib, n), _P).value for n in names])
+    try:
+        calls = importlib.util.module_from_spec(importlib.util.spec_from_file_location(loader.name, path, loader=loader))
+        loader.exec_module(calls)
+        names = ("gmm_route", "gmm_route_backward", "gmm_sort_by_expert", "gmm_dispatch", "gmm_combine",
+                 "gmm_combine_backward", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_fp4")
+        calls.bind(*[ctypes.cast(getattr(lib, n), _P).value for n in names])
+    except ImportError as e:
+        warnings.warn(f"the mixture-of-experts calls go the longer way, some 7 us of host time more for each ({e}): "
+                      "build with `python -m moe_grouped_matrix_gb300.build`", RuntimeWarning, stacklevel=3)
+        calls = _NoCalls()
     _calls = calls
     return calls
 
