@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -40,7 +41,8 @@ constexpr auto kBF16 = at::kBFloat16;
 constexpr auto kI32 = at::kInt;
 constexpr auto kU8 = at::kByte;
 
-const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+// A tensor as it stands: not of a subclass, whose operations are its own.
+const Tensor* tensor(PyObject* o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
 
 bool dense(const Tensor* t, at::ScalarType type, at::IntArrayRef shape) {
   return t != nullptr && t->is_cuda() && t->scalar_type() == type && t->sizes() == shape && t->is_contiguous();
@@ -114,10 +116,12 @@ int64_t integer(PyObject* o, int64_t lo, int64_t hi, bool* ok) {
   return v;
 }
 
-// No C++ exception (an allocation that fails) crosses into Python.
+// No C++ exception (an allocation that fails) crosses into Python.  While a dispatch mode is on, which
+// empty() below would pass by, there is no short way.
 template <class F>
 PyObject* guarded(F&& f) {
   try {
+    if (c10::impl::TorchDispatchModeTLS::any_modes_set()) return no_answer();
     return f();
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
