@@ -6,6 +6,7 @@ this file and are rebuilt when any source or header is newer.  Beside them g++
 compiles ``csrc/host_calls.cpp`` (no device code) against the installed
 PyTorch's headers; the name of the result says which PyTorch and Python it is
 for, so another one finds no file of its own instead of one that does not fit.
+A PyTorch without CUDA gets none.
 """
 
 from __future__ import annotations
@@ -85,8 +86,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd[1:1] = ["-Xptxas", "-v"]
             jobs.append((cmd, obj))
 
+    import torch
+
     host_calls = host_calls_path()
-    if force or _stale(host_calls, [HOST_CALLS] + headers):
+    if torch.version.cuda is not None and (force or _stale(host_calls, [HOST_CALLS] + headers)):
         tmp_calls = host_calls + f".tmp{os.getpid()}"
         jobs.append((_host_calls_command(tmp_calls), tmp_calls))
 

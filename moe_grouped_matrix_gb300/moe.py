@@ -76,7 +76,8 @@ class Fp4Tensor(NamedTuple):
 
 # These calls are a few microseconds of GPU work at decoding sizes, so the checks below cost as
 # little as they can: one test that holds for good arguments, and the reason only where it fails.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# A PyTorch without CUDA has no such function, and no tensor that any call takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(device, stream):

@@ -3,6 +3,8 @@ are found by that, and without them, or with a file that does not load, every ca
 (no GPU needed)."""
 
 import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -57,3 +59,29 @@ def test_a_file_that_does_not_load(unbound, monkeypatch, tmp_path):
     monkeypatch.setattr(B, "host_calls_path", lambda: str(bad))
     with pytest.warns(RuntimeWarning, match="longer way"):
         refuses_host_tensors()
+
+
+WITHOUT_CUDA = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+torch.version.cuda = None
+import moe_grouped_matrix_gb300 as G
+from moe_grouped_matrix_gb300 import build as B
+B._host_calls_command = None
+B.HERE = B.BUILD_DIR  # where no host-side calls are
+B.build()
+for call in (lambda: G.route(torch.zeros((4, 8)), 2), lambda: G.gmm(*[torch.zeros(2, 2, 2)] * 3)):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA tensor" in str(e)
+    else:
+        raise AssertionError
+"""
+
+
+def test_a_pytorch_without_cuda_imports_and_builds():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-W", "ignore", "-c", WITHOUT_CUDA], cwd=root, capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr[-2000:]
