@@ -22,19 +22,22 @@ extern "C" {
 
 /* ------------------------------------------------------------------ the router */
 
-/* gmm_route() score */
-enum { GMM_SCORE_SOFTMAX = 0, GMM_SCORE_SIGMOID = 1 };
+/* gmm_route() score; GMM_SCORE_BIASED may be or-ed to it there: select_bias is the score's. */
+enum { GMM_SCORE_SOFTMAX = 0, GMM_SCORE_SIGMOID = 1, GMM_SCORE_BIASED = 16 };
 
 /* Largest topk of gmm_route(). */
 #define GMM_MAX_TOPK 32
 
 /*
  * Top-k routing.  For each token t with logits l[e], e < num_experts:
- *   key[e] = l[e] + select_bias[e] in fp32 (l[e] without select_bias);
+ *   key[e] = l[e] + select_bias[e] in fp32 (l[e] without select_bias); with
+ *            GMM_SCORE_BIASED s(l)[e] + select_bias[e], s the softmax over all experts or
+ *            the sigmoid in fp32 (the form of biases that balance the experts' loads);
  *   the topk experts with the largest keys are chosen, in falling order, equal
  *   keys by rising index (-0 equals 0).  An expert whose key is -inf or NaN is
- *   never chosen: a logit of -inf switches an expert off for the token.  (A NaN or
- *   +inf logit makes the weights that its score enters NaN.)
+ *   never chosen, nor is one whose logit is -inf: that switches it off for the token.
+ *   (A NaN logit, and for the softmax +inf, makes the weights that its score enters NaN,
+ *   and with GMM_SCORE_BIASED the keys.)
  *   Without renormalize the weight of a chosen expert is scale * s(l)[e], with s
  *   the softmax over all experts or the sigmoid; with renormalize those scores
  *   are divided by their sum over the chosen experts.  select_bias moves the

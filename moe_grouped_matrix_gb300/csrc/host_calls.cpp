@@ -139,7 +139,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = logits->size(0), experts = logits->size(1);
     bool ok = experts <= GMM_MAX_GROUPS && PyFloat_CheckExact(a[4]);
     const int64_t topk = integer(a[1], 1, experts < GMM_MAX_TOPK ? experts : GMM_MAX_TOPK, &ok);
-    const int64_t score = integer(a[2], 0, 1, &ok), renormalize = integer(a[3], 0, 1, &ok);
+    const int64_t score = integer(a[2], 0, GMM_SCORE_BIASED | 1, &ok), renormalize = integer(a[3], 0, 1, &ok);
     ok = ok && (a[5] == Py_None || dense(bias, kF32, {experts}));
     ok = ok && (a[6] == Py_None || dense(mask, at::kBool, {tokens}) || dense(mask, kU8, {tokens}));
     if (!ok || !here({logits, bias, mask})) return no_answer();

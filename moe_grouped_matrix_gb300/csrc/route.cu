@@ -1,7 +1,7 @@
 // The router of a mixture-of-experts layer: the top-k choice of experts with
 // its weights, and the gradient of the weights with respect to the logits.
 //
-//   key[e] = l[e] + bias[e];  chosen: the topk largest keys, ties by index
+//   key[e] = l[e] + bias[e], or s(l)[e] + bias[e];  chosen: the topk largest keys, ties by index
 //   w_j = scale * s(l)[e_j], or scale * s(l)[e_j] / sum_i s(l)[e_i]
 // with s the softmax over all experts or the sigmoid.  Renormalised weights of
 // either score are a softmax over the chosen experts' values v, v = l for the
@@ -13,8 +13,10 @@
 // integer with the same order (0: cannot be chosen) and each of the topk rounds
 // is one warp-wide integer maximum, a ballot for the lowest lane that holds it
 // and a rescan of that lane's V keys.  Bound by the rounds' latency: 64 tokens, 4
-// of 64 experts, 1.9 us in a graph; 4096 tokens, 8 of 128 experts, 7 us under the
-// profiler for 2 MB of logits, the gradient 6 us.
+// of 64 experts, 1.7 us in a graph; 4096 tokens, 8 of 128 experts, 5.4 us for 1 or
+// 2 MB of logits, 5.6 with a bias on the logits and 6.5 with one on the scores, whose
+// exponentials come before the choice (a kernel of its own: as a branch in one
+// kernel it took the other forms 6.0 us).
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -52,6 +54,10 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+__device__ __forceinline__ float sigmoid(float l) {
+  const float e = expf(-fabsf(l));  // neither side overflows
+  return (l < 0.f ? e : 1.f) / (1.f + e);
+}
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
 
 // V consecutive logits of this lane (past the last expert: -inf).  Whole 16-byte
@@ -91,7 +97,8 @@ struct RouteParams {
   int32_t* chosen;
 };
 
-template <int V, class T>
+// kScored: the bias is the score's.
+template <int V, class T, bool kScored>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
   griddep_begin();
   p.logits = after_begin(p.logits), p.bias = after_begin(p.bias), p.mask = after_begin(p.mask);
@@ -108,10 +115,26 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) l[i] = -INFINITY;
   }
+  // The softmax over all experts is exp(l - high) / total.
+  auto over_all = [&](float& high, float& total) {
+    high = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) high = fmaxf(high, l[i]);
+    high = warp_max(high);
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += expf(l[i] - high);
+    total = warp_sum(total);
+  };
+  float high = 0.f, total = 1.f;
+  if (kScored && !p.sigmoid) over_all(high, total);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const float b = p.bias != nullptr && e0 + i < p.experts ? __ldg(p.bias + e0 + i) : 0.f;
-    key[i] = ordered(l[i] + b);
+    float to = l[i];
+    if constexpr (kScored) {
+      if (to > -INFINITY) to = p.sigmoid ? sigmoid(to) : expf(to - high) / total;
+    }
+    key[i] = ordered(to + b);
   }
   uint32_t best = 0;
   int at = 0;
@@ -153,15 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
   } else if (p.sigmoid) {
     w = took ? p.scale * expf(v) : 0.f;
   } else if (live) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-    top = warp_max(top);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) sum += expf(l[i] - top);
-    sum = warp_sum(sum);
-    w = took ? p.scale * (expf(mine_l - top) / sum) : 0.f;
+    if (!kScored) over_all(high, total);
+    w = took ? p.scale * (expf(mine_l - high) / total) : 0.f;
   }
   if (lane < p.topk) {
     p.weights[t * p.topk + lane] = w;
@@ -283,12 +299,13 @@ cudaError_t by_width(int v, F&& go) {
 }
 
 template <class T>
-cudaError_t route(const RouteParams& p, cudaStream_t stream) {
+cudaError_t route(const RouteParams& p, bool scored, cudaStream_t stream) {
   return by_width(lane_experts(p.experts), [&](auto v) {
     constexpr int V = decltype(v)::value;
     RouteParams q = p;
     q.wide = p.experts % V == 0 && p.ld * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
-    return launch_dependent(route_kernel<V, T>, unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0, stream, 1, q);
+    auto kern = scored ? route_kernel<V, T, true> : route_kernel<V, T, false>;
+    return launch_dependent(kern, unsigned((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, 0, stream, 1, q);
   });
 }
 
@@ -323,6 +340,8 @@ extern "C" int gmm_route(const void* logits, int logits_dtype, int64_t tokens, i
                          int32_t topk, int score, int renormalize, float scale, const float* select_bias,
                          const uint8_t* token_mask, float* weights, int32_t* experts, void* stream) {
   using namespace gmmk;
+  const bool scored = (score & GMM_SCORE_BIASED) != 0 && select_bias != nullptr;
+  score &= ~GMM_SCORE_BIASED;
   if (int st = check(logits, logits_dtype, tokens, num_experts, logits_ld, topk, score)) return st;
   if (tokens > 0 && (logits == nullptr || weights == nullptr || experts == nullptr))
     return GMM_ERR_NULL;
@@ -332,7 +351,7 @@ extern "C" int gmm_route(const void* logits, int logits_dtype, int64_t tokens, i
   const RouteParams p{logits, tokens, logits_ld, num_experts, topk, score == GMM_SCORE_SIGMOID, renormalize != 0, 0,
                       scale, select_bias, token_mask, weights, experts};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_dtype == GMM_DTYPE_F32 ? route<float>(p, s) : route<__nv_bfloat16>(p, s);
+  const cudaError_t e = logits_dtype == GMM_DTYPE_F32 ? route<float>(p, scored, s) : route<__nv_bfloat16>(p, scored, s);
   return e == cudaSuccess ? GMM_OK : record_cuda_error(e);
 }
 

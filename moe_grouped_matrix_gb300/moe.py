@@ -34,6 +34,7 @@ __all__ = ["route", "route_backward", "ExpertOrder", "sort_by_expert", "dispatch
            "combine_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gmm_fp4", "MAX_TOPK"]
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+_BIASED = {"softmax": 16, "sigmoid": 17}
 FP4_FORMATS = {"nvfp4": 0, "mxfp4": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 MAX_TOPK = 32
@@ -169,24 +170,35 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _score(score):
+def _biased(bias_on):
+    """The scores' codes where select_bias is not the logit's."""
+    if bias_on != "score":
+        raise ValueError("bias_on must be 'logit' or 'score'")
+    return _BIASED
+
+
+def _score(score, codes=SCORES):
     try:
-        return SCORES[score]
+        return codes[score]
     except KeyError:
         raise ValueError(f"score must be one of {sorted(SCORES)}") from None
 
 
-def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bias=None, token_mask=None, stream=None):
+def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bias=None, token_mask=None, stream=None,
+          bias_on="logit"):
     """The topk experts of each token and their weights: (weights float32 [tokens, topk], experts
     int32 [tokens, topk]) from logits [tokens, experts] (bfloat16 or float32, rows may have a
     pitch).  Experts are chosen by logit + select_bias (float32 [experts]), largest first, equal
-    ones by index; experts whose logit is -inf or NaN are never chosen.  Weights are
+    ones by index; experts whose logit is -inf or NaN are never chosen.  With bias_on="score" they
+    are chosen by softmax (over all experts) or sigmoid + select_bias, the form of biases that
+    balance the experts' loads: the two choose different experts.  The bias moves the choice only,
+    never the weights.  Weights are
     scale * softmax (over all experts) or scale * sigmoid of the logits, divided by their sum over
     the chosen experts with renormalize.  Tokens whose token_mask (bool or uint8 [tokens]) is 0,
     and slots past the experts that can be chosen, have expert -1 and weight 0."""
     if stream is None:
-        got = (_calls or _bind()).route(logits, topk, SCORES.get(score), 1 if renormalize else 0, scale, select_bias,
-                                        token_mask)
+        got = (_calls or _bind()).route(logits, topk, (SCORES if bias_on == "logit" else _biased(bias_on)).get(score),
+                                        1 if renormalize else 0, scale, select_bias, token_mask)
         if got.__class__ is tuple:
             return got
         _run("gmm_route", got)
@@ -204,7 +216,8 @@ def route(logits, topk, score="softmax", renormalize=True, scale=1.0, select_bia
         weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
         chosen = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
     _run("gmm_route", _lib().gmm_route(
-        logits.data_ptr(), code, tokens, experts, ld, topk, _score(score), int(bool(renormalize)), float(scale),
+        logits.data_ptr(), code, tokens, experts, ld, topk,
+        _score(score, SCORES if bias_on == "logit" else _biased(bias_on)), int(bool(renormalize)), float(scale),
         _ptr(select_bias), _ptr(token_mask), weights.data_ptr(), chosen.data_ptr(), _on(logits.device, stream)))
     return weights, chosen
 
