@@ -145,8 +145,9 @@ int gmm_quantize_fp4(const void* x, int x_dtype, int32_t batch, int64_t rows_per
                      int format, const int32_t* rows, const int32_t* source, int32_t topk, void* codes,
                      void* block_scale, float* row_scale, void* stream);
 
-/* The values a quantised matrix stands for, rounded once to out_dtype (BF16 holds them exactly
- * while they are in its normal range). */
+/* The values a quantised matrix stands for, rounded once to out_dtype, whatever row_scale holds
+ * (with the powers of two of gmm_quantize_fp4() BF16 holds them exactly while they are in its
+ * normal range). */
 int gmm_dequantize_fp4(const void* codes, const void* block_scale, const float* row_scale, int format, int32_t batch,
                        int64_t rows_per_batch, int64_t k, void* out, int out_dtype, void* stream);
 

@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "../../include/libgmm_moe.h"
 #include "internal.h"
@@ -322,6 +323,14 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   }
 }
 
+// f = fl32(x * y) on a point half way between two bf16 values, where a second rounding would tie: a unit
+// towards the exact product, if it is not that point.
+__device__ __noinline__ float off_half_way(float f, float x, float y) {
+  const double left = double(x) * double(y) - double(f);  // exact
+  if (left == 0.0) return f;
+  return __uint_as_float(__float_as_uint(f) + ((left > 0.0) == (f > 0.f) ? 1 : -1));
+}
+
 // A CTA for each row; a thread writes 16 bytes at a time (8 bf16 or 4 f32 values), so that a warp's
 // store is whole lines, and has four such pieces on their way.
 template <class T, bool kNv>
@@ -350,25 +359,37 @@ __global__ void __launch_bounds__(kMaxThreads) dequantize_fp4_kernel(DequantPara
                           : uint32_t(__ldg(reinterpret_cast<const uint16_t*>(codes) + u));
       }
     }
+    auto put = [&](auto exact) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int32_t u = u0 + i * int32_t(blockDim.x);
-      if (u >= pieces) continue;
-      const float s = scale_value<kNv>(byte[i]);
-      uint32_t w[4];
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int32_t u = u0 + i * int32_t(blockDim.x);
+        if (u >= pieces) continue;
+        const float s = scale_value<kNv>(byte[i]);
+        uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < kVals / 2; ++j) {
-        const float2 q = e2m1x2_values(c[i] >> (8 * j));
-        const float x = q.x * s * rs, y = q.y * s * rs;
-        if constexpr (sizeof(T) == 4) {
-          w[2 * j] = __float_as_uint(x), w[2 * j + 1] = __float_as_uint(y);
-        } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-          memcpy(&w[j], &h, 4);
+        for (int j = 0; j < kVals / 2; ++j) {
+          const float2 q = e2m1x2_values(c[i] >> (8 * j));
+          float x = q.x * s * rs, y = q.y * s * rs;  // q * s is exact
+          if constexpr (sizeof(T) == 4) {
+            w[2 * j] = __float_as_uint(x), w[2 * j + 1] = __float_as_uint(y);
+          } else {
+            if constexpr (!decltype(exact)::value) {
+              if ((__float_as_uint(x) & 0xFFFFu) == 0x8000u) x = off_half_way(x, q.x * s, rs);
+              if ((__float_as_uint(y) & 0xFFFFu) == 0x8000u) y = off_half_way(y, q.y * s, rs);
+            }
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            memcpy(&w[j], &h, 4);
+          }
         }
+        out[u] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      out[u] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    };
+    // A code times its scale has 6 bits: with a power of two for the row, as gmm_quantize_fp4 gives, the
+    // product is exact wherever its bf16 value is not 0.
+    if (kNv && sizeof(T) == 2 && (__float_as_uint(rs) & 0x7FFFFFu) != 0)
+      put(std::false_type{});
+    else
+      put(std::true_type{});
   }
 }
 
