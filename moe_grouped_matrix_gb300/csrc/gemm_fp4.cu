@@ -45,8 +45,11 @@
 // PFLOP/s; MXFP4 562 us.  128 experts, 32768 rows, 2048 -> 2048: 83 us for 456 MB
 // (67 us at the copy rate).  Decoding, 64 experts, 256 rows, 4096 -> 2048: 52 us
 // for 303 MB (45 us), 46 back to back with the rows' quantisation.  What bounds
-// the first is the issuing of a stage's 16 instructions beside its waits, about
-// 600 cycles for 420 of MMA; for seconds on end the power cap (700 us).
+// the first is the way from L2 to the SMs: its tiles bring 8.5 GB of codes and 1.5
+// of scales into shared memory, 34.9 KB a CTA and stage, which at the 62 bytes a
+// cycle that an SM takes by TMA are 563 of a stage's about 600 cycles, beside 420
+// of MMA (10.0 GB at 18 TB/s: 557 us; 4 experts, 8192 rows, 4096 -> 8192: 1.43 GB
+// counted, as planned, in 94 us).  For seconds on end it is the power cap (700 us).
 //
 // Roles (512 threads): warp 0 copies codes; warp 1 tensor memory and MMA (the
 // leader's in a pair); warps 2-9 epilogue, each set of four every other 32 rows;
