@@ -114,7 +114,8 @@ int gmm_combine_backward(const void* dout, const void* in, int dtype, int64_t to
 /* A matrix [rows, k] in one of the formats below is
  *   codes        [rows, k / 2] e2m1, two per byte, the even k in the low nibble
  *   block_scale  [ceil(k / (16 * block)), rows, 16] bytes: the scales of a row's blocks
- *                by windows of 16 blocks; bytes past the last block are 0
+ *                by windows of 16 blocks; bytes past the last block are 0 (gmm_fp4() reads
+ *                whole windows: a NaN there would reach its sums)
  *   row_scale    f32 [rows], NVFP4 only
  * and stands for code * block_scale * row_scale.  A batch of matrices (the experts'
  * weights) has a leading dimension in each array.
@@ -161,7 +162,7 @@ int gmm_dequantize_fp4(const void* codes, const void* block_scale, const float* 
  *   lhs_*      [m, k] quantised rows;  rhs_*  [num_local_groups][n, k] quantised weights
  *   k % 32 == 0, n % 8 == 0; m, k and n at most 2^31 - 1024; codes, block scales and out
  *   16-byte aligned
- *   group_sizes, group offset, bias, workspace and stream as in gmm().
+ *   group_sizes, group_offset (a host value), bias, workspace and stream as in gmm().
  */
 int gmm_fp4(const void* lhs_codes, const void* lhs_block_scale, const float* lhs_row_scale, int64_t m, int64_t k,
             const void* rhs_codes, const void* rhs_block_scale, const float* rhs_row_scale, int format,

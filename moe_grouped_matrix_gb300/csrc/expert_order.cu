@@ -461,8 +461,9 @@ cudaError_t combine(const void* in, int64_t tokens, int64_t d, int32_t topk, con
       int64_t parts;
       // Wide units: 32 bytes a lane, four rows at once of more than two; where the sums are many, 64 bytes, two
       // rows and CTAs of two warps (8192 tokens, 2 rows of 4096 bf16 31.5 us, with 128 threads 33.5, as few
-      // tokens 34; 64 tokens, 4 rows of 2048 2.0 us in a graph, as many tokens 2.2; 8 MB lie between what
-      // gains and what loses).  Narrow units: 24 bytes, 128 threads (8192 tokens, 8 rows of 1027 bf16 37 us,
+      // tokens 34; 4096 tokens, 8 rows of 2048 25.3, as few 26.4; but 8192 tokens, 8 rows of 1032, with some
+      // lanes of a token's last run idle, 33.0, as few 32.0; 64 tokens, 4 rows of 2048 2.0 us in a graph, as
+      // many tokens 2.2; 8 MB lie between that and the others).  Narrow units: 24 bytes, 128 threads (8192 tokens, 8 rows of 1027 bf16 37 us,
       // with 32 bytes 49 and with 8 39; 3001 tokens, 5 rows of 1027 f32 12.5 us, with 32 bytes 13.1 and with
       // 16 14.6; 8192 tokens, 2 rows of 2047 f32 32 us, with 64 threads 48).
       auto go = [&](auto per, auto batch, auto threads) -> cudaError_t {
@@ -502,9 +503,9 @@ cudaError_t combine_backward(const void* dout, const void* in, int64_t tokens, i
       constexpr bool kWide = sizeof(U) == 16;
       constexpr int kPer = units_of<U>(kWide ? 32 : sizeof(U) == 2 ? 16 : 24);
       // 4 warps a token leave the fewest idle at a token's ends; tokens that do not fill the SMs with them
-      // (8 CTAs of each of 152) have as many as the row has columns for, up to 16 (8 rows of 7168 bf16:
+      // (8 CTAs on each of 152) have as many as the row has columns for, up to 16 (8 rows of 7168 bf16:
       // 64 tokens 6 us, with four warps 14; 608 tokens 24, with four 29; 1216 tokens 49 with either)
-      const bool few = tokens <= 1216;
+      const bool few = tokens <= 8 * 152;
       const int64_t warps = (units + 32 * kPer - 1) / (32 * kPer), most = few ? 16 : 4;
       auto kern = few ? combine_backward_kernel<U, T, kPer, 1, 16> : combine_backward_kernel<U, T, kPer, 1, 4>;
       if constexpr (kWide) {

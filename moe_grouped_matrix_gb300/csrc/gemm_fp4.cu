@@ -218,9 +218,13 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 
 // Tells the leader that this CTA's scales of a stage are turned: a copy of 16 bytes to the same place
-// there, whose arrival counts on the leader's barrier.  The copy is an operation of the async proxy,
-// ordered after the turned scales by the fence before it, as the MMA's reading of them has to be; an
-// mbarrier arrive with release at cluster scope took 1570 cycles here, this takes 140.
+// there, whose bytes count on the leader's barrier.  The order that is relied on: each lane's turned
+// scales, its proxy fence, the warp's synchronisation, this copy (of the async proxy, so after the fence),
+// the copy's completion (a release at cluster scope on the barrier), the leader's wait (an acquire), the
+// tcgen05.cp that reads the scales.  Each step but one is documented as such: that the completion's
+// release carries, beside the copy itself, what precedes the copy.  An mbarrier arrive with release at
+// cluster scope would not need that step, but it takes 1570 cycles for this copy's 140: prefill 752 us
+// for 596, 128 experts 104 for 84; with a warp for each window 698 and 102, with 8 windows 662 and 96.
 constexpr uint32_t kSignalBytes = 16;
 __device__ __forceinline__ void signal_leader(uint32_t addr, uint32_t bar) {
   asm volatile(

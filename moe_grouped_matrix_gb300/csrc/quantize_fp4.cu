@@ -405,8 +405,11 @@ cudaError_t quantize_as(const QuantParams& p, bool wide, cudaStream_t s) {
 
 // Threads a row and units a thread that cover a row's whole windows.  With many rows a thread takes
 // 4 units, so that a row of up to 2048 values is one warp's, with no barrier, and one of 4096 two
-// warps' (16384 rows of 4096 bf16 to NVFP4: 31 us, one unit a thread 41 us); with few rows one unit
-// a thread, for the latency (4096 rows of 2048 in expert order: 12.3 us, 4 units 14.3 us).
+// warps' (16384 rows of 4096 bf16 to NVFP4: 28.7 us, one unit a thread 38.9 us); with few rows one unit
+// a thread, for the latency (4096 rows of 2048 in expert order, 4 rows each: 8.3 us, 4 units 10.6 us).
+// The two meet at some 5000 rows of 1536 or 2048 values, at 10000 of them in expert order, and at 3000 rows
+// of 4096: 8192 lies among these (12288 rows of 2048 in expert order 22.0 us, as few 22.3; 6144 rows of
+// 2048 8.6 us, as many 8.1; of 4096 15.7, as many 12.6, which it gives away).
 template <class T, bool kNv>
 cudaError_t quantize(const QuantParams& p, cudaStream_t s) {
   const bool wide = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ld * sizeof(T) % 16 == 0;

@@ -67,8 +67,9 @@ class ExpertOrder(NamedTuple):
 class Fp4Tensor(NamedTuple):
     """Matrices [.., rows, k] of e2m1 codes: codes uint8 [.., rows, k / 2] (even k in the low
     nibble), block_scale uint8 [.., windows, rows, 16] (16 blocks a window; e4m3 bytes a block of
-    16 for "nvfp4", E8M0 bytes a block of 32 for "mxfp4"), row_scale float32 [.., rows] ("nvfp4")
-    or None."""
+    16 for "nvfp4", E8M0 bytes a block of 32 for "mxfp4"; bytes past the last block are 0: gmm_fp4()
+    reads whole windows, and a NaN there would reach its sums), row_scale float32 [.., rows]
+    ("nvfp4") or None."""
     codes: torch.Tensor
     block_scale: torch.Tensor
     row_scale: Optional[torch.Tensor]
@@ -448,7 +449,7 @@ def gmm_fp4(lhs, rhs, group_sizes, rhs_bias=None, group_offset=0, out=None, out_
     """out[r] = lhs[r] @ W_g^T for each row r of local group g, all other rows zero, as gmm() with the
     NT layout: lhs an Fp4Tensor [m, k], rhs an Fp4Tensor [G_local, n, k] of the same format, on the
     block-scaled 4-bit tensor cores.  k must be a multiple of 32 and n of 8; rhs_bias
-    [G_local, 1, n] bfloat16 or float32."""
+    [G_local, 1, n] bfloat16 or float32; group_offset an int (gmm()'s may be on the device)."""
     if stream is None and rhs_bias is None and out is None and lhs.format == rhs.format and lhs.codes.is_cuda:
         ws = workspace
         if ws is None:
