@@ -512,3 +512,9 @@ from .moe import (MAX_TOPK, ExpertOrder, Fp4Tensor, combine, combine_backward, d
 
 __all__ += ["MAX_TOPK", "ExpertOrder", "Fp4Tensor", "combine", "combine_backward", "dequantize_fp4", "dispatch",
             "dispatch_backward", "gmm_fp4", "quantize_fp4", "route", "route_backward", "sort_by_expert"]
+
+from .experts import (BalanceLoss, Int4Tensor, balance_loss, balance_loss_backward, dequantize_int4,  # noqa: E402
+                      gated_act, gated_act_backward, matvec_int4, quantize_int4)
+
+__all__ += ["BalanceLoss", "Int4Tensor", "balance_loss", "balance_loss_backward", "dequantize_int4", "gated_act",
+            "gated_act_backward", "matvec_int4", "quantize_int4"]
