@@ -100,7 +100,8 @@ int gmm_gated_act_backward(const void* dout, const void* h, int dtype, int64_t r
 int gmm_quantize_int4(const void* x, int x_dtype, int32_t batch, int64_t rows_per_batch, int64_t k, int64_t x_ld,
                       int32_t group, void* codes, void* scale, void* zero, void* stream);
 
-/* The values that a quantised matrix stands for, rounded once to out_dtype (BF16 or F32). */
+/* The values that a quantised matrix stands for, rounded once to out_dtype (BF16 or F32).  codes
+ * 4-byte aligned, scale 2-byte. */
 int gmm_dequantize_int4(const void* codes, const void* scale, const void* zero, int32_t group, int32_t batch,
                         int64_t rows_per_batch, int64_t k, void* out, int out_dtype, void* stream);
 

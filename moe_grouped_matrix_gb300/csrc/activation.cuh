@@ -15,9 +15,11 @@ __device__ __forceinline__ float act_inner(float g) {
   return kAct == GMM_ACT_SILU ? g : kGeluTwice * (g + kGeluCube * g * g * g);
 }
 
+// exp(-|x|) does not overflow, so what it scales keeps its precision down to fp32's least numbers.
 template <int kAct>
 __device__ __forceinline__ float act_value(float g) {
-  return g / (1.f + expf(-act_inner<kAct>(g)));
+  const float x = act_inner<kAct>(g), e = expf(-fabsf(x));
+  return (x < 0.f ? g * e : g) / (1.f + e);
 }
 
 // act(g) and its derivative s + g s (1 - s) x'(g), s = 1 / (1 + exp(-x)).  With e = exp(-|x|) both s and

@@ -450,7 +450,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
   if (out_dtype != GMM_DTYPE_BF16 && out_dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
   if (tokens < 0 || tokens > kMaxSize || k < 1 || k > kMaxSize || n < 1 || n > kMaxSize || n % 8 != 0 ||
       (group != 32 && group != 64 && group != 128) || k % group != 0 || num_experts < 1 ||
-      num_experts > GMM_MAX_GROUPS || topk < 1 || topk > GMM_MAX_TOPK || (experts == nullptr && topk != 1) ||
+      num_experts > GMM_MAX_GROUPS || topk < 1 || topk > GMM_MAX_TOPK || (tokens > 0 && experts == nullptr && topk != 1) ||
       (act != GMM_ACT_NONE && act != GMM_ACT_SILU && act != GMM_ACT_GELU))
     return GMM_ERR_SHAPE;
   if (act != GMM_ACT_NONE && (n % 16 != 0 || weights != nullptr)) return GMM_ERR_SHAPE;

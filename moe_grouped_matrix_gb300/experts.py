@@ -258,6 +258,11 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
         _want(weights, "weights", torch.float32, (x.shape[0], topk))
         front = front[:1]
     code = 0 if act is None else _act(act)
+    step = 8 if act is None else 16
+    if n < 1 or n % step:
+        raise ValueError(f"n must be a multiple of {step}, got {n}")
+    if ld % 8:
+        raise ValueError("x must have a row pitch that is a multiple of 8")
     with _on_stream(stream):
         out = torch.empty(front + (n if act is None else n // 2,), dtype=out_dtype, device=x.device)
     _run("gmm_matvec_int4", _lib().gmm_matvec_int4(
