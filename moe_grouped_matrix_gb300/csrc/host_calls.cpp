@@ -18,7 +18,7 @@
 
 #include <initializer_list>
 
-#include "../../include/libgmm_moe.h"
+#include "../../include/libgmm_experts.h"
 
 namespace {
 
@@ -33,6 +33,14 @@ struct Calls {
   decltype(&gmm_quantize_fp4) quantize;
   decltype(&gmm_dequantize_fp4) dequantize;
   decltype(&gmm_fp4) fp4;
+  decltype(&gmm_balance_scratch_bytes) balance_scratch;
+  decltype(&gmm_balance_loss) balance;
+  decltype(&gmm_balance_loss_backward) balance_backward;
+  decltype(&gmm_gated_act) gated;
+  decltype(&gmm_gated_act_backward) gated_backward;
+  decltype(&gmm_quantize_int4) quantize_int4;
+  decltype(&gmm_dequantize_int4) dequantize_int4;
+  decltype(&gmm_matvec_int4) matvec_int4;
 } g_calls{};
 
 using at::Tensor;
@@ -343,6 +351,178 @@ PyObject* gmm_fp4_call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A token mask: none, or a byte for each token.
+bool mask_ok(PyObject* o, const Tensor* mask, int64_t tokens) {
+  return o == Py_None || dense(mask, at::kBool, {tokens}) || dense(mask, kU8, {tokens});
+}
+
+// balance_loss(logits, experts, score, token_mask, sequences) -> (losses, counts, tokens)
+PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) return no_answer();
+    const Tensor *logits = tensor(a[0]), *chosen = tensor(a[1]), *mask = tensor(a[3]);
+    const int64_t ld = pitch(logits);
+    if (ld < 0 || chosen == nullptr || chosen->dim() != 2) return no_answer();
+    const int64_t tokens = logits->size(0), experts = logits->size(1), topk = chosen->size(1);
+    bool ok = experts >= 1 && experts <= GMM_MAX_GROUPS && topk >= 1 && topk <= GMM_MAX_TOPK;
+    const int64_t score = integer(a[2], 0, 1, &ok), sequences = integer(a[4], 1, INT32_MAX, &ok);
+    if (!ok || tokens % sequences != 0 || !dense(chosen, kI32, {tokens, topk}) || !mask_ok(a[3], mask, tokens) ||
+        !here({logits, chosen, mask}))
+      return no_answer();
+    const size_t bytes = g_calls.balance_scratch(tokens, int32_t(experts), sequences);
+    Tensor losses = empty({2}, kF32, *logits), counts = empty({sequences, experts}, kI32, *logits),
+           counted = empty({1}, kI32, *logits), scratch = empty({int64_t(bytes)}, kU8, *logits);
+    const int st = g_calls.balance(logits->data_ptr(), code_of(*logits), tokens, int32_t(experts), ld,
+                                   ptr<int32_t>(*chosen), int32_t(topk), int(score), ptr_or_null<uint8_t>(mask),
+                                   sequences, ptr<float>(losses), ptr<int32_t>(counts), ptr<int32_t>(counted),
+                                   scratch.data_ptr(), bytes, stream_of(*logits));
+    return answer(st, {losses, counts, counted});
+  });
+}
+
+// balance_loss_backward(dlosses, counts, tokens, logits, score, token_mask) -> dlogits
+PyObject* balance_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) return no_answer();
+    const Tensor *dlosses = tensor(a[0]), *counts = tensor(a[1]), *counted = tensor(a[2]), *logits = tensor(a[3]),
+                 *mask = tensor(a[5]);
+    const int64_t ld = pitch(logits);
+    if (ld < 0 || counts == nullptr || counts->dim() != 2) return no_answer();
+    const int64_t tokens = logits->size(0), experts = logits->size(1), sequences = counts->size(0);
+    bool ok = experts >= 1 && experts <= GMM_MAX_GROUPS && sequences >= 1;
+    const int64_t score = integer(a[4], 0, 1, &ok);
+    if (!ok || tokens % sequences != 0 || !dense(counts, kI32, {sequences, experts}) || !dense(counted, kI32, {1}) ||
+        !dense(dlosses, kF32, {2}) || !mask_ok(a[5], mask, tokens) || !here({dlosses, counts, counted, logits, mask}))
+      return no_answer();
+    Tensor dlogits = empty({tokens, experts}, logits->scalar_type(), *logits);
+    const int st = g_calls.balance_backward(ptr<float>(*dlosses), ptr<int32_t>(*counts), ptr<int32_t>(*counted),
+                                            logits->data_ptr(), code_of(*logits), tokens, int32_t(experts), ld,
+                                            int(score), ptr_or_null<uint8_t>(mask), sequences, dlogits.data_ptr(),
+                                            stream_of(*logits));
+    return answer(st, {dlogits});
+  });
+}
+
+// gated_act(h, act) -> out
+PyObject* gated_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 2) return no_answer();
+    const Tensor* h = tensor(a[0]);
+    const int64_t ld = pitch(h);
+    bool ok = ld >= 0 && h->size(1) >= 2 && h->size(1) % 2 == 0;
+    const int64_t act = integer(a[1], 1, 2, &ok);
+    if (!ok || !here({h})) return no_answer();
+    const int64_t rows = h->size(0), f = h->size(1) / 2;
+    Tensor out = empty({rows, f}, h->scalar_type(), *h);
+    const int st = g_calls.gated(h->data_ptr(), code_of(*h), rows, f, ld, int(act), out.data_ptr(), stream_of(*h));
+    return answer(st, {out});
+  });
+}
+
+// gated_act_backward(dout, h, act) -> dh
+PyObject* gated_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 3) return no_answer();
+    const Tensor *dout = tensor(a[0]), *h = tensor(a[1]);
+    const int64_t ld = pitch(h);
+    bool ok = ld >= 0 && h->size(1) >= 2 && h->size(1) % 2 == 0;
+    const int64_t act = integer(a[2], 1, 2, &ok);
+    if (!ok) return no_answer();
+    const int64_t rows = h->size(0), f = h->size(1) / 2;
+    if (!dense(dout, h->scalar_type(), {rows, f}) || !here({dout, h})) return no_answer();
+    Tensor dh = empty({rows, 2 * f}, h->scalar_type(), *h);
+    const int st = g_calls.gated_backward(dout->data_ptr(), h->data_ptr(), code_of(*h), rows, f, ld, int(act),
+                                          dh.data_ptr(), stream_of(*h));
+    return answer(st, {dh});
+  });
+}
+
+bool int4_group(int64_t group) { return group == 32 || group == 64 || group == 128; }
+
+// quantize_int4(x, group, zero points) -> (codes, scale, zero or None); 2-D x
+PyObject* quantize_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 3) return no_answer();
+    const Tensor* x = tensor(a[0]);
+    const int64_t ld = pitch(x);
+    bool ok = ld >= 0;
+    const int64_t group = integer(a[1], 32, 128, &ok), zeros = integer(a[2], 0, 1, &ok);
+    if (!ok || !int4_group(group) || x->size(1) < 1 || x->size(1) % group != 0 || !here({x})) return no_answer();
+    const int64_t rows = x->size(0), k = x->size(1), windows = (k + 255) / 256, each = 256 / group;
+    Tensor codes = empty({rows, k / 2}, kU8, *x), scale = empty({windows, rows, each}, kBF16, *x), zero;
+    if (zeros) zero = empty({windows, rows, each}, kU8, *x);
+    const int st = g_calls.quantize_int4(x->data_ptr(), code_of(*x), 1, rows, k, ld, int32_t(group), codes.data_ptr(),
+                                         scale.data_ptr(), zeros ? zero.data_ptr() : nullptr, stream_of(*x));
+    return answer(st, {codes, scale, zero});
+  });
+}
+
+// An Int4Tensor's parts with `lead` leading dimensions: its sizes, or false.
+bool int4_of(const Tensor* codes, const Tensor* scale, const Tensor* zero, bool has_zero, int64_t group, int lead,
+             int64_t* batch, int64_t* rows, int64_t* k) {
+  if (codes == nullptr || codes->dim() != lead + 2 || !int4_group(group)) return false;
+  *batch = lead != 0 ? codes->size(0) : 1;
+  *rows = codes->size(lead), *k = 2 * codes->size(lead + 1);
+  if (*k < 1 || *k % group != 0) return false;
+  const int64_t w = (*k + 255) / 256, each = 256 / group;
+  return lead != 0 ? dense(codes, kU8, {*batch, *rows, *k / 2}) && dense(scale, kBF16, {*batch, w, *rows, each}) &&
+                         (!has_zero || dense(zero, kU8, {*batch, w, *rows, each}))
+                   : dense(codes, kU8, {*rows, *k / 2}) && dense(scale, kBF16, {w, *rows, each}) &&
+                         (!has_zero || dense(zero, kU8, {w, *rows, each}));
+}
+
+// dequantize_int4(codes, scale, zero, group, out is f32) -> values; 2-D
+PyObject* dequantize_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) return no_answer();
+    const Tensor *codes = tensor(a[0]), *scale = tensor(a[1]), *zero = tensor(a[2]);
+    bool ok = true;
+    const int64_t group = integer(a[3], 32, 128, &ok), f32 = integer(a[4], 0, 1, &ok);
+    int64_t batch, rows, k;
+    if (!ok || !int4_of(codes, scale, zero, a[2] != Py_None, group, 0, &batch, &rows, &k) || !here({codes, scale, zero}))
+      return no_answer();
+    Tensor out = empty({rows, k}, f32 ? kF32 : kBF16, *codes);
+    const int st = g_calls.dequantize_int4(codes->data_ptr(), scale->data_ptr(), ptr_or_null<uint8_t>(zero),
+                                           int32_t(group), 1, rows, k, out.data_ptr(), code_of(out), stream_of(*codes));
+    return answer(st, {out});
+  });
+}
+
+// matvec_int4(x, codes, scale, zero, group, experts, weights, act, out is f32) -> out; with experts
+PyObject* matvec_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 9) return no_answer();
+    const Tensor *x = tensor(a[0]), *codes = tensor(a[1]), *scale = tensor(a[2]), *zero = tensor(a[3]),
+                 *chosen = tensor(a[5]), *weights = tensor(a[6]);
+    bool ok = x != nullptr && chosen != nullptr && chosen->dim() == 2;
+    const int64_t group = integer(a[4], 32, 128, &ok), act = integer(a[7], 0, 2, &ok), f32 = integer(a[8], 0, 1, &ok);
+    int64_t num, rows, k;
+    if (!ok || !int4_of(codes, scale, zero, a[3] != Py_None, group, 1, &num, &rows, &k)) return no_answer();
+    const int64_t tokens = chosen->size(0), topk = chosen->size(1);
+    const bool sums = a[6] != Py_None, slots = x->dim() == 3;
+    if (topk < 1 || topk > GMM_MAX_TOPK || num < 1 || num > GMM_MAX_GROUPS || rows < 1 ||
+        rows % (act != 0 ? 16 : 8) != 0 || (act != 0 && sums) || !dense(chosen, kI32, {tokens, topk}) ||
+        (sums && !dense(weights, kF32, {tokens, topk})) || x->scalar_type() != kBF16 ||
+        !here({x, codes, scale, zero, chosen, weights}))
+      return no_answer();
+    int64_t ld = k;
+    if (slots) {
+      if (!dense(x, kBF16, {tokens, topk, k})) return no_answer();
+    } else {
+      ld = pitch(x);
+      if (ld < 0 || ld % 8 != 0 || x->size(0) != tokens || x->size(1) != k) return no_answer();
+    }
+    const int64_t out_n = act != 0 ? rows / 2 : rows;
+    const auto type = f32 ? kF32 : kBF16;
+    Tensor out = sums ? empty({tokens, out_n}, type, *x) : empty({tokens, topk, out_n}, type, *x);
+    const int st = g_calls.matvec_int4(x->data_ptr(), tokens, k, ld, slots, codes->data_ptr(), scale->data_ptr(),
+                                       ptr_or_null<uint8_t>(zero), int32_t(group), int32_t(num), rows,
+                                       ptr<int32_t>(*chosen), int32_t(topk), ptr_or_null<float>(weights), int(act),
+                                       out.data_ptr(), code_of(out), stream_of(*x));
+    return answer(st, {out});
+  });
+}
+
 // bind(addresses of the C ABI's functions, in the order of Calls)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void** to = reinterpret_cast<void**>(&g_calls);
@@ -372,6 +552,13 @@ PyMethodDef g_methods[] = {method("bind", bind),
                            method("quantize_fp4", quantize_fp4),
                            method("dequantize_fp4", dequantize_fp4),
                            method("gmm_fp4", gmm_fp4_call),
+                           method("balance_loss", balance_loss),
+                           method("balance_loss_backward", balance_loss_backward),
+                           method("gated_act", gated_act),
+                           method("gated_act_backward", gated_act_backward),
+                           method("quantize_int4", quantize_int4),
+                           method("dequantize_int4", dequantize_int4),
+                           method("matvec_int4", matvec_int4),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_host_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

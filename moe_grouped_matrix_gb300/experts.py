@@ -20,7 +20,8 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _I, _I32, _I64, _P, _SZ, SIGNATURES, _dev, _on_stream
-from .moe import MAX_TOPK, _float_code, _lib, _on, _ptr, _rows, _run, _score, _want
+from . import moe as _moe
+from .moe import _OUT_F32, MAX_TOPK, SCORES, _float_code, _lib, _on, _ptr, _rows, _run, _score, _want
 
 __all__ = ["BalanceLoss", "balance_loss", "balance_loss_backward", "gated_act", "gated_act_backward", "Int4Tensor",
            "quantize_int4", "dequantize_int4", "matvec_int4"]
@@ -74,6 +75,11 @@ def balance_loss(logits, experts, score="softmax", token_mask=None, sequences=1,
     tokens of <f, p>, and the z loss the mean of logsumexp(logits)^2.  The tokens are `sequences` runs
     of equal length, each with loads of its own.  Tokens whose token_mask (bool or uint8 [tokens]) is
     0, or whose logits are all -inf, do not count; slots outside [0, E) are dropped."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).balance_loss(logits, experts, SCORES.get(score), token_mask, sequences)
+        if got.__class__ is tuple:
+            return BalanceLoss._make(got)
+        _run("gmm_balance_loss", got)
     ld = _rows(logits, "logits")
     code = _float_code(logits, "logits")
     tokens, n = logits.shape
@@ -103,6 +109,12 @@ def balance_loss_backward(dlosses, balance, logits, score="softmax", token_mask=
     """Gradient of <dlosses, balance.losses> with respect to the logits, [tokens, E] of their dtype:
     dlosses float32 [2] (the losses' coefficients times the gradient they get), balance the
     BalanceLoss of these logits with the same score and token_mask."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).balance_loss_backward(dlosses, balance.counts, balance.tokens, logits,
+                                                                  SCORES.get(score), token_mask)
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_balance_loss_backward", got)
     ld = _rows(logits, "logits")
     code = _float_code(logits, "logits")
     tokens, n = logits.shape
@@ -138,6 +150,11 @@ def _halves(h):
 def gated_act(h, act="silu", stream=None):
     """act(h[:, :f]) * h[:, f:] in fp32, rounded once: [rows, f] from h [rows, 2 f] (bfloat16 or
     float32, rows may have a pitch); act "silu" or "gelu" (its tanh form)."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).gated_act(h, ACTS.get(act))
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_gated_act", got)
     ld, f = _halves(h)
     code = _float_code(h, "h")
     with _on_stream(stream):
@@ -149,6 +166,11 @@ def gated_act(h, act="silu", stream=None):
 
 def gated_act_backward(dout, h, act="silu", stream=None):
     """Gradient of gated_act() with respect to h, [rows, 2 f], from dout [rows, f] of h's dtype."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).gated_act_backward(dout, h, ACTS.get(act))
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_gated_act_backward", got)
     ld, f = _halves(h)
     code = _float_code(h, "h")
     _want(dout, "dout", h.dtype, (h.shape[0], f))
@@ -176,6 +198,11 @@ def quantize_int4(x, group=128, zero_points=False, stream=None):
     row, as an Int4Tensor; with zero_points a zero point for each, too, and codes 0 to 15.  x is
     [rows, k] (rows may have a pitch) or a dense [batch, rows, k], the experts' weights for
     matvec_int4()."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).quantize_int4(x, group, 1 if zero_points else 0)
+        if got.__class__ is tuple:
+            return Int4Tensor(*got, group)
+        _run("gmm_quantize_int4", got)
     code = _float_code(x, "x")
     if x.dim() == 3:
         _dev(x, "x")
@@ -210,6 +237,11 @@ def _int4_args(q, name):
 
 def dequantize_int4(q, out_dtype=torch.bfloat16, stream=None):
     """The values an Int4Tensor stands for, [.., rows, k] of out_dtype (bfloat16 or float32)."""
+    if stream is None:
+        got = (_moe._calls or _moe._bind()).dequantize_int4(q.codes, q.scale, q.zero, q.group, _OUT_F32.get(out_dtype))
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_dequantize_int4", got)
     lead, rows, k = _int4_args(q, "q")
     with _on_stream(stream):
         out = torch.empty(lead + (rows, k), dtype=out_dtype, device=q.codes.device)
@@ -231,6 +263,12 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
     Without experts w is one matrix [n, k] and h is [tokens, n].  Sums are fp32, rounded once to
     out_dtype (bfloat16 or float32).  Weights are read once for every 8 tokens of an expert (with
     weights, for every 8 tokens): for more than a few, sort the rows and use gmm()."""
+    if stream is None and experts is not None:
+        got = (_moe._calls or _moe._bind()).matvec_int4(x, w.codes, w.scale, w.zero, w.group, experts, weights,
+                                                        0 if act is None else ACTS.get(act), _OUT_F32.get(out_dtype))
+        if got.__class__ is torch.Tensor:
+            return got
+        _run("gmm_matvec_int4", got)
     lead, n, k = _int4_args(w, "w")
     if x.dim() not in (2, 3) or x.shape[-1] != k:
         raise ValueError(f"x must be [tokens, {k}] or [tokens, topk, {k}]")
