@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "internal.h"
@@ -33,7 +34,7 @@
 namespace gmmk {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kWindow = 256;                 // k of a stage
 constexpr int kCols = 8;                     // columns of an item
 constexpr int kMaxSlots = 512;               // slots of a launch
@@ -52,7 +53,8 @@ struct Params {
   int32_t act;            // of gated tiles
   void* out;
   int32_t out_n, out_f32;  // columns of out, its type
-  int32_t kw;             // warps to a tile: 2, 4 or 8
+  int32_t team_log2;      // of the warps to a tile
+  int32_t x_rows, x_pitch;  // kStaged: rows of x in shared memory, and elements between them
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
@@ -65,19 +67,18 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight bf16 as pairs (0, 4), (1, 5), (2, 6), (3, 7): those that one mask takes out of a word of codes.
+__device__ __forceinline__ uint4 in_pairs(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
 }
 
 // Two codes, at bits 0-3 and 16-19 of w, as bf16 with `off` = 128 + zero taken off.
@@ -89,11 +90,15 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, __nv_bfloat162 off) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A warp's ring: kStages windows' codes, then their scales, then their zero points.  Four stages are
+// some 128 KB on their way to an SM, well over the 45 that memory's latency asks for at its rate.
 template <int kGroup, bool kZero>
-struct Stage {
-  static constexpr int kEach = kWindow / kGroup;
-  static constexpr int kScale = kCodeBytes, kZeros = kScale + 16 * kEach * 2;
-  static constexpr int kBytes = kZeros + (kZero ? 16 * kEach : 0);
+struct Ring {
+  static constexpr int kEach = kWindow / kGroup;  // groups of a window
+  static constexpr int kScales = 16 * kEach * 2, kZeros = kZero ? 16 * kEach : 0;
+  static constexpr int kStages = 4;
+  static constexpr int kBytes = kStages * (kCodeBytes + kScales + kZeros);
+  static_assert(kBytes % 128 == 0, "rows of codes are whole lines of banks");
 };
 
 // The table of items that each CTA makes of the slots.
@@ -105,17 +110,20 @@ struct Table {
   int32_t warp_heads[kWarps];
 };
 
-// Where a warp is in its sequence of (unit, pair of item and window).
-struct Place {
-  int64_t unit;
-  int32_t pair, end;       // of the warp in the unit
-  int32_t item, window;
-  int64_t half0, half1;    // expert * n + first row of each half tile; half1 < 0: none
+// A team's place among the units: a group of items (one, or with weights those of 8 tokens) and a tile.
+struct Unit {
+  int32_t group, tile;
+  // on by dgroup * tiles + dtile units
+  __device__ __forceinline__ void advance(int dgroup, int dtile, int tiles) {
+    group += dgroup, tile += dtile;
+    if (tile >= tiles) tile -= tiles, ++group;
+  }
 };
 
-template <int kGroup, bool kZero, bool kGated, bool kSum, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(Params p) {
-  using S = Stage<kGroup, kZero>;
+template <int kGroup, bool kZero, bool kGated, bool kSum, bool kStaged>
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
+  using R = Ring<kGroup, kZero>;
+  constexpr int kStages = R::kStages, kEach = R::kEach;
   griddep_begin();
   p.x = after_begin(p.x), p.codes = after_begin(p.codes), p.scale = after_begin(p.scale);
   p.zero = after_begin(p.zero), p.chosen = after_begin(p.chosen), p.weights = after_begin(p.weights);
@@ -124,7 +132,6 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(Params p) {
   __shared__ float part[2][kWarps][16][kCols + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slots = p.tokens * p.topk;
-  const int KW = p.kw, kTiles = kWarps / KW;  // tiles of a unit
 
   // ---- items: slots of the same expert in their order, 8 at a time (kSum: those of 8 tokens; a
   // token's second slot of the same expert has an item of its own).  A head is an item's first slot.
@@ -220,183 +227,212 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(Params p) {
     }
   }
 
-  // ---- the warp's sequence
-  const int tile_units = (p.tiles + kTiles - 1) / kTiles;
-  const int64_t units = int64_t(kSum ? chunks : table.items) * tile_units;
-  const int kw = warp % KW;
-  const uint32_t ring = smem_u32(smem) + uint32_t(warp) * (kStages * S::kBytes);
-
-  auto halves = [&](Place& at) {  // of the tile, in the item's expert
-    const int tile = int(at.unit % tile_units) * kTiles + warp / KW;
-    const int64_t base = int64_t(table.expert[at.item]) * p.n;
-    if constexpr (kGated) {
-      at.half0 = base + tile * 8, at.half1 = base + p.n / 2 + tile * 8;
-    } else {
-      at.half0 = base + tile * 16, at.half1 = tile * 16 + 8 < p.n ? base + tile * 16 + 8 : -1;
-    }
+  // ---- the warp's part of its team's units, in order: pairs of an item and a window
+  const int lg = p.team_log2, size = 1 << lg;    // warps of a team
+  const int member = warp & (size - 1), team = warp >> lg;
+  const int teams = int(gridDim.x) * (kWarps >> lg);  // of all CTAs; a CTA's are far apart
+  const int groups = kSum ? chunks : table.items;
+  const int start = int(blockIdx.x) + team * int(gridDim.x);
+  const int dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
+  Unit ahead{start / p.tiles, 0};
+  ahead.tile = start - ahead.group * p.tiles;
+  Unit here = ahead;
+  uint8_t* const ring = smem + warp * R::kBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  // the pairs of a unit that are this warp's: [begin, end) of its items' windows
+  auto part_of = [&](const Unit& u, int& first, int& begin, int& end) {
+    first = kSum ? table.first[u.group] : u.group;
+    const int64_t pairs = int64_t(kSum ? table.first[u.group + 1] - first : 1) * p.windows;
+    begin = int((pairs * member) >> lg), end = int((pairs * (member + 1)) >> lg);
   };
-  // The first pair of a unit, or of the next that has any for this warp.
-  auto enter = [&](Place& at) {
-    for (; at.unit < units; at.unit += gridDim.x) {
-      const int group = int(at.unit / tile_units), tile = int(at.unit % tile_units) * kTiles + warp / KW;
-      const int first = kSum ? table.first[group] : group, n = kSum ? table.first[group + 1] - first : 1;
-      const int pairs = tile < p.tiles ? n * p.windows : 0;
-      at.pair = int(int64_t(pairs) * kw / KW), at.end = int(int64_t(pairs) * (kw + 1) / KW);
-      if (at.pair < at.end) {
-        at.item = first + at.pair / p.windows, at.window = at.pair % p.windows;
-        halves(at);
+
+  // what is fetched ahead: its pair, and where this lane's pieces are
+  const int lane_row = lane >> 3, lane_chunk = lane & 7;
+  constexpr int kHalfScales = 8 * kEach * 2 / 16, kHalfZeros = kZero ? 8 * kEach / 16 : 1;  // pieces of 8 rows'
+  const int64_t pitch = p.k / 2, scale_step = int64_t(p.n) * kEach * 2;
+  int pair = 0, pair_end = 0, item = 0, window = 0;
+  bool second = false;  // the tile has its second 8 rows
+  const uint8_t *code0 = nullptr, *code1 = nullptr, *scale = nullptr, *zero = nullptr;
+  auto aim = [&] {
+    const int64_t e = table.expert[item];
+    const int row0 = kGated ? ahead.tile * 8 : ahead.tile * 16;
+    second = kGated || row0 + 8 < p.n;
+    const int row1 = !second ? row0 : kGated ? p.n / 2 + row0 : row0 + 8;
+    const uint8_t* at = p.codes + (e * p.n + lane_row) * pitch + int64_t(window) * (kWindow / 2) + lane_chunk * 16;
+    code0 = at + row0 * pitch, code1 = at + row1 * pitch;
+    const int64_t in_window = (e * p.windows + window) * p.n;
+    scale = p.scale + (in_window + (lane < kHalfScales ? row0 : row1)) * (kEach * 2) + lane % kHalfScales * 16;
+    if constexpr (kZero) zero = p.zero + (in_window + (lane < kHalfZeros ? row0 : row1)) * kEach + lane % kHalfZeros * 16;
+  };
+  auto enter = [&] {
+    while (ahead.group < groups) {
+      int first;
+      part_of(ahead, first, pair, pair_end);
+      if (pair < pair_end) {
+        const int skip = kSum ? pair / p.windows : 0;
+        item = first + skip, window = pair - skip * p.windows;
+        aim();
         return;
       }
+      ahead.advance(dgroup, dtile, p.tiles);
     }
   };
-  auto next = [&](Place& at) {
-    if (++at.pair == at.end) {
-      at.unit += gridDim.x;
-      enter(at);
-    } else if (++at.window == p.windows) {
-      at.window = 0, ++at.item;
-      halves(at);
-    }
-  };
-  auto fetch = [&](const Place& at, int stage) {
-    const uint32_t to = ring + uint32_t(stage) * S::kBytes;
-    const int chunk = lane & 7;
-    const bool in = at.window * kWindow + chunk * 32 < p.k;
-    const int64_t pitch = p.k / 2, off = int64_t(at.window) * (kWindow / 2) + (in ? chunk * 16 : 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 4 + (lane >> 3);
-      const bool there = in && (i < 2 || at.half1 >= 0);
-      const int64_t r = (i < 2 || at.half1 < 0 ? at.half0 : at.half1) + (row & 7);
-      copy16(to + row * 128 + ((chunk ^ (row & 7)) << 4), p.codes + r * pitch + off, there);
-    }
-    // scales and zero points: 8 rows' are contiguous.  half = (expert, row) -> (expert, window, row)
-    auto at_window = [&](int64_t half) {
-      const int64_t e = table.expert[at.item];
-      return (e * p.windows + at.window) * p.n + (half - e * p.n);
-    };
-    constexpr int kHalf = 8 * S::kEach;  // values of half a tile
-    const int which = lane / (kHalf / 8), piece = lane % (kHalf / 8);
-    if (which < 2) {
-      const int64_t half = which == 0 || at.half1 < 0 ? at.half0 : at.half1;
-      copy16(to + S::kScale + which * kHalf * 2 + piece * 16, p.scale + at_window(half) * (S::kEach * 2) + piece * 16,
-             which == 0 || at.half1 >= 0);
-    }
-    if constexpr (kZero) {
-      const int whichz = lane / (kHalf / 16), piecez = lane % (kHalf / 16);
-      if (whichz < 2) {
-        const int64_t half = whichz == 0 || at.half1 < 0 ? at.half0 : at.half1;
-        copy16(to + S::kZeros + whichz * kHalf + piecez * 16, p.zero + at_window(half) * S::kEach + piecez * 16,
-               whichz == 0 || at.half1 >= 0);
+  auto fetch = [&](int stage) {  // and on to the next
+    if (ahead.group < groups) {
+      const uint32_t to = ring_at + stage * kCodeBytes + lane_row * 128;
+      const int64_t k0 = int64_t(window) * kWindow + lane_chunk * 32;
+      const bool in = k0 < p.k;
+      const int64_t back = in ? 0 : -lane_chunk * 16;  // an address inside for what is not there
+      const uint32_t c0 = (lane_chunk ^ lane_row) << 4, c4 = c0 ^ 64;
+      copy16(to + c0, code0 + back, in);
+      copy16(to + 512 + c4, code0 + 4 * pitch + back, in);
+      copy16(to + 1024 + c0, code1 + back, in && second);
+      copy16(to + 1536 + c4, code1 + 4 * pitch + back, in && second);
+      if (lane < 2 * kHalfScales)
+        copy16(ring_at + kStages * kCodeBytes + stage * R::kScales + lane * 16, scale, lane < kHalfScales || second);
+      if constexpr (kZero)
+        if (lane < 2 * kHalfZeros)
+          copy16(ring_at + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros + lane * 16, zero,
+                 lane < kHalfZeros || second);
+      if (++pair == pair_end) {
+        ahead.advance(dgroup, dtile, p.tiles);
+        enter();
+      } else if (kSum && ++window == p.windows) {
+        window = 0, ++item;
+        aim();
+      } else {
+        if constexpr (!kSum) ++window;
+        code0 += kWindow / 2, code1 += kWindow / 2, scale += scale_step;
+        if constexpr (kZero) zero += scale_step / 2;
       }
     }
+    copies_commit();
   };
+  enter();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(s);
+
+  __nv_bfloat16* const staged = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
+  if constexpr (kStaged) {  // all of x, each 8 in the order of a word's pairs: 0 4 1 5 2 6 3 7
+    const int eights = p.k / 8;
+    for (int r = 0; r < p.x_rows; ++r) {
+      const __nv_bfloat16* row = p.x + (p.x_slot != 0 ? r * p.x_slot : r * p.x_token);
+      for (int i = tid; i < eights; i += kThreads)
+        *reinterpret_cast<uint4*>(staged + r * p.x_pitch + i * 8) = in_pairs(__ldg(reinterpret_cast<const uint4*>(row) + i));
+    }
+    __syncthreads();
+  }
 
   const int g = lane >> 2, t4 = lane & 3;
-  Place ahead, here;
-  ahead.unit = blockIdx.x;
-  enter(ahead);
-  here = ahead;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (ahead.unit < units) {
-      fetch(ahead, s);
-      next(ahead);
-    }
-    copies_commit();
-  }
   int stage = 0, parity = 0;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, parity ^= 1) {
-    float res[4] = {0.f, 0.f, 0.f, 0.f};
-    int item = -1;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const __nv_bfloat16* xp = nullptr;  // column g of the item
+  for (; here.group < groups; here.advance(dgroup, dtile, p.tiles), parity ^= 1) {
+    int first, at, end;
+    part_of(here, first, at, end);
+    int now = first + (kSum ? at / p.windows : 0), w = kSum ? at - (now - first) * p.windows : at;
+    float res[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const __nv_bfloat16* xp = nullptr;  // column g of the item, from this lane's k on
+    bool there = false;                 // a column without a slot is zeros
     float w0 = 1.f, w1 = 1.f;           // weights of columns 2 t4 and 2 t4 + 1
-    auto flush = [&] {
-      res[0] += w0 * acc[0], res[1] += w1 * acc[1], res[2] += w0 * acc[2], res[3] += w1 * acc[3];
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-    };
-    while (here.unit == unit) {
-      if (here.item != item) {
-        if (kSum && item >= 0) flush();
-        item = here.item;
-        const int s = table.slot[item][g];
-        xp = s < 0 ? nullptr : p.x + (s / p.topk) * p.x_token + (s % p.topk) * p.x_slot;
+    bool fresh = true;
+    for (; at < end; ++at) {
+      if (fresh) {
+        fresh = false;
+        const int s = table.slot[now][g];
+        there = s >= 0;
+        if constexpr (kStaged)
+          xp = staged + (p.x_slot != 0 ? s : s / p.topk) * p.x_pitch + t4 * 8;
+        else
+          xp = p.x + (s / p.topk) * p.x_token + (s % p.topk) * p.x_slot + t4 * 8;
         if constexpr (kSum) {
-          const int s0 = table.slot[item][2 * t4], s1 = table.slot[item][2 * t4 + 1];
+          const int s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
           w0 = s0 < 0 ? 0.f : p.weights[s0], w1 = s1 < 0 ? 0.f : p.weights[s1];
         }
       }
-      // x of this window for all groups
-      const int k0 = here.window * kWindow;
-      const int groups = min(S::kEach, (p.k - k0) / kGroup);
+      const int k0 = w * kWindow;
       copies_wait<kStages - 2>();
       __syncwarp();
-      if (ahead.unit < units) {
-        fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
-        next(ahead);
-      }
-      copies_commit();
-      const uint32_t at = ring + uint32_t(stage) * S::kBytes;
-#pragma unroll
-      for (int q = 0; q < S::kEach; ++q) {
-        if (q < groups) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t z0 = 8, z1 = 8;
-          if constexpr (kZero) {
-            z0 = smem[at - smem_u32(smem) + S::kZeros + g * S::kEach + q];
-            z1 = smem[at - smem_u32(smem) + S::kZeros + (g + 8) * S::kEach + q];
-          }
-          const uint32_t o0 = 0x43004300u + z0 * 0x00010001u, o1 = 0x43004300u + z1 * 0x00010001u;
-          const __nv_bfloat162 off0 = *reinterpret_cast<const __nv_bfloat162*>(&o0);
-          const __nv_bfloat162 off1 = *reinterpret_cast<const __nv_bfloat162*>(&o1);
-#pragma unroll
-          for (int j = 0; j < kGroup / 32; ++j) {
-            const int chunk = q * (kGroup / 32) + j;
-            uint4 b = make_uint4(0, 0, 0, 0);
-            if (xp != nullptr) b = __ldg(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32 + t4 * 8));
-            const uint32_t wa = lds32(at + g * 128 + ((chunk ^ g) << 4) + t4 * 4);
-            const uint32_t wb = lds32(at + (g + 8) * 128 + ((chunk ^ g) << 4) + t4 * 4);
-            mma(c, two_codes<kZero>(wa, off0), two_codes<kZero>(wb, off1), two_codes<kZero>(wa >> 4, off0),
-                two_codes<kZero>(wb >> 4, off1), __byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632));
-            mma(c, two_codes<kZero>(wa >> 8, off0), two_codes<kZero>(wb >> 8, off1), two_codes<kZero>(wa >> 12, off0),
-                two_codes<kZero>(wb >> 12, off1), __byte_perm(b.y, b.w, 0x5410), __byte_perm(b.y, b.w, 0x7632));
-          }
-          const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(smem + (at - smem_u32(smem)) + S::kScale);
-          const float s0 = __bfloat162float(sc[g * S::kEach + q]), s1 = __bfloat162float(sc[(g + 8) * S::kEach + q]);
-          acc[0] = fmaf(s0, c[0], acc[0]), acc[1] = fmaf(s0, c[1], acc[1]);
-          acc[2] = fmaf(s1, c[2], acc[2]), acc[3] = fmaf(s1, c[3], acc[3]);
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t* codes = ring + stage * kCodeBytes + g * 128 + t4 * 4;
+      using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
+      const uint8_t* scales = ring + kStages * kCodeBytes + stage * R::kScales;
+      Scales sa = reinterpret_cast<const Scales*>(scales)[g], sb = reinterpret_cast<const Scales*>(scales)[g + 8];
+      const uint8_t* zeros = ring + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros;
+      auto group = [&](int q) {
+        uint32_t o0 = 0x43084308u, o1 = 0x43084308u;
+        if constexpr (kZero) {
+          o0 = 0x43004300u + zeros[g * kEach + q] * 0x00010001u;
+          o1 = 0x43004300u + zeros[(g + 8) * kEach + q] * 0x00010001u;
         }
+        const __nv_bfloat162 off0 = *reinterpret_cast<const __nv_bfloat162*>(&o0);
+        const __nv_bfloat162 off1 = *reinterpret_cast<const __nv_bfloat162*>(&o1);
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains
+#pragma unroll
+        for (int j = 0; j < kGroup / 32; ++j) {
+          const int chunk = q * (kGroup / 32) + j;
+          uint4 b = make_uint4(0, 0, 0, 0);
+          if (there) {
+            if constexpr (kStaged)
+              b = *reinterpret_cast<const uint4*>(xp + k0 + chunk * 32);
+            else
+              b = in_pairs(__ldg(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32)));
+          }
+          const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + ((chunk ^ g) << 4));
+          const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 1024 + ((chunk ^ g) << 4));
+          mma(c[0], two_codes<kZero>(wa, off0), two_codes<kZero>(wb, off1), two_codes<kZero>(wa >> 4, off0),
+              two_codes<kZero>(wb >> 4, off1), b.x, b.y);
+          mma(c[1], two_codes<kZero>(wa >> 8, off0), two_codes<kZero>(wb >> 8, off1), two_codes<kZero>(wa >> 12, off0),
+              two_codes<kZero>(wb >> 12, off1), b.z, b.w);
+        }
+        const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[q / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[q / 2];
+        const float s0 = __uint_as_float(q % 2 ? pa & 0xFFFF0000u : pa << 16);
+        const float s1 = __uint_as_float(q % 2 ? pb & 0xFFFF0000u : pb << 16);
+        acc[0] = fmaf(s0, c[0][0] + c[1][0], acc[0]), acc[1] = fmaf(s0, c[0][1] + c[1][1], acc[1]);
+        acc[2] = fmaf(s1, c[0][2] + c[1][2], acc[2]), acc[3] = fmaf(s1, c[0][3] + c[1][3], acc[3]);
+      };
+      if (k0 + kWindow <= p.k) {
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) group(q);
+      } else {
+        const int left = (p.k - k0) / kGroup;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q)
+          if (q < left) group(q);
       }
-      __syncwarp();
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      next(here);
+      if (!kSum) {
+        ++w;
+      } else if (++w == p.windows || at + 1 == end) {
+        res[0] += w0 * acc[0], res[1] += w1 * acc[1], res[2] += w0 * acc[2], res[3] += w1 * acc[3];
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        if (w == p.windows) w = 0, ++now, fresh = true;
+      }
     }
-    flush();
-    part[parity][warp][g][2 * t4] = res[0], part[parity][warp][g][2 * t4 + 1] = res[1];
-    part[parity][warp][g + 8][2 * t4] = res[2], part[parity][warp][g + 8][2 * t4 + 1] = res[3];
-    __syncthreads();
-    // sums over the warps of a tile, and out
-    const int group = int(unit / tile_units), tile0 = int(unit % tile_units) * kTiles;
+    const float* sums = kSum ? res : acc;
+    part[parity][warp][g][2 * t4] = sums[0], part[parity][warp][g][2 * t4 + 1] = sums[1];
+    part[parity][warp][g + 8][2 * t4] = sums[2], part[parity][warp][g + 8][2 * t4 + 1] = sums[3];
+    if (lg == 0)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 << lg) : "memory");
+    // sums over the team's warps, and out
     constexpr int kRows = kGated ? 8 : 16;
-    for (int i = tid; i < kTiles * kRows * kCols; i += kThreads) {
-      const int row = i % kRows, tile = i / kRows % kTiles, col = i / (kRows * kTiles);
+    for (int i = member * 32 + lane; i < kRows * kCols; i += 32 << lg) {
+      const int row = i % kRows, col = i / kRows;
       int64_t to;
       if constexpr (kSum) {
-        const int t = group * kCols + col;
-        if (t >= p.tokens) continue;
-        to = t;
+        to = here.group * kCols + col;
+        if (to >= p.tokens) continue;
       } else {
-        to = table.slot[group][col];
+        to = table.slot[here.group][col];
         if (to < 0) continue;
       }
-      const int c = (tile0 + tile) * kRows + row;
+      const int64_t c = int64_t(here.tile) * kRows + row;
       if (c >= p.out_n) continue;
       float v = 0.f;
-      for (int w = 0; w < KW; ++w) v += part[parity][tile * KW + w][row][col];
+      for (int m = 0; m < size; ++m) v += part[parity][(team << lg) + m][row][col];
       if constexpr (kGated) {
         float u = 0.f;
-        for (int w = 0; w < KW; ++w) u += part[parity][tile * KW + w][row + 8][col];
+        for (int m = 0; m < size; ++m) u += part[parity][(team << lg) + m][row + 8][col];
         v = (p.act == GMM_ACT_SILU ? act_value<GMM_ACT_SILU>(v) : act_value<GMM_ACT_GELU>(v)) * u;
       }
       put(to, c, v);
@@ -405,16 +441,21 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(Params p) {
   copies_wait<0>();
 }
 
+constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * 2 * kWarps * 16 * (kCols + 1);
+
 template <int kGroup, bool kZero, bool kGated, bool kSum>
-cudaError_t launch(const Params& p, int64_t units, int sms, cudaStream_t stream) {
-  // two CTAs to an SM: 114 KB each, 21 of them the table and the sums
-  constexpr int kStages = 94000 / (kWarps * Stage<kGroup, kZero>::kBytes);
-  constexpr size_t smem = size_t(kWarps) * kStages * Stage<kGroup, kZero>::kBytes;
-  auto kern = matvec_kernel<kGroup, kZero, kGated, kSum, kStages>;
-  // set for every launch: the attribute is the current device's
-  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) return e;
-  const int64_t grid = units < 2 * sms ? units : 2 * sms;
-  return launch_dependent(kern, unsigned(grid < 1 ? 1 : grid), kThreads, smem, stream, 1, p);
+cudaError_t launch(Params p, int64_t units, int sms, cudaStream_t stream) {
+  size_t smem = size_t(kWarps) * Ring<kGroup, kZero>::kBytes;
+  // x goes to shared memory where it fits; rows half a line of banks apart
+  p.x_rows = p.x_slot != 0 ? p.tokens * p.topk : p.tokens;
+  const int64_t x_pitch = p.k % 64 == 0 ? int64_t(p.k) + 32 : p.k, x_bytes = p.x_rows * x_pitch * 2;
+  const bool staged = x_bytes <= int64_t(kMaxShared - smem);
+  if (staged) smem += size_t(x_bytes), p.x_pitch = int32_t(x_pitch);
+  auto kern = staged ? matvec_kernel<kGroup, kZero, kGated, kSum, true> : matvec_kernel<kGroup, kZero, kGated, kSum, false>;
+  // for every launch: the attribute is the current device's, and one size for all calls
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
+  const int64_t ctas = ((units << p.team_log2) + kWarps - 1) / kWarps;
+  return launch_dependent(kern, unsigned(ctas < sms ? ctas : sms), kThreads, smem, stream, 1, p);
 }
 
 template <int kGroup, bool kZero>
@@ -425,10 +466,17 @@ cudaError_t by_form(const Params& p, int64_t units, int sms, cudaStream_t stream
 }
 
 cudaError_t matvec(Params p, int group, int sms, cudaStream_t stream) {
-  p.kw = p.windows >= 8 ? 8 : p.windows >= 4 || p.weights != nullptr ? 4 : 2;
-  // units at most: an item for each slot, or 8 tokens
-  const int64_t groups = p.weights != nullptr ? (p.tokens + kCols - 1) / kCols : int64_t(p.tokens) * p.topk;
-  const int64_t units = groups * ((p.tiles + kWarps / p.kw - 1) / (kWarps / p.kw));
+  // units at most: a tile of each slot's expert, or of each 8 tokens with their experts one after another
+  const bool sums = p.weights != nullptr;
+  const int64_t units = int64_t(p.tiles) * (sums ? (p.tokens + kCols - 1) / kCols : p.tokens * p.topk);
+  const int64_t pairs = int64_t(p.windows) * (!sums ? 1 : (p.tokens < kCols ? p.tokens : kCols) * p.topk);
+  // warps to a tile: those with which the last team is done first, a unit's start and end counted as a window
+  int64_t best = INT64_MAX;
+  for (int lg = 0; (1 << lg) <= kWarps; ++lg) {
+    const int64_t teams = int64_t(sms) * (kWarps >> lg), rounds = (units + teams - 1) / teams;
+    const int64_t windows = rounds * (((pairs + (1 << lg) - 1) >> lg) + 1);
+    if (windows < best) best = windows, p.team_log2 = lg;
+  }
   const bool zero = p.zero != nullptr;
   switch (group) {
     case 32: return zero ? by_form<32, true>(p, units, sms, stream) : by_form<32, false>(p, units, sms, stream);
