@@ -61,6 +61,9 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there
   const int bytes = there ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -73,6 +76,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Eight bf16 as pairs (0, 4), (1, 5), (2, 6), (3, 7): those that one mask takes out of a word of codes.
@@ -105,6 +117,7 @@ struct Ring {
 struct Table {
   int32_t expert[kMaxSlots];          // of each slot; then of each item
   int16_t slot[kMaxSlots][kCols];     // of each item's columns; -1: none
+  int16_t head[kMaxSlots];            // of each item: its first slot
   int16_t first[kMaxSlots / kCols + kMaxSlots + 1];  // with weights: first item of each 8 tokens
   int32_t items;
   int32_t warp_heads[kWarps];
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     if constexpr (kSum) {
       if (i < slots && i % (kCols * p.topk) == 0) table.first[i / (kCols * p.topk)] = int16_t(at);
     }
-    if (is_head) number[i] = at, table.expert[at] = mine[r];  // at <= i: read above by all
+    if (is_head) number[i] = at, table.head[at] = int16_t(i), table.expert[at] = mine[r];  // at <= i: read above by all
     __syncthreads();
     if (tid == 0)
       for (int w = 0; w < kWarps; ++w) table.items += table.warp_heads[w];
@@ -249,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   // what is fetched ahead: its pair, and where this lane's pieces are
   const int lane_row = lane >> 3, lane_chunk = lane & 7;
   constexpr int kHalfScales = 8 * kEach * 2 / 16, kHalfZeros = kZero ? 8 * kEach / 16 : 1;  // pieces of 8 rows'
+  const uint32_t lane_at = lane_row * 128 + ((lane_chunk ^ lane_row) << 4);  // and rows 4 on: chunks ^ 4
+  const int whole = p.k / kWindow;
   const int64_t pitch = p.k / 2, scale_step = int64_t(p.n) * kEach * 2;
   int pair = 0, pair_end = 0, item = 0, window = 0;
   bool second = false;  // the tile has its second 8 rows
@@ -279,21 +294,28 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   };
   auto fetch = [&](int stage) {  // and on to the next
     if (ahead.group < groups) {
-      const uint32_t to = ring_at + stage * kCodeBytes + lane_row * 128;
-      const int64_t k0 = int64_t(window) * kWindow + lane_chunk * 32;
-      const bool in = k0 < p.k;
-      const int64_t back = in ? 0 : -lane_chunk * 16;  // an address inside for what is not there
-      const uint32_t c0 = (lane_chunk ^ lane_row) << 4, c4 = c0 ^ 64;
-      copy16(to + c0, code0 + back, in);
-      copy16(to + 512 + c4, code0 + 4 * pitch + back, in);
-      copy16(to + 1024 + c0, code1 + back, in && second);
-      copy16(to + 1536 + c4, code1 + 4 * pitch + back, in && second);
-      if (lane < 2 * kHalfScales)
-        copy16(ring_at + kStages * kCodeBytes + stage * R::kScales + lane * 16, scale, lane < kHalfScales || second);
-      if constexpr (kZero)
-        if (lane < 2 * kHalfZeros)
-          copy16(ring_at + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros + lane * 16, zero,
-                 lane < kHalfZeros || second);
+      const uint32_t to = ring_at + stage * kCodeBytes + lane_at;
+      const uint32_t to_scale = ring_at + kStages * kCodeBytes + stage * R::kScales + lane * 16;
+      const uint32_t to_zero = ring_at + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros + lane * 16;
+      if (second && window < whole) {
+        copy16(to, code0);
+        copy16((to ^ 64) + 512, code0 + 4 * pitch);
+        copy16(to + 1024, code1);
+        copy16((to ^ 64) + 1536, code1 + 4 * pitch);
+        if (lane < 2 * kHalfScales) copy16(to_scale, scale);
+        if constexpr (kZero)
+          if (lane < 2 * kHalfZeros) copy16(to_zero, zero);
+      } else {  // zeros for what is past k or n, with an address inside
+        const bool in = window * kWindow + lane_chunk * 32 < p.k;
+        const int64_t back = in ? 0 : lane_chunk * -16;
+        copy16(to, code0 + back, in);
+        copy16((to ^ 64) + 512, code0 + 4 * pitch + back, in);
+        copy16(to + 1024, code1 + back, in && second);
+        copy16((to ^ 64) + 1536, code1 + 4 * pitch + back, in && second);
+        if (lane < 2 * kHalfScales) copy16(to_scale, scale, lane < kHalfScales || second);
+        if constexpr (kZero)
+          if (lane < 2 * kHalfZeros) copy16(to_zero, zero, lane < kHalfZeros || second);
+      }
       if (++pair == pair_end) {
         ahead.advance(dgroup, dtile, p.tiles);
         enter();
@@ -331,21 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     int now = first + (kSum ? at / p.windows : 0), w = kSum ? at - (now - first) * p.windows : at;
     float res[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
     const __nv_bfloat16* xp = nullptr;  // column g of the item, from this lane's k on
-    bool there = false;                 // a column without a slot is zeros
-    float w0 = 1.f, w1 = 1.f;           // weights of columns 2 t4 and 2 t4 + 1
+    float w0 = 0.f, w1 = 0.f;           // weights of columns 2 t4 and 2 t4 + 1, if these have slots
+    bool has0 = false, has1 = false;
     bool fresh = true;
     for (; at < end; ++at) {
       if (fresh) {
         fresh = false;
-        const int s = table.slot[now][g];
-        there = s >= 0;
+        // a column without a slot takes the head's x: nothing of it is used
+        int s = table.slot[now][g];
+        if (s < 0) s = table.head[now];
         if constexpr (kStaged)
           xp = staged + (p.x_slot != 0 ? s : s / p.topk) * p.x_pitch + t4 * 8;
         else
           xp = p.x + (s / p.topk) * p.x_token + (s % p.topk) * p.x_slot + t4 * 8;
         if constexpr (kSum) {
           const int s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
-          w0 = s0 < 0 ? 0.f : p.weights[s0], w1 = s1 < 0 ? 0.f : p.weights[s1];
+          has0 = s0 >= 0, has1 = s1 >= 0;
+          if (has0) w0 = p.weights[s0];
+          if (has1) w1 = p.weights[s1];
         }
       }
       const int k0 = w * kWindow;
@@ -365,22 +390,26 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         }
         const __nv_bfloat162 off0 = *reinterpret_cast<const __nv_bfloat162*>(&o0);
         const __nv_bfloat162 off1 = *reinterpret_cast<const __nv_bfloat162*>(&o1);
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains
+        float c[2][4];  // two chains
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
           const int chunk = q * (kGroup / 32) + j;
-          uint4 b = make_uint4(0, 0, 0, 0);
-          if (there) {
-            if constexpr (kStaged)
-              b = *reinterpret_cast<const uint4*>(xp + k0 + chunk * 32);
-            else
-              b = in_pairs(__ldg(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32)));
-          }
+          uint4 b;
+          if constexpr (kStaged)
+            b = *reinterpret_cast<const uint4*>(xp + k0 + chunk * 32);
+          else
+            b = in_pairs(__ldg(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32)));
           const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + ((chunk ^ g) << 4));
           const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 1024 + ((chunk ^ g) << 4));
-          mma(c[0], two_codes<kZero>(wa, off0), two_codes<kZero>(wb, off1), two_codes<kZero>(wa >> 4, off0),
+          auto sum = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+            if (j == 0)
+              mma_first(c[i], a0, a1, a2, a3, b0, b1);
+            else
+              mma(c[i], a0, a1, a2, a3, b0, b1);
+          };
+          sum(0, two_codes<kZero>(wa, off0), two_codes<kZero>(wb, off1), two_codes<kZero>(wa >> 4, off0),
               two_codes<kZero>(wb >> 4, off1), b.x, b.y);
-          mma(c[1], two_codes<kZero>(wa >> 8, off0), two_codes<kZero>(wb >> 8, off1), two_codes<kZero>(wa >> 12, off0),
+          sum(1, two_codes<kZero>(wa >> 8, off0), two_codes<kZero>(wb >> 8, off1), two_codes<kZero>(wa >> 12, off0),
               two_codes<kZero>(wb >> 12, off1), b.z, b.w);
         }
         const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[q / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[q / 2];
@@ -402,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       if (!kSum) {
         ++w;
       } else if (++w == p.windows || at + 1 == end) {
-        res[0] += w0 * acc[0], res[1] += w1 * acc[1], res[2] += w0 * acc[2], res[3] += w1 * acc[3];
+        if (has0) res[0] += w0 * acc[0], res[2] += w0 * acc[2];
+        if (has1) res[1] += w1 * acc[1], res[3] += w1 * acc[3];
         acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
         if (w == p.windows) w = 0, ++now, fresh = true;
       }
