@@ -105,22 +105,31 @@ int gmm_quantize_int4(const void* x, int x_dtype, int32_t batch, int64_t rows_pe
 int gmm_dequantize_int4(const void* codes, const void* scale, const void* zero, int32_t group, int32_t batch,
                         int64_t rows_per_batch, int64_t k, void* out, int out_dtype, void* stream);
 
+/* Bytes of scratch that gmm_matvec_int4() needs (0 for few tokens, and for sizes that it refuses);
+ * no content is expected, none is kept. */
+size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t group, int has_zero, int32_t topk, int x_per_slot);
+
 /*
  * Products of few tokens with the 4-bit weights of the experts that each chose, in the
  * order of the tokens (no sort):
- *   h[t, j] = W(experts[t, j]) x[t, j]          (fp32 sums of exact products)
+ *   h[t, j] = W(experts[t, j]) x[t, j]
+ *           = sum over groups of scale * (sum of code x - zero * sum of x)
+ *             (codes 0 .. 15, two's complement ones counted from -8 with zero 8; exact products
+ *             and fp32 sums)
  *   y[t, j] = h[t, j], or with act: act(first half of h[t, j]) * second half
  *   out[t, j] = y[t, j], or with weights: out[t] = sum over j of weights[t, j] * y[t, j]
  * rounded once to out_dtype.  A slot whose expert is outside [0, num_experts) gives zeros,
  * and nothing to a sum.  Each expert's weights are read once for every 8 of its tokens (for
  * every 8 tokens, with weights), so this is for the few rows an expert has in decoding; gmm()
- * is for more.  The same inputs give the same bits.
+ * is for more.  The same inputs give the same bits.  A row of x with an infinity or NaN gives NaN.
  *
  *   x        BF16 [tokens, k] with row pitch x_ld (x_per_slot 0: all slots of a token share
  *            it) or dense [tokens, topk, k] (x_per_slot 1; x_ld is not used)
  *   codes, scale, zero   [num_experts][n, k] as above; zero NULL or not
  *   experts  int32 [tokens, topk], or NULL: topk is 1 and every token's expert is 0
  *   weights  NULL or f32 [tokens, topk]; not with act
+ *   scratch  gmm_matvec_scratch_bytes() bytes, 16-byte aligned (NULL for none); calls that may run
+ *            at the same time need one each
  *   out      [tokens, topk, n] or (weights) [tokens, n], n / 2 with act; BF16 or F32
  * k % group == 0, n % 8 == 0 (% 16 with act); x, codes, scale, zero 16-byte aligned, x_ld a
  * multiple of 8; topk <= GMM_MAX_TOPK; num_experts <= GMM_MAX_GROUPS.
@@ -128,7 +137,7 @@ int gmm_dequantize_int4(const void* codes, const void* scale, const void* zero, 
 int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t x_ld, int x_per_slot, const void* codes,
                     const void* scale, const void* zero, int32_t group, int32_t num_experts, int64_t n,
                     const int32_t* experts, int32_t topk, const float* weights, int act, void* out, int out_dtype,
-                    void* stream);
+                    void* scratch, size_t scratch_bytes, void* stream);
 
 #ifdef __cplusplus
 }

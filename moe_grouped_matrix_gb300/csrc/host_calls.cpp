@@ -41,6 +41,7 @@ struct Calls {
   decltype(&gmm_quantize_int4) quantize_int4;
   decltype(&gmm_dequantize_int4) dequantize_int4;
   decltype(&gmm_matvec_int4) matvec_int4;
+  decltype(&gmm_matvec_scratch_bytes) matvec_scratch;
 } g_calls{};
 
 using at::Tensor;
@@ -515,10 +516,14 @@ PyObject* matvec_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t out_n = act != 0 ? rows / 2 : rows;
     const auto type = f32 ? kF32 : kBF16;
     Tensor out = sums ? empty({tokens, out_n}, type, *x) : empty({tokens, topk, out_n}, type, *x);
+    const size_t bytes = g_calls.matvec_scratch(tokens, k, int32_t(group), a[3] != Py_None, int32_t(topk), slots);
+    Tensor scratch;
+    if (bytes > 0) scratch = empty({int64_t(bytes)}, kU8, *x);
     const int st = g_calls.matvec_int4(x->data_ptr(), tokens, k, ld, slots, codes->data_ptr(), scale->data_ptr(),
                                        ptr_or_null<uint8_t>(zero), int32_t(group), int32_t(num), rows,
                                        ptr<int32_t>(*chosen), int32_t(topk), ptr_or_null<float>(weights), int(act),
-                                       out.data_ptr(), code_of(out), stream_of(*x));
+                                       out.data_ptr(), code_of(out), bytes > 0 ? scratch.data_ptr() : nullptr, bytes,
+                                       stream_of(*x));
     return answer(st, {out});
   });
 }

@@ -5,12 +5,22 @@
 // Bound by memory: half a byte a weight, read once.  At 6.8 TB/s an SM gets some 47
 // weights a cycle, and may spend 2.7 issue slots of a lane on each; one fp32
 // multiply-add with its conversion takes about 2 for a single token.  So the sums run on
-// mma.sync m16n8k16, 16 weight rows by 8 columns: the codes become bf16 in 1.4
-// instructions each for all 8 columns (a nibble or-ed into 128's mantissa is 128 + code,
-// and one packed subtraction takes 128 and the zero point off, exactly), x is bf16 as it
-// stands, products are exact and sums fp32.  A group's sum is scaled in fp32.  A matrix
-// instruction's k are a set without an order, so a lane takes the eight k of a 32-bit
-// word for its own, and x is permuted alike.
+// mma.sync m16n8k16, 16 weight rows by 8 columns, with operands that cost next to nothing:
+// the bit pattern of a whole number below 256 is, read as bf16, that number times 2^-133 (a
+// subnormal, or the first binade above them, whose spacing is the same), so a mask takes two
+// codes out of a word, at its bits 0-3 and 16-19 or, 16 times as large, at 4-7 and 20-23: five
+// instructions for eight weights and all their columns.  The other operand is x times a power
+// of two that puts each row's largest value at 2^116, exactly (x is bf16, so is the product:
+// what lies 2^242 below the largest is lost), divided by 16 where the codes are 16 times as
+// large.  Products are exact, sums fp32.  Codes are not negative there (two's complement ones
+// have their top bit flipped, which adds 8): the sum starts at -8 (or -zero) times the group's
+// sum of x, which is computed once for each row.  That makes the terms of a sum up to
+// |code| + 2 * 8 times |x| instead of |code - 8| times, a few units of fp32 more of error.  A
+// row with an infinity or NaN gives NaN.  A group's sum is scaled in fp32, and the power of two
+// taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the
+// eight k of a 32-bit word for its own, and x is permuted alike.  x of few tokens is made ready
+// by each CTA in its shared memory while its first weights are on their way, x of more by a kernel
+// ahead.
 //
 // A warp streams windows of 16 rows by 256 k through a ring of its own in shared memory,
 // by asynchronous copies that only it waits for: no barrier between warps but one for each
@@ -54,7 +64,11 @@ struct Params {
   void* out;
   int32_t out_n, out_f32;  // columns of out, its type
   int32_t team_log2;      // of the warps to a tile
-  int32_t x_rows, x_pitch;  // kStaged: rows of x in shared memory, and elements between them
+  int32_t x_rows, x_pitch;  // rows of x made ready, and elements between them
+  // where not in shared memory: the rows, their groups' sums, and what takes their results to their size
+  __nv_bfloat16* ready;
+  float* sums;
+  float* roots;
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
@@ -78,28 +92,62 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same with nothing to add to.
-__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
 
-// Eight bf16 as pairs (0, 4), (1, 5), (2, 6), (3, 7): those that one mask takes out of a word of codes.
-__device__ __forceinline__ uint4 in_pairs(uint4 v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                    __byte_perm(v.y, v.w, 0x7632));
-}
+constexpr int kTop = 116;                  // rows' largest values are brought to 2^116
 
-// Two codes, at bits 0-3 and 16-19 of w, as bf16 with `off` = 128 + zero taken off.
-template <bool kZero>
-__device__ __forceinline__ uint32_t two_codes(uint32_t w, __nv_bfloat162 off) {
-  // two's complement + 8 is the code with its top bit flipped
-  const uint32_t raw = (w & 0x000F000Fu) ^ (kZero ? 0x43004300u : 0x43084308u);
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&raw), off);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// Rows of x are made ready by windows, a warp each.  First the largest finite magnitude of each.
+__device__ __forceinline__ uint32_t largest(const __nv_bfloat16* x, int k, int window) {
+  const int c = window * kWindow + (threadIdx.x & 31) * 8;
+  uint32_t m = 0;
+  if (c < k) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+      if (lo < 0x7F80u) m = max(m, lo);
+      if (hi < 0x7F80u) m = max(m, hi);
+    }
+  }
+  return __reduce_max_sync(0xffffffffu, m);
+}
+// The power of two that a row's largest value, of these windows, has or, if that is even, the next.
+__device__ __forceinline__ int power_of(const uint32_t* tops, int windows) {
+  uint32_t top = 0;
+  for (int i = threadIdx.x & 31; i < windows; i += 32) top = max(top, tops[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  return (top == 0 ? 0 : top < 0x80u ? 31 - __clz(int(top)) - 133 : int(top >> 7) - 127) | 1;
+}
+// The root of what takes a result to its own size: 2^(133 - kTop + power).
+__device__ __forceinline__ float root_of(int power) { return __int_as_float((127 + (133 - kTop + power) / 2) << 23); }
+// A window of the row: x 2^(kTop - power) as bf16, in each 8 in the order of the masks, 0 4 1 5 2 6 3 7,
+// the odd ones over 16; and -8 (kZero: -1) times the groups' sums times 2^-133.
+template <int kGroup, bool kZero>
+__device__ __forceinline__ void make_ready(const __nv_bfloat16* x, int k, int window, int power, __nv_bfloat16* to,
+                                           float* sums) {
+  const int lane = threadIdx.x & 31, c = window * kWindow + lane * 8;
+  const int up = kTop - power, first = up / 2;  // up to 249: in two steps, each exact
+  const float u0 = __int_as_float((127 + first) << 23), u1 = __int_as_float((127 + up - first) << 23);
+  float sum = 0.f;
+  if (c < k) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) * u0 * u1;
+      sum += f[i];
+      if (i % 2) f[i] *= 0.0625f;
+    }
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      out[i] = __float_as_uint(f[i]) >> 16 | (__float_as_uint(f[i + 4]) & 0xFFFF0000u);
+    *reinterpret_cast<uint4*>(to + c) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+#pragma unroll
+  for (int d = 1; d < kGroup / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane % (kGroup / 8) == 0 && c < k) sums[c / kGroup] = sum * (kZero ? -0x1p-100f : -0x1p-97f) * 0x1p-33f;
 }
 
 // A warp's ring: kStages windows' codes, then their scales, then their zero points.  Four stages are
@@ -118,6 +166,8 @@ struct Table {
   int32_t expert[kMaxSlots];          // of each slot; then of each item
   int16_t slot[kMaxSlots][kCols];     // of each item's columns; -1: none
   int16_t head[kMaxSlots];            // of each item: its first slot
+  int16_t row[kMaxSlots];             // of each slot: its row of x
+  int32_t columns[kMaxSlots];         // of each item
   int16_t first[kMaxSlots / kCols + kMaxSlots + 1];  // with weights: first item of each 8 tokens
   int32_t items;
   int32_t warp_heads[kWarps];
@@ -133,6 +183,14 @@ struct Unit {
   }
 };
 
+template <bool kShared, class T>
+__device__ __forceinline__ T load(const T* p) {
+  if constexpr (kShared)
+    return *p;
+  else
+    return __ldg(p);
+}
+
 template <int kGroup, bool kZero, bool kGated, bool kSum, bool kStaged>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   using R = Ring<kGroup, kZero>;
@@ -140,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   griddep_begin();
   p.x = after_begin(p.x), p.codes = after_begin(p.codes), p.scale = after_begin(p.scale);
   p.zero = after_begin(p.zero), p.chosen = after_begin(p.chosen), p.weights = after_begin(p.weights);
+  p.ready = after_begin(p.ready), p.sums = after_begin(p.sums), p.roots = after_begin(p.roots);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Table table;
   __shared__ float part[2][kWarps][16][kCols + 1];
@@ -151,9 +210,20 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   for (int i = tid; i < slots; i += kThreads) {
     const int e = p.chosen != nullptr ? p.chosen[i] : 0;
     table.expert[i] = e >= 0 && e < p.experts ? e : -1;
+    table.row[i] = int16_t(p.x_slot != 0 ? i : i / p.topk);
+    table.columns[i] = 0;
   }
   for (int i = tid; i < kMaxSlots * kCols / 2; i += kThreads) reinterpret_cast<uint32_t*>(table.slot)[i] = 0xFFFFFFFFu;
   if (tid == 0) table.items = 0;
+  const int64_t x_step = p.x_slot != 0 ? p.x_slot : p.x_token;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(&part[0][0][0][0]);  // of the windows of x
+  if constexpr (kStaged) {
+    for (int i = warp; i < p.x_rows * p.windows; i += kWarps) {
+      const int row = i / p.windows;
+      const uint32_t top = largest(p.x + row * x_step, p.k, i - row * p.windows);
+      if (lane == 0) tops[i] = top;
+    }
+  }
   __syncthreads();
   // a slot's item: its head's, of which this thread keeps what it needs until all have read the table
   int head[kMaxSlots / kThreads], column[kMaxSlots / kThreads], mine[kMaxSlots / kThreads];
@@ -217,7 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   }
 #pragma unroll
   for (int r = 0; r < kMaxSlots / kThreads; ++r)
-    if (head[r] >= 0) table.slot[number[head[r]]][column[r]] = int16_t(r * kThreads + tid);
+    if (head[r] >= 0) {
+      table.slot[number[head[r]]][column[r]] = int16_t(r * kThreads + tid);
+      if constexpr (!kSum) atomicAdd(&table.columns[number[head[r]]], 1);
+    }
   const int chunks = (p.tokens + kCols - 1) / kCols;
   if (kSum && tid == 0) table.first[chunks] = int16_t(table.items);
   __syncthreads();
@@ -243,9 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   // ---- the warp's part of its team's units, in order: pairs of an item and a window
   const int lg = p.team_log2, size = 1 << lg;    // warps of a team
   const int member = warp & (size - 1), team = warp >> lg;
-  const int teams = int(gridDim.x) * (kWarps >> lg);  // of all CTAs; a CTA's are far apart
+  // teams of all CTAs; a CTA's are far apart, so that the last round is spread over all of them, or next
+  // to one another, so that they read the same rows of x through the SM's cache
+  const int teams = int(gridDim.x) * (kWarps >> lg);
   const int groups = kSum ? chunks : table.items;
-  const int start = int(blockIdx.x) + team * int(gridDim.x);
+  const int start = kStaged ? int(blockIdx.x) + team * int(gridDim.x) : int(blockIdx.x) * (kWarps >> lg) + team;
   const int dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
   Unit ahead{start / p.tiles, 0};
   ahead.tile = start - ahead.group * p.tiles;
@@ -253,10 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   uint8_t* const ring = smem + warp * R::kBytes;
   const uint32_t ring_at = smem_u32(ring);
   // the pairs of a unit that are this warp's: [begin, end) of its items' windows
+  const int begin_one = int((int64_t(p.windows) * member) >> lg), end_one = int((int64_t(p.windows) * (member + 1)) >> lg);
   auto part_of = [&](const Unit& u, int& first, int& begin, int& end) {
-    first = kSum ? table.first[u.group] : u.group;
-    const int64_t pairs = int64_t(kSum ? table.first[u.group + 1] - first : 1) * p.windows;
-    begin = int((pairs * member) >> lg), end = int((pairs * (member + 1)) >> lg);
+    if constexpr (kSum) {
+      first = table.first[u.group];
+      const int64_t pairs = int64_t(table.first[u.group + 1] - first) * p.windows;
+      begin = int((pairs * member) >> lg), end = int((pairs * (member + 1)) >> lg);
+    } else {
+      first = u.group, begin = begin_one, end = end_one;
+    }
   };
 
   // what is fetched ahead: its pair, and where this lane's pieces are
@@ -334,43 +414,49 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s);
 
-  __nv_bfloat16* const staged = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
-  if constexpr (kStaged) {  // all of x, each 8 in the order of a word's pairs: 0 4 1 5 2 6 3 7
-    const int eights = p.k / 8;
-    for (int r = 0; r < p.x_rows; ++r) {
-      const __nv_bfloat16* row = p.x + (p.x_slot != 0 ? r * p.x_slot : r * p.x_token);
-      for (int i = tid; i < eights; i += kThreads)
-        *reinterpret_cast<uint4*>(staged + r * p.x_pitch + i * 8) = in_pairs(__ldg(reinterpret_cast<const uint4*>(row) + i));
+  // rows of x made ready: in shared memory, or by the kernel ahead
+  const int x_groups = p.k / kGroup;
+  const __nv_bfloat16* ready = p.ready;
+  const float* sums = p.sums;
+  const float* roots = p.roots;
+  if constexpr (kStaged) {
+    auto* to = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
+    auto* to_sums = reinterpret_cast<float*>(to + p.x_rows * p.x_pitch);
+    float* to_roots = to_sums + p.x_rows * x_groups;
+    ready = to, sums = to_sums, roots = to_roots;
+    for (int i = warp; i < p.x_rows * p.windows; i += kWarps) {
+      const int row = i / p.windows, power = power_of(tops + row * p.windows, p.windows);
+      make_ready<kGroup, kZero>(p.x + row * x_step, p.k, i - row * p.windows, power, to + row * p.x_pitch,
+                                to_sums + row * x_groups);
+      if (lane == 0) to_roots[row] = root_of(power);
     }
     __syncthreads();
   }
 
   const int g = lane >> 2, t4 = lane & 3;
-  int stage = 0, parity = 0;
+  int stage = 0, parity = 0, last = -1;
+  const __nv_bfloat16* xp = nullptr;                // column g of the last item, from this lane's k on
+  const float *sums0 = nullptr, *sums1 = nullptr;   // of columns 2 t4 and 2 t4 + 1
+  float w0 = 0.f, w1 = 0.f, root0 = 0.f, root1 = 0.f;
+  bool has0 = false, has1 = false;
   for (; here.group < groups; here.advance(dgroup, dtile, p.tiles), parity ^= 1) {
     int first, at, end;
     part_of(here, first, at, end);
     int now = first + (kSum ? at / p.windows : 0), w = kSum ? at - (now - first) * p.windows : at;
     float res[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const __nv_bfloat16* xp = nullptr;  // column g of the item, from this lane's k on
-    float w0 = 0.f, w1 = 0.f;           // weights of columns 2 t4 and 2 t4 + 1, if these have slots
-    bool has0 = false, has1 = false;
-    bool fresh = true;
     for (; at < end; ++at) {
-      if (fresh) {
-        fresh = false;
+      if (now != last) {
+        last = now;
         // a column without a slot takes the head's x: nothing of it is used
-        int s = table.slot[now][g];
-        if (s < 0) s = table.head[now];
-        if constexpr (kStaged)
-          xp = staged + (p.x_slot != 0 ? s : s / p.topk) * p.x_pitch + t4 * 8;
-        else
-          xp = p.x + (s / p.topk) * p.x_token + (s % p.topk) * p.x_slot + t4 * 8;
+        const int head = table.row[table.head[now]];
+        const int s = table.slot[now][g], s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
+        has0 = s0 >= 0, has1 = s1 >= 0;
+        const int r0 = has0 ? table.row[s0] : head, r1 = has1 ? table.row[s1] : head;
+        xp = ready + int64_t(s < 0 ? head : table.row[s]) * p.x_pitch + t4 * 8;
+        sums0 = sums + int64_t(r0) * x_groups, sums1 = sums + int64_t(r1) * x_groups;
         if constexpr (kSum) {
-          const int s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
-          has0 = s0 >= 0, has1 = s1 >= 0;
-          if (has0) w0 = p.weights[s0];
-          if (has1) w1 = p.weights[s1];
+          w0 = has0 ? p.weights[s0] : 0.f, w1 = has1 ? p.weights[s1] : 0.f;
+          root0 = roots[r0], root1 = roots[r1];
         }
       }
       const int k0 = w * kWindow;
@@ -378,124 +464,144 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       __syncwarp();
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       const uint8_t* codes = ring + stage * kCodeBytes + g * 128 + t4 * 4;
-      using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
       const uint8_t* scales = ring + kStages * kCodeBytes + stage * R::kScales;
-      Scales sa = reinterpret_cast<const Scales*>(scales)[g], sb = reinterpret_cast<const Scales*>(scales)[g + 8];
       const uint8_t* zeros = ring + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros;
-      auto group = [&](int q) {
-        uint32_t o0 = 0x43084308u, o1 = 0x43084308u;
+      auto group = [&](int q, float s0, float s1) {
+        const float n0 = load<kStaged>(sums0 + w * kEach + q), n1 = load<kStaged>(sums1 + w * kEach + q);
+        float c[4] = {n0, n1, n0, n1};
         if constexpr (kZero) {
-          o0 = 0x43004300u + zeros[g * kEach + q] * 0x00010001u;
-          o1 = 0x43004300u + zeros[(g + 8) * kEach + q] * 0x00010001u;
+          const float z0 = float(zeros[g * kEach + q]), z1 = float(zeros[(g + 8) * kEach + q]);
+          c[0] *= z0, c[1] *= z0, c[2] *= z1, c[3] *= z1;
         }
-        const __nv_bfloat162 off0 = *reinterpret_cast<const __nv_bfloat162*>(&o0);
-        const __nv_bfloat162 off1 = *reinterpret_cast<const __nv_bfloat162*>(&o1);
-        float c[2][4];  // two chains
+        constexpr uint32_t kFlip = kZero ? 0u : 0x00080008u;  // two's complement + 8 is the top bit flipped
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
           const int chunk = q * (kGroup / 32) + j;
-          uint4 b;
-          if constexpr (kStaged)
-            b = *reinterpret_cast<const uint4*>(xp + k0 + chunk * 32);
-          else
-            b = in_pairs(__ldg(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32)));
-          const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + ((chunk ^ g) << 4));
-          const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 1024 + ((chunk ^ g) << 4));
-          auto sum = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-            if (j == 0)
-              mma_first(c[i], a0, a1, a2, a3, b0, b1);
-            else
-              mma(c[i], a0, a1, a2, a3, b0, b1);
-          };
-          sum(0, two_codes<kZero>(wa, off0), two_codes<kZero>(wb, off1), two_codes<kZero>(wa >> 4, off0),
-              two_codes<kZero>(wb >> 4, off1), b.x, b.y);
-          sum(1, two_codes<kZero>(wa >> 8, off0), two_codes<kZero>(wb >> 8, off1), two_codes<kZero>(wa >> 12, off0),
-              two_codes<kZero>(wb >> 12, off1), b.z, b.w);
+          const uint4 b = load<kStaged>(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32));
+          const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + ((chunk ^ g) << 4)), va = wa >> 8;
+          const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 1024 + ((chunk ^ g) << 4)), vb = wb >> 8;
+          auto low = [](uint32_t v) { return (v & 0x000F000Fu) ^ kFlip; };
+          auto high = [](uint32_t v) { return (v & 0x00F000F0u) ^ (kFlip << 4); };
+          mma(c, low(wa), low(wb), high(wa), high(wb), b.x, b.y);
+          mma(c, low(va), low(vb), high(va), high(vb), b.z, b.w);
         }
-        const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[q / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[q / 2];
-        const float s0 = __uint_as_float(q % 2 ? pa & 0xFFFF0000u : pa << 16);
-        const float s1 = __uint_as_float(q % 2 ? pb & 0xFFFF0000u : pb << 16);
-        acc[0] = fmaf(s0, c[0][0] + c[1][0], acc[0]), acc[1] = fmaf(s0, c[0][1] + c[1][1], acc[1]);
-        acc[2] = fmaf(s1, c[0][2] + c[1][2], acc[2]), acc[3] = fmaf(s1, c[0][3] + c[1][3], acc[3]);
+        acc[0] = fmaf(s0, c[0], acc[0]), acc[1] = fmaf(s0, c[1], acc[1]);
+        acc[2] = fmaf(s1, c[2], acc[2]), acc[3] = fmaf(s1, c[3], acc[3]);
       };
       if (k0 + kWindow <= p.k) {
+        using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
+        const Scales sa = reinterpret_cast<const Scales*>(scales)[g], sb = reinterpret_cast<const Scales*>(scales)[g + 8];
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) group(q);
+        for (int q = 0; q < kEach; ++q) {
+          const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[q / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[q / 2];
+          group(q, __uint_as_float(q % 2 ? pa & 0xFFFF0000u : pa << 16), __uint_as_float(q % 2 ? pb & 0xFFFF0000u : pb << 16));
+        }
       } else {
+        const __nv_bfloat16* one = reinterpret_cast<const __nv_bfloat16*>(scales) + g * kEach;
         const int left = (p.k - k0) / kGroup;
-#pragma unroll
-        for (int q = 0; q < kEach; ++q)
-          if (q < left) group(q);
+#pragma unroll 1
+        for (int q = 0; q < left; ++q) group(q, __bfloat162float(one[q]), __bfloat162float(one[8 * kEach + q]));
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
       if (!kSum) {
         ++w;
       } else if (++w == p.windows || at + 1 == end) {
-        if (has0) res[0] += w0 * acc[0], res[2] += w0 * acc[2];
-        if (has1) res[1] += w1 * acc[1], res[3] += w1 * acc[3];
+        if (has0) res[0] += w0 * (acc[0] * root0 * root0), res[2] += w0 * (acc[2] * root0 * root0);
+        if (has1) res[1] += w1 * (acc[1] * root1 * root1), res[3] += w1 * (acc[3] * root1 * root1);
         acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        if (w == p.windows) w = 0, ++now, fresh = true;
+        if (w == p.windows) w = 0, ++now;
       }
     }
-    const float* sums = kSum ? res : acc;
-    part[parity][warp][g][2 * t4] = sums[0], part[parity][warp][g][2 * t4 + 1] = sums[1];
-    part[parity][warp][g + 8][2 * t4] = sums[2], part[parity][warp][g + 8][2 * t4 + 1] = sums[3];
+    const float* mine4 = kSum ? res : acc;
+    part[parity][warp][g][2 * t4] = mine4[0], part[parity][warp][g][2 * t4 + 1] = mine4[1];
+    part[parity][warp][g + 8][2 * t4] = mine4[2], part[parity][warp][g + 8][2 * t4 + 1] = mine4[3];
     if (lg == 0)
       __syncwarp();
     else
       asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 << lg) : "memory");
     // sums over the team's warps, and out
     constexpr int kRows = kGated ? 8 : 16;
-    for (int i = member * 32 + lane; i < kRows * kCols; i += 32 << lg) {
+    const int columns = kSum ? p.tokens - here.group * kCols : table.columns[here.group];
+    const float* sum = &part[parity][team << lg][0][0];
+    for (int i = member * 32 + lane; i < kRows * min(columns, kCols); i += 32 << lg) {
       const int row = i % kRows, col = i / kRows;
-      int64_t to;
-      if constexpr (kSum) {
-        to = here.group * kCols + col;
-        if (to >= p.tokens) continue;
-      } else {
-        to = table.slot[here.group][col];
-        if (to < 0) continue;
-      }
       const int64_t c = int64_t(here.tile) * kRows + row;
       if (c >= p.out_n) continue;
-      float v = 0.f;
-      for (int m = 0; m < size; ++m) v += part[parity][(team << lg) + m][row][col];
-      if constexpr (kGated) {
-        float u = 0.f;
-        for (int m = 0; m < size; ++m) u += part[parity][(team << lg) + m][row + 8][col];
-        v = (p.act == GMM_ACT_SILU ? act_value<GMM_ACT_SILU>(v) : act_value<GMM_ACT_GELU>(v)) * u;
+      const float* from = sum + row * (kCols + 1) + col;
+      float v = 0.f, u = 0.f;
+      for (int m = 0; m < size; ++m) {
+        v += from[m * 16 * (kCols + 1)];
+        if constexpr (kGated) u += from[(m * 16 + 8) * (kCols + 1)];
       }
-      put(to, c, v);
+      if constexpr (kSum) {
+        put(here.group * kCols + col, c, v);
+      } else {
+        const int to = table.slot[here.group][col];
+        const float root = roots[table.row[to]];
+        v = v * root * root;
+        if constexpr (kGated) {
+          u = u * root * root;
+          v = (p.act == GMM_ACT_SILU ? act_value<GMM_ACT_SILU>(v) : act_value<GMM_ACT_GELU>(v)) * u;
+        }
+        put(to, c, v);
+      }
     }
   }
   copies_wait<0>();
 }
 
+// Rows of x made ready where a CTA's shared memory does not hold them: a CTA a row.
+template <int kGroup, bool kZero>
+__global__ void __launch_bounds__(256) make_ready_kernel(Params p) {
+  griddep_begin();
+  p.x = after_begin(p.x);
+  __shared__ uint32_t tops[8];
+  const int row = blockIdx.x, warp = threadIdx.x >> 5;
+  const __nv_bfloat16* x = p.x + row * (p.x_slot != 0 ? p.x_slot : p.x_token);
+  uint32_t top = 0;
+  for (int w = warp; w < p.windows; w += 8) top = max(top, largest(x, p.k, w));
+  if ((threadIdx.x & 31) == 0) tops[warp] = top;
+  __syncthreads();
+  const int power = power_of(tops, 8);
+  for (int w = warp; w < p.windows; w += 8)
+    make_ready<kGroup, kZero>(x, p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * (p.k / kGroup));
+  if (threadIdx.x == 0) p.roots[row] = root_of(power);
+}
+
 constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * 2 * kWarps * 16 * (kCols + 1);
 
+// Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the groups' sums, the roots.
+int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + k / group * 4 + 4); }
+// In shared memory rows are half a line of banks apart.
+int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
+bool is_staged(int64_t rows, int64_t k, int group, bool zero) {
+  const int64_t each = kWindow / group, ring = int64_t(kWarps) * 4 * (kCodeBytes + 16 * each * (zero ? 3 : 2));
+  return ready_bytes(rows, staged_pitch(k), k, group) <= int64_t(kMaxShared) - ring;
+}
+int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
+
 template <int kGroup, bool kZero, bool kGated, bool kSum>
-cudaError_t launch(Params p, int64_t units, int sms, cudaStream_t stream) {
-  size_t smem = size_t(kWarps) * Ring<kGroup, kZero>::kBytes;
-  // x goes to shared memory where it fits; rows half a line of banks apart
-  p.x_rows = p.x_slot != 0 ? p.tokens * p.topk : p.tokens;
-  const int64_t x_pitch = p.k % 64 == 0 ? int64_t(p.k) + 32 : p.k, x_bytes = p.x_rows * x_pitch * 2;
-  const bool staged = x_bytes <= int64_t(kMaxShared - smem);
-  if (staged) smem += size_t(x_bytes), p.x_pitch = int32_t(x_pitch);
+cudaError_t launch(const Params& p, bool staged, int64_t units, int sms, cudaStream_t stream) {
+  using R = Ring<kGroup, kZero>;
+  static_assert(R::kStages == 4, "is_staged() counts them");
+  const size_t smem = size_t(kWarps) * R::kBytes + (staged ? size_t(ready_bytes(p.x_rows, p.x_pitch, p.k, kGroup)) : 0);
   auto kern = staged ? matvec_kernel<kGroup, kZero, kGated, kSum, true> : matvec_kernel<kGroup, kZero, kGated, kSum, false>;
   // for every launch: the attribute is the current device's, and one size for all calls
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
+  if (!staged)
+    if (cudaError_t e = launch_dependent(make_ready_kernel<kGroup, kZero>, unsigned(p.x_rows), 256, 0, stream, 1, p)) return e;
   const int64_t ctas = ((units << p.team_log2) + kWarps - 1) / kWarps;
   return launch_dependent(kern, unsigned(ctas < sms ? ctas : sms), kThreads, smem, stream, 1, p);
 }
 
 template <int kGroup, bool kZero>
-cudaError_t by_form(const Params& p, int64_t units, int sms, cudaStream_t stream) {
-  if (p.weights != nullptr) return launch<kGroup, kZero, false, true>(p, units, sms, stream);
-  return p.act != GMM_ACT_NONE ? launch<kGroup, kZero, true, false>(p, units, sms, stream)
-                               : launch<kGroup, kZero, false, false>(p, units, sms, stream);
+cudaError_t by_form(const Params& p, bool staged, int64_t units, int sms, cudaStream_t stream) {
+  if (p.weights != nullptr) return launch<kGroup, kZero, false, true>(p, staged, units, sms, stream);
+  return p.act != GMM_ACT_NONE ? launch<kGroup, kZero, true, false>(p, staged, units, sms, stream)
+                               : launch<kGroup, kZero, false, false>(p, staged, units, sms, stream);
 }
 
-cudaError_t matvec(Params p, int group, int sms, cudaStream_t stream) {
+cudaError_t matvec(Params p, int group, bool staged, int sms, cudaStream_t stream) {
   // units at most: a tile of each slot's expert, or of each 8 tokens with their experts one after another
   const bool sums = p.weights != nullptr;
   const int64_t units = int64_t(p.tiles) * (sums ? (p.tokens + kCols - 1) / kCols : p.tokens * p.topk);
@@ -509,9 +615,9 @@ cudaError_t matvec(Params p, int group, int sms, cudaStream_t stream) {
   }
   const bool zero = p.zero != nullptr;
   switch (group) {
-    case 32: return zero ? by_form<32, true>(p, units, sms, stream) : by_form<32, false>(p, units, sms, stream);
-    case 64: return zero ? by_form<64, true>(p, units, sms, stream) : by_form<64, false>(p, units, sms, stream);
-    default: return zero ? by_form<128, true>(p, units, sms, stream) : by_form<128, false>(p, units, sms, stream);
+    case 32: return zero ? by_form<32, true>(p, staged, units, sms, stream) : by_form<32, false>(p, staged, units, sms, stream);
+    case 64: return zero ? by_form<64, true>(p, staged, units, sms, stream) : by_form<64, false>(p, staged, units, sms, stream);
+    default: return zero ? by_form<128, true>(p, staged, units, sms, stream) : by_form<128, false>(p, staged, units, sms, stream);
   }
 }
 
@@ -520,10 +626,22 @@ bool misaligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) %
 }  // namespace
 }  // namespace gmmk
 
+extern "C" size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t group, int has_zero, int32_t topk,
+                                           int x_per_slot) {
+  using namespace gmmk;
+  if (tokens <= 0 || tokens > kMaxSize || k < 1 || k > kMaxSize || (group != 32 && group != 64 && group != 128) ||
+      topk < 1 || topk > GMM_MAX_TOPK)
+    return 0;
+  const int64_t most = launch_tokens(topk), count = tokens < most ? tokens : most;
+  const int64_t rows = x_per_slot != 0 ? count * topk : count;
+  // a last launch of fewer tokens may not need what the others do
+  return is_staged(rows, k, group, has_zero != 0) ? 0 : size_t(ready_bytes(rows, k, k, group));
+}
+
 extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t x_ld, int x_per_slot, const void* codes,
                                const void* scale, const void* zero, int32_t group, int32_t num_experts, int64_t n,
                                const int32_t* experts, int32_t topk, const float* weights, int act, void* out,
-                               int out_dtype, void* stream) {
+                               int out_dtype, void* scratch, size_t scratch_bytes, void* stream) {
   using namespace gmmk;
   if (out_dtype != GMM_DTYPE_BF16 && out_dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
   if (tokens < 0 || tokens > kMaxSize || k < 1 || k > kMaxSize || n < 1 || n > kMaxSize || n % 8 != 0 ||
@@ -537,10 +655,14 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
   if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(scale, 16) || misaligned(zero, 16) ||
       misaligned(experts, 4) || misaligned(weights, 4) || misaligned(out, out_dtype == GMM_DTYPE_F32 ? 4 : 2))
     return GMM_ERR_ALIGN;
+  if (misaligned(scratch, 16)) return GMM_ERR_ALIGN;
+  if (scratch_bytes < gmm_matvec_scratch_bytes(tokens, k, group, zero != nullptr, topk, x_per_slot) ||
+      (scratch == nullptr && scratch_bytes > 0))
+    return GMM_ERR_WORKSPACE;
   int sms = 0;
   if (int st = require_device(&sms)) return st;
   const int64_t out_n = act != GMM_ACT_NONE ? n / 2 : n;
-  const int64_t most = kMaxSlots / topk / kCols * kCols;  // tokens of a launch
+  const int64_t most = launch_tokens(topk);
   for (int64_t t0 = 0; t0 < tokens; t0 += most) {
     const int64_t count = tokens - t0 < most ? tokens - t0 : most;
     Params p{};
@@ -554,9 +676,17 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     p.tokens = int32_t(count), p.topk = topk;
     p.weights = weights == nullptr ? nullptr : weights + t0 * topk;
     p.act = act, p.out_n = int32_t(out_n), p.out_f32 = out_dtype == GMM_DTYPE_F32;
+    p.x_rows = int32_t(x_per_slot != 0 ? count * topk : count);
+    const bool staged = is_staged(p.x_rows, k, group, zero != nullptr);
+    p.x_pitch = int32_t(staged ? staged_pitch(k) : k);
+    if (!staged) {
+      p.ready = static_cast<__nv_bfloat16*>(scratch);
+      p.sums = reinterpret_cast<float*>(p.ready + int64_t(p.x_rows) * k);
+      p.roots = reinterpret_cast<float*>(p.sums + int64_t(p.x_rows) * (k / group));
+    }
     const int64_t first = t0 * (weights != nullptr ? 1 : topk) * out_n;
     p.out = static_cast<char*>(out) + first * (out_dtype == GMM_DTYPE_F32 ? 4 : 2);
-    const cudaError_t e = matvec(p, group, sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = matvec(p, group, staged, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return record_cuda_error(e);
   }
   return GMM_OK;

@@ -38,7 +38,9 @@ SIGNATURES.update({
     "gmm_gated_act_backward": ([_P, _P, _I, _I64, _I64, _I64, _I, _P, _P], _I),
     "gmm_quantize_int4": ([_P, _I, _I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P], _I),
     "gmm_dequantize_int4": ([_P, _P, _P, _I32, _I32, _I64, _I64, _P, _I, _P], _I),
-    "gmm_matvec_int4": ([_P, _I64, _I64, _I64, _I, _P, _P, _P, _I32, _I32, _I64, _P, _I32, _P, _I, _P, _I, _P], _I),
+    "gmm_matvec_int4": ([_P, _I64, _I64, _I64, _I, _P, _P, _P, _I32, _I32, _I64, _P, _I32, _P, _I, _P, _I, _P, _SZ, _P],
+                        _I),
+    "gmm_matvec_scratch_bytes": ([_I64, _I64, _I32, _I, _I32, _I], _SZ),
 })
 
 
@@ -261,7 +263,7 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
     topk, n / 2] (n a multiple of 16); with weights float32 [tokens, topk] the sum over j of
     weights[t, j] h[t, j], [tokens, n].  Slots outside [0, E) are zeros, and nothing to a sum.
     Without experts w is one matrix [n, k] and h is [tokens, n].  Sums are fp32, rounded once to
-    out_dtype (bfloat16 or float32).  Weights are read once for every 8 tokens of an expert (with
+    out_dtype (bfloat16 or float32); a row of x with an infinity or NaN gives NaN.  Weights are read once for every 8 tokens of an expert (with
     weights, for every 8 tokens): for more than a few, sort the rows and use gmm()."""
     if stream is None and experts is not None:
         got = (_moe._calls or _moe._bind()).matvec_int4(x, w.codes, w.scale, w.zero, w.group, experts, weights,
@@ -301,10 +303,13 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
         raise ValueError(f"n must be a multiple of {step}, got {n}")
     if ld % 8:
         raise ValueError("x must have a row pitch that is a multiple of 8")
+    lib = _lib()
+    nbytes = lib.gmm_matvec_scratch_bytes(x.shape[0], k, w.group, int(w.zero is not None), topk, int(x.dim() == 3))
     with _on_stream(stream):
+        scratch = torch.empty((nbytes,), dtype=torch.uint8, device=x.device) if nbytes else None
         out = torch.empty(front + (n if act is None else n // 2,), dtype=out_dtype, device=x.device)
-    _run("gmm_matvec_int4", _lib().gmm_matvec_int4(
+    _run("gmm_matvec_int4", lib.gmm_matvec_int4(
         x.data_ptr(), x.shape[0], k, ld, int(x.dim() == 3), w.codes.data_ptr(), w.scale.data_ptr(), _ptr(w.zero),
         w.group, num, n, _ptr(experts), topk, _ptr(weights), code, out.data_ptr(), _float_code(out, "out_dtype"),
-        _on(x.device, stream)))
+        _ptr(scratch), nbytes, _on(x.device, stream)))
     return out

@@ -122,7 +122,8 @@ def _bind():
         names = ("gmm_route", "gmm_route_backward", "gmm_sort_by_expert", "gmm_dispatch", "gmm_combine",
                  "gmm_combine_backward", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_fp4",
                  "gmm_balance_scratch_bytes", "gmm_balance_loss", "gmm_balance_loss_backward", "gmm_gated_act",
-                 "gmm_gated_act_backward", "gmm_quantize_int4", "gmm_dequantize_int4", "gmm_matvec_int4")
+                 "gmm_gated_act_backward", "gmm_quantize_int4", "gmm_dequantize_int4", "gmm_matvec_int4",
+                 "gmm_matvec_scratch_bytes")
         calls.bind(*[ctypes.cast(getattr(lib, n), _P).value for n in names])
     except ImportError as e:
         warnings.warn(f"the mixture-of-experts calls go the longer way, some 7 us of host time more for each ({e}): "

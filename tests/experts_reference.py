@@ -139,8 +139,18 @@ def values(q):
     return (v * scale[..., None]).reshape(codes.shape)
 
 
-def matvec(x, w, experts, weights=None, kind=None):
-    """(out, size of the terms of each sum): x [T, k] or [T, K, k], w [E, n, k], all 64-bit."""
+def term_sizes(q):
+    """Of the terms scale code x and scale zero x, codes counted from 0: what multiplies |x|."""
+    codes, scale, zero = unpack(q)
+    v = codes.reshape(codes.shape[:-1] + (-1, q.group))
+    v = v + 16.0 if zero is None else v + zero[..., None]  # (code + 8) + 8
+    return (v * scale[..., None]).reshape(codes.shape)
+
+
+def matvec(x, w, experts, weights=None, kind=None, sizes=None):
+    """(out, size of the terms of each sum): x [T, k] or [T, K, k], w [E, n, k], all 64-bit; the terms are
+    |w x|, or those of term_sizes()."""
+    sizes = np.abs(w) if sizes is None else sizes
     T, K = experts.shape
     n = w.shape[1]
     h, size = np.zeros((T, K, n)), np.zeros((T, K, n))
@@ -149,7 +159,7 @@ def matvec(x, w, experts, weights=None, kind=None):
             e = experts[t, j]
             if 0 <= e < w.shape[0]:
                 v = x[t, j] if x.ndim == 3 else x[t]
-                h[t, j], size[t, j] = w[e] @ v, np.abs(w[e]) @ np.abs(v)
+                h[t, j], size[t, j] = w[e] @ v, sizes[e] @ np.abs(v)
     if kind is not None:
         f = n // 2
         a, slope, arg, slopes = act(h[..., :f], kind)
@@ -164,5 +174,6 @@ def matvec(x, w, experts, weights=None, kind=None):
 
 def matvec_adds(k, group):
     """Roundings that a sum's term goes through, in units of 2^-23 (the matrix instructions may cut off):
-    16 products and the sum so far in each of a group's instructions, then the groups, the warps, the slots."""
+    16 products and the sum so far in each of a group's instructions (or the sum of x that the zero point takes),
+    then the groups, the warps, the slots."""
     return 2 * (group // 16) + -(-k // group) + 8 + 32

@@ -29,7 +29,7 @@ def lib():
 def test_every_declared_call_is_exported_and_bound(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = re.findall(r"^(?:int|size_t)\s+(gmm_[a-z0-9_]+)\s*\(", text, flags=re.M)
-    assert len(names) == 8
+    assert len(names) == 9
     for name in names:
         assert hasattr(lib, name) and name in G.SIGNATURES
         args = re.search(re.escape(name) + r"\s*\((.*?)\);", text, flags=re.S).group(1)
@@ -45,7 +45,7 @@ ABACK = dict(dout=P, h=P, dtype=0, rows=4, f=8, ld=16, act=1, dh=P, stream=None)
 QUANT = dict(x=P, dtype=0, batch=1, rows=4, k=256, ld=256, group=64, codes=P, scale=P, zero=P, stream=None)
 DEQUANT = dict(codes=P, scale=P, zero=P, group=64, batch=1, rows=4, k=256, out=P, dtype=0, stream=None)
 VEC = dict(x=P, tokens=4, k=256, ld=256, per_slot=0, codes=P, scale=P, zero=None, group=64, experts=8, n=32, chosen=P,
-           topk=2, weights=None, act=0, out=P, out_dtype=0, stream=None)
+           topk=2, weights=None, act=0, out=P, out_dtype=0, scratch=None, scratch_bytes=0, stream=None)
 
 REFUSALS = [
     ("gmm_balance_loss", LOSS, NULL, [dict(logits=None), dict(chosen=None), dict(losses=None), dict(counts=None),
@@ -89,7 +89,10 @@ REFUSALS = [
                                      dict(ld=255), dict(ld=260), dict(k=LARGEST + 1024, ld=LARGEST + 1024),
                                      dict(n=LARGEST + 8), dict(tokens=LARGEST + 1)]),
     ("gmm_matvec_int4", VEC, ALIGN, [dict(x=ODD8), dict(codes=ODD8), dict(scale=ODD8), dict(zero=ODD8), dict(chosen=ODD),
-                                     dict(weights=ODD), dict(out_dtype=1, out=ODD)]),
+                                     dict(weights=ODD), dict(out_dtype=1, out=ODD), dict(scratch=ODD8)]),
+    ("gmm_matvec_int4", VEC, WORKSPACE, [dict(tokens=100, k=4096, ld=4096), dict(tokens=100, k=4096, ld=4096, scratch=P,
+                                                                                 scratch_bytes=1000),
+                                         dict(scratch_bytes=16)]),
 ]
 
 
@@ -112,6 +115,15 @@ def test_scratch_bytes(lib):
         assert lib.gmm_balance_scratch_bytes(tokens, experts, sequences) > 0
     for bad in [(-1, 8, 1), (8, 0, 1), (8, 1025, 1), (8, 8, 0), (8, 8, 3)]:
         assert lib.gmm_balance_scratch_bytes(*bad) == 0
+
+
+def test_matvec_scratch_bytes(lib):
+    assert lib.gmm_matvec_scratch_bytes(1, 4096, 128, 0, 8, 0) == 0
+    many = lib.gmm_matvec_scratch_bytes(64, 4096, 128, 0, 8, 0)
+    assert many == 64 * (4096 * 2 + 32 * 4 + 4) and lib.gmm_matvec_scratch_bytes(6400, 4096, 128, 0, 8, 0) == many
+    for bad in [(0, 4096, 128, 0, 8, 0), (-1, 4096, 128, 0, 8, 0), (64, 0, 128, 0, 8, 0), (64, 4096, 16, 0, 8, 0),
+                (64, 4096, 128, 0, 0, 0), (64, 4096, 128, 0, 33, 0)]:
+        assert lib.gmm_matvec_scratch_bytes(*bad) == 0
 
 
 # ---------------------------------------------------------------- the binding, on tensors without memory

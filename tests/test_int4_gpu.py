@@ -1,7 +1,8 @@
 """Weights in 4-bit integers, and their products with few tokens, against the 64-bit statement.
 
-Codes, scales and zero points are decided by exact quotients and have to be equal.  A product's sum is off by at
-most experts_reference.matvec_adds() units of 2^-23 of the sum of its terms' sizes, its output by half a step."""
+Codes, scales and zero points are decided by exact quotients and have to be equal.  A product is the sum
+of scale code x and -scale zero x, codes counted from 0; it is off by at most experts_reference.matvec_adds() units of
+2^-23 of the sum of these terms' sizes, its output by half a step."""
 
 import numpy as np
 import pytest
@@ -118,12 +119,13 @@ def check_matvec(x, w, experts=None, weights=None, act=None, out_dtype=torch.flo
     out = G.matvec_int4(x, w, experts, weights, act, out_dtype, **more)
     torch.cuda.synchronize()
     assert out.dtype == out_dtype
-    w64 = R.values(w)
+    w64, sizes = R.values(w), R.term_sizes(w)
     if experts is None:
-        want, size = R.matvec(R.as64(x), w64[None], np.zeros((x.shape[0], 1), int), None, act)
+        want, size = R.matvec(R.as64(x), w64[None], np.zeros((x.shape[0], 1), int), None, act, sizes[None])
         want, size = want[:, 0], size[:, 0]
     else:
-        want, size = R.matvec(R.as64(x), w64, experts.cpu().numpy(), None if weights is None else R.as64(weights), act)
+        want, size = R.matvec(R.as64(x), w64, experts.cpu().numpy(), None if weights is None else R.as64(weights), act,
+                              sizes)
     assert tuple(out.shape) == want.shape
     tol = (R.matvec_adds(x.shape[-1], w.group) + x.shape[-1] // 256) * 2.0 ** -23 * size
     tol = tol + R.half_step(out_dtype) * (np.abs(want) + tol) + 2.0 ** -126
@@ -238,6 +240,23 @@ def test_nan_and_infinity_reach_only_their_own_slots():
     assert out[4].isnan().all() and not out[5].isfinite().any()
     rest = [0, 1, 2, 3, 6, 7, 8]
     assert torch.equal(out[rest], G.matvec_int4(x[rest], w, experts[rest], out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("power", [-120, -60, 60, 110])
+def test_rows_of_x_of_any_size(power):
+    """Rows next to others that are far larger or smaller, and values in a row that span bf16's range."""
+    w = make(3, 48, 768, 64, True)
+    x = normal((10, 768), 3, dtype=torch.bfloat16)
+    x[2:5] *= 2.0 ** power
+    x[5, ::2] *= 2.0 ** power
+    x[6, 1:] = 0
+    x[7] = 0
+    x[8] = torch.tensor([1, 3 - 2 ** 15], dtype=torch.int16, device=DEV).view(torch.bfloat16).repeat(384)  # subnormal
+    experts = choose(10, 3, 2, 1, 0.0)
+    check_matvec(x, w, experts)
+    check_matvec(x.repeat(7, 1), w, experts.repeat(7, 1))
+    weights = normal((10, 2), 4)
+    check_matvec(x, w, experts, weights)
 
 
 def test_entries_past_the_last_group_are_not_read():
