@@ -45,10 +45,11 @@ namespace gmmk {
 namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kWindow = 256;                 // k of a stage
+constexpr int kWindow = 256;                 // k of a window of scales
+constexpr int kSpan = 2 * kWindow;           // k of a stage
 constexpr int kCols = 8;                     // columns of an item
-constexpr int kMaxSlots = 512;               // slots of a launch
-constexpr int kCodeBytes = 16 * kWindow / 2;
+constexpr int kMaxSlots = 256;               // slots of a launch
+constexpr int kPitch = kSpan / 2 + 16;      // bytes between rows of codes in shared memory: see below
 
 struct Params {
   const __nv_bfloat16* x;
@@ -56,7 +57,7 @@ struct Params {
   const uint8_t* codes;
   const uint8_t* scale;  // bf16, by windows
   const uint8_t* zero;
-  int32_t experts, n, k, windows, tiles;  // tiles of 16 rows of an expert
+  int32_t experts, n, k, windows, spans, tiles;  // tiles of 16 rows of an expert
   const int32_t* chosen;  // NULL: expert 0
   int32_t tokens, topk;
   const float* weights;   // NULL: no sum over slots
@@ -84,14 +85,31 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// (v & mask) ^ flip in one instruction, which takes at most one immediate: both are kept in registers.
+__device__ __forceinline__ uint32_t masked(uint32_t v, uint32_t mask, uint32_t flip) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(v), "r"(mask), "r"(flip));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
+// c += A B, or c = A B.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, bool first) {
+  if (first)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 constexpr int kTop = 116;                  // rows' largest values are brought to 2^116
 
@@ -150,26 +168,27 @@ __device__ __forceinline__ void make_ready(const __nv_bfloat16* x, int k, int wi
   if (lane % (kGroup / 8) == 0 && c < k) sums[c / kGroup] = sum * (kZero ? -0x1p-100f : -0x1p-97f) * 0x1p-33f;
 }
 
-// A warp's ring: kStages windows' codes, then their scales, then their zero points.  Four stages are
-// some 128 KB on their way to an SM, well over the 45 that memory's latency asks for at its rate.
+// A warp's two stages: codes, scales, zero points of a span.  Rows of codes are a 16-byte piece apart
+// from whole lines of banks, so that one word of 8 rows by 4 lanes meets all banks.  One stage of each
+// warp on its way is 64 KB for an SM, over the 45 that memory's latency asks for at its rate.
 template <int kGroup, bool kZero>
 struct Ring {
   static constexpr int kEach = kWindow / kGroup;  // groups of a window
-  static constexpr int kScales = 16 * kEach * 2, kZeros = kZero ? 16 * kEach : 0;
-  static constexpr int kStages = 4;
-  static constexpr int kBytes = kStages * (kCodeBytes + kScales + kZeros);
-  static_assert(kBytes % 128 == 0, "rows of codes are whole lines of banks");
+  static constexpr int kScaleAt = 16 * kPitch, kZeroAt = kScaleAt + 2 * 16 * kEach * 2;
+  static constexpr int kStage = kZeroAt + (kZero ? 2 * 16 * kEach : 0);
+  static constexpr int kBytes = 2 * kStage;
 };
 
 // The table of items that each CTA makes of the slots.
 struct Table {
-  int32_t expert[kMaxSlots];          // of each slot; then of each item
+  int32_t expert[kMaxSlots];          // of each slot; -1: none
+  int32_t item[kMaxSlots];            // the expert of each item
   int16_t slot[kMaxSlots][kCols];     // of each item's columns; -1: none
   int16_t head[kMaxSlots];            // of each item: its first slot
   int16_t row[kMaxSlots];             // of each slot: its row of x
   int32_t columns[kMaxSlots];         // of each item
   int16_t first[kMaxSlots / kCols + kMaxSlots + 1];  // with weights: first item of each 8 tokens
-  int32_t items;
+  int16_t number[kMaxSlots];          // of the item that a slot is the head of
   int32_t warp_heads[kWarps];
 };
 
@@ -194,105 +213,92 @@ __device__ __forceinline__ T load(const T* p) {
 template <int kGroup, bool kZero, bool kGated, bool kSum, bool kStaged>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   using R = Ring<kGroup, kZero>;
-  constexpr int kStages = R::kStages, kEach = R::kEach;
+  constexpr int kEach = R::kEach;
   griddep_begin();
   p.x = after_begin(p.x), p.codes = after_begin(p.codes), p.scale = after_begin(p.scale);
   p.zero = after_begin(p.zero), p.chosen = after_begin(p.chosen), p.weights = after_begin(p.weights);
   p.ready = after_begin(p.ready), p.sums = after_begin(p.sums), p.roots = after_begin(p.roots);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Table table;
-  __shared__ float part[2][kWarps][16][kCols + 1];
+  __shared__ float part[kWarps][16][kCols + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slots = p.tokens * p.topk;
 
   // ---- items: slots of the same expert in their order, 8 at a time (kSum: those of 8 tokens; a
   // token's second slot of the same expert has an item of its own).  A head is an item's first slot.
-  for (int i = tid; i < slots; i += kThreads) {
+  static_assert(kMaxSlots <= kThreads, "a slot a thread");
+  if (tid < slots) {
+    const int i = tid;
     const int e = p.chosen != nullptr ? p.chosen[i] : 0;
     table.expert[i] = e >= 0 && e < p.experts ? e : -1;
     table.row[i] = int16_t(p.x_slot != 0 ? i : i / p.topk);
     table.columns[i] = 0;
   }
   for (int i = tid; i < kMaxSlots * kCols / 2; i += kThreads) reinterpret_cast<uint32_t*>(table.slot)[i] = 0xFFFFFFFFu;
-  if (tid == 0) table.items = 0;
   const int64_t x_step = p.x_slot != 0 ? p.x_slot : p.x_token;
-  uint32_t* tops = reinterpret_cast<uint32_t*>(&part[0][0][0][0]);  // of the windows of x
+  uint32_t* tops = reinterpret_cast<uint32_t*>(&part[0][0][0]);  // of the windows of x
   if constexpr (kStaged) {
-    for (int i = warp; i < p.x_rows * p.windows; i += kWarps) {
-      const int row = i / p.windows;
-      const uint32_t top = largest(p.x + row * x_step, p.k, i - row * p.windows);
-      if (lane == 0) tops[i] = top;
-    }
+    for (int row = 0; row < p.x_rows; ++row)
+#pragma unroll 4
+      for (int w = warp; w < p.windows; w += kWarps) {
+        const uint32_t top = largest(p.x + row * x_step, p.k, w);
+        if (lane == 0) tops[row * p.windows + w] = top;
+      }
   }
   __syncthreads();
-  // a slot's item: its head's, of which this thread keeps what it needs until all have read the table
-  int head[kMaxSlots / kThreads], column[kMaxSlots / kThreads], mine[kMaxSlots / kThreads];
-#pragma unroll
-  for (int r = 0; r < kMaxSlots / kThreads; ++r) {
-    const int i = r * kThreads + tid;
-    head[r] = -1, column[r] = 0, mine[r] = -1;
-    if (i >= slots) continue;
-    const int e = table.expert[i];
-    mine[r] = e;
-    if (e < 0) continue;
-    head[r] = i;
+  // this thread's slot: its expert, its item's head and its column there
+  int mine = -1, head = -1, column = 0;
+  if (tid < slots) mine = table.expert[tid];
+  if (mine >= 0) {
+    head = tid;
     if constexpr (kSum) {
-      const int t = i / p.topk, t0 = t / kCols * kCols;
-      column[r] = t - t0;
+      const int t = tid / p.topk, t0 = t / kCols * kCols;
+      column = t - t0;
       int twin = 0;  // earlier slots of the token with this expert
-      for (int j = t * p.topk; j < i; ++j) twin += table.expert[j] == e;
+      for (int j = t * p.topk; j < tid; ++j) twin += table.expert[j] == mine;
       // the first token of the eight with so many of them
       for (int u = t0; u < t; ++u) {
         int seen = 0, at = -1;
         for (int j = u * p.topk; j < (u + 1) * p.topk; ++j)
-          if (table.expert[j] == e && seen++ == twin) at = j;
+          if (table.expert[j] == mine && seen++ == twin) at = j;
         if (at >= 0) {
-          head[r] = at;
+          head = at;
           break;
         }
       }
     } else {
-      int before = 0, at = i;
-      for (int j = 0; j < i; ++j)
-        if (table.expert[j] == e) {
+      int before = 0, at = tid;
+      for (int j = 0; j < tid; ++j)
+        if (table.expert[j] == mine) {
           if (before % kCols == 0) at = j;
           ++before;
         }
-      column[r] = before % kCols;
-      head[r] = column[r] == 0 ? i : at;
+      column = before % kCols;
+      head = column == 0 ? tid : at;
     }
+  }
+  // heads numbered in the order of their slots
+  const bool is_head = mine >= 0 && head == tid;
+  const uint32_t ballot = __ballot_sync(0xffffffffu, is_head);
+  if (lane == 0) table.warp_heads[warp] = __popc(ballot);
+  __syncthreads();
+  int items = 0, number = __popc(ballot & ((1u << lane) - 1u));
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) number += table.warp_heads[w];
+    items += table.warp_heads[w];
+  }
+  if (tid < slots) {
+    if (kSum && tid % (kCols * p.topk) == 0) table.first[tid / (kCols * p.topk)] = int16_t(number);
+    if (is_head) table.number[tid] = int16_t(number), table.head[number] = int16_t(tid), table.item[number] = mine;
   }
   __syncthreads();
-  // heads numbered in the order of their slots: expert[] turns into that of the items, and a head's
-  // number goes to number[] (the ring, not yet in use)
-  int32_t* number = reinterpret_cast<int32_t*>(smem);
-#pragma unroll
-  for (int r = 0; r < kMaxSlots / kThreads; ++r) {
-    const int i = r * kThreads + tid;
-    const bool is_head = head[r] == i && mine[r] >= 0;
-    const uint32_t ballot = __ballot_sync(0xffffffffu, is_head);
-    if (lane == 0) table.warp_heads[warp] = __popc(ballot);
-    __syncthreads();
-    int at = table.items;
-    for (int w = 0; w < warp; ++w) at += table.warp_heads[w];
-    at += __popc(ballot & ((1u << lane) - 1u));
-    if constexpr (kSum) {
-      if (i < slots && i % (kCols * p.topk) == 0) table.first[i / (kCols * p.topk)] = int16_t(at);
-    }
-    if (is_head) number[i] = at, table.head[at] = int16_t(i), table.expert[at] = mine[r];  // at <= i: read above by all
-    __syncthreads();
-    if (tid == 0)
-      for (int w = 0; w < kWarps; ++w) table.items += table.warp_heads[w];
-    __syncthreads();
+  if (mine >= 0) {
+    table.slot[table.number[head]][column] = int16_t(tid);
+    if constexpr (!kSum) atomicAdd(&table.columns[table.number[head]], 1);
   }
-#pragma unroll
-  for (int r = 0; r < kMaxSlots / kThreads; ++r)
-    if (head[r] >= 0) {
-      table.slot[number[head[r]]][column[r]] = int16_t(r * kThreads + tid);
-      if constexpr (!kSum) atomicAdd(&table.columns[number[head[r]]], 1);
-    }
   const int chunks = (p.tokens + kCols - 1) / kCols;
-  if (kSum && tid == 0) table.first[chunks] = int16_t(table.items);
+  if (kSum && tid == 0) table.first[chunks] = int16_t(items);
   __syncthreads();
 
   auto put = [&](int64_t row, int64_t c, float v) {
@@ -302,117 +308,127 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       static_cast<__nv_bfloat16*>(p.out)[row * p.out_n + c] = __float2bfloat16_rn(v);
   };
   if constexpr (!kSum) {  // rows of slots without an expert
-#pragma unroll
-    for (int r = 0; r < kMaxSlots / kThreads; ++r) {
-      uint32_t none = __ballot_sync(0xffffffffu, r * kThreads + tid < slots && mine[r] < 0);
-      while (none != 0) {
-        const int64_t i = r * kThreads + warp * 32 + __ffs(none) - 1;
-        none &= none - 1;
-        for (int64_t c = int64_t(blockIdx.x) * 32 + lane; c < p.out_n; c += int64_t(gridDim.x) * 32) put(i, c, 0.f);
-      }
+    uint32_t none = __ballot_sync(0xffffffffu, tid < slots && mine < 0);
+    while (none != 0) {
+      const int i = warp * 32 + __ffs(none) - 1;
+      none &= none - 1;
+      for (int64_t c = int64_t(blockIdx.x) * 32 + lane; c < p.out_n; c += int64_t(gridDim.x) * 32) put(i, c, 0.f);
     }
   }
 
-  // ---- the warp's part of its team's units, in order: pairs of an item and a window
+  // ---- the warp's part of its team's units, in order: pairs of an item and a span
   const int lg = p.team_log2, size = 1 << lg;    // warps of a team
   const int member = warp & (size - 1), team = warp >> lg;
   // teams of all CTAs; a CTA's are far apart, so that the last round is spread over all of them, or next
   // to one another, so that they read the same rows of x through the SM's cache
   const int teams = int(gridDim.x) * (kWarps >> lg);
-  const int groups = kSum ? chunks : table.items;
+  const int groups = kSum ? chunks : items;
   const int start = kStaged ? int(blockIdx.x) + team * int(gridDim.x) : int(blockIdx.x) * (kWarps >> lg) + team;
   const int dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
   Unit ahead{start / p.tiles, 0};
   ahead.tile = start - ahead.group * p.tiles;
   Unit here = ahead;
   uint8_t* const ring = smem + warp * R::kBytes;
-  const uint32_t ring_at = smem_u32(ring);
-  // the pairs of a unit that are this warp's: [begin, end) of its items' windows
-  const int begin_one = int((int64_t(p.windows) * member) >> lg), end_one = int((int64_t(p.windows) * (member + 1)) >> lg);
+  const int lane_row = lane >> 4, lane_chunk = lane & 15;
+  // where this lane's pieces of the next span go
+  const uint32_t fill_codes = smem_u32(ring) + lane_row * kPitch + lane_chunk * 16, fill_lane = smem_u32(ring) + lane * 16;
+  uint32_t fill = 0;
+  // the pairs of a unit that are this warp's: [begin, end) of its items' spans
+  const int begin_one = int((int64_t(p.spans) * member) >> lg), end_one = int((int64_t(p.spans) * (member + 1)) >> lg);
   auto part_of = [&](const Unit& u, int& first, int& begin, int& end) {
     if constexpr (kSum) {
       first = table.first[u.group];
-      const int64_t pairs = int64_t(table.first[u.group + 1] - first) * p.windows;
+      const int64_t pairs = int64_t(table.first[u.group + 1] - first) * p.spans;
       begin = int((pairs * member) >> lg), end = int((pairs * (member + 1)) >> lg);
     } else {
       first = u.group, begin = begin_one, end = end_one;
     }
   };
 
-  // what is fetched ahead: its pair, and where this lane's pieces are
-  const int lane_row = lane >> 3, lane_chunk = lane & 7;
-  constexpr int kHalfScales = 8 * kEach * 2 / 16, kHalfZeros = kZero ? 8 * kEach / 16 : 1;  // pieces of 8 rows'
-  const uint32_t lane_at = lane_row * 128 + ((lane_chunk ^ lane_row) << 4);  // and rows 4 on: chunks ^ 4
-  const int whole = p.k / kWindow;
+  // what is fetched ahead: its pair, and where this lane's pieces are: every other row of codes from
+  // lane_row on, and a piece of 8 rows' scales of one of the span's two windows
+  constexpr int kPieces = 8 * kEach * 2 / 16, kZeroPieces = kZero ? 8 * kEach / 16 : 1;
+  const int whole = p.k / kSpan;
   const int64_t pitch = p.k / 2, scale_step = int64_t(p.n) * kEach * 2;
-  int pair = 0, pair_end = 0, item = 0, window = 0;
+  int pair = 0, pair_end = 0, item = 0, span = 0;
   bool second = false;  // the tile has its second 8 rows
   const uint8_t *code0 = nullptr, *code1 = nullptr, *scale = nullptr, *zero = nullptr;
   auto aim = [&] {
-    const int64_t e = table.expert[item];
+    const int64_t e = table.item[item];
     const int row0 = kGated ? ahead.tile * 8 : ahead.tile * 16;
     second = kGated || row0 + 8 < p.n;
     const int row1 = !second ? row0 : kGated ? p.n / 2 + row0 : row0 + 8;
-    const uint8_t* at = p.codes + (e * p.n + lane_row) * pitch + int64_t(window) * (kWindow / 2) + lane_chunk * 16;
+    const uint8_t* at = p.codes + (e * p.n + lane_row) * pitch + int64_t(span) * (kSpan / 2) + lane_chunk * 16;
     code0 = at + row0 * pitch, code1 = at + row1 * pitch;
-    const int64_t in_window = (e * p.windows + window) * p.n;
-    scale = p.scale + (in_window + (lane < kHalfScales ? row0 : row1)) * (kEach * 2) + lane % kHalfScales * 16;
-    if constexpr (kZero) zero = p.zero + (in_window + (lane < kHalfZeros ? row0 : row1)) * kEach + lane % kHalfZeros * 16;
+    const int64_t in_window = (e * p.windows + 2 * int64_t(span)) * p.n;
+    scale = p.scale + (in_window + int64_t(lane / (2 * kPieces)) * p.n + (lane / kPieces % 2 ? row1 : row0)) * (kEach * 2) +
+            lane % kPieces * 16;
+    if constexpr (kZero)
+      zero = p.zero + (in_window + int64_t(lane / (2 * kZeroPieces)) * p.n + (lane / kZeroPieces % 2 ? row1 : row0)) * kEach +
+             lane % kZeroPieces * 16;
   };
   auto enter = [&] {
     while (ahead.group < groups) {
       int first;
       part_of(ahead, first, pair, pair_end);
       if (pair < pair_end) {
-        const int skip = kSum ? pair / p.windows : 0;
-        item = first + skip, window = pair - skip * p.windows;
+        const int skip = kSum ? pair / p.spans : 0;
+        item = first + skip, span = pair - skip * p.spans;
         aim();
         return;
       }
       ahead.advance(dgroup, dtile, p.tiles);
     }
   };
-  auto fetch = [&](int stage) {  // and on to the next
+  auto fetch = [&] {  // and on to the next
     if (ahead.group < groups) {
-      const uint32_t to = ring_at + stage * kCodeBytes + lane_at;
-      const uint32_t to_scale = ring_at + kStages * kCodeBytes + stage * R::kScales + lane * 16;
-      const uint32_t to_zero = ring_at + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros + lane * 16;
-      if (second && window < whole) {
-        copy16(to, code0);
-        copy16((to ^ 64) + 512, code0 + 4 * pitch);
-        copy16(to + 1024, code1);
-        copy16((to ^ 64) + 1536, code1 + 4 * pitch);
-        if (lane < 2 * kHalfScales) copy16(to_scale, scale);
+      const uint32_t to = fill_codes + fill, to_lane = fill_lane + fill;
+      if (second && span < whole) {
+        const uint8_t *c0 = code0, *c1 = code1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          copy16(to + 2 * i * kPitch, c0);
+          copy16(to + (8 + 2 * i) * kPitch, c1);
+          c0 += 2 * pitch, c1 += 2 * pitch;
+        }
+        if (lane < 4 * kPieces) copy16(to_lane + R::kScaleAt, scale);
         if constexpr (kZero)
-          if (lane < 2 * kHalfZeros) copy16(to_zero, zero);
+          if (lane < 4 * kZeroPieces) copy16(to_lane + R::kZeroAt, zero);
       } else {  // zeros for what is past k or n, with an address inside
-        const bool in = window * kWindow + lane_chunk * 32 < p.k;
+        const bool in = span * kSpan + lane_chunk * 32 < p.k, two = 2 * span + 1 < p.windows;
         const int64_t back = in ? 0 : lane_chunk * -16;
-        copy16(to, code0 + back, in);
-        copy16((to ^ 64) + 512, code0 + 4 * pitch + back, in);
-        copy16(to + 1024, code1 + back, in && second);
-        copy16((to ^ 64) + 1536, code1 + 4 * pitch + back, in && second);
-        if (lane < 2 * kHalfScales) copy16(to_scale, scale, lane < kHalfScales || second);
-        if constexpr (kZero)
-          if (lane < 2 * kHalfZeros) copy16(to_zero, zero, lane < kHalfZeros || second);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          copy16(to + 2 * i * kPitch, code0 + 2 * i * pitch + back, in);
+          copy16(to + (8 + 2 * i) * kPitch, code1 + 2 * i * pitch + back, in && second);
+        }
+        if (lane < 4 * kPieces) {
+          const bool there = (two || lane < 2 * kPieces) && (second || lane / kPieces % 2 == 0);
+          copy16(to_lane + R::kScaleAt, there ? scale : p.scale, there);
+        }
+        if constexpr (kZero) {
+          if (lane < 4 * kZeroPieces) {
+            const bool there = (two || lane < 2 * kZeroPieces) && (second || lane / kZeroPieces % 2 == 0);
+            copy16(to_lane + R::kZeroAt, there ? zero : p.zero, there);
+          }
+        }
       }
+      fill = R::kStage - fill;
       if (++pair == pair_end) {
         ahead.advance(dgroup, dtile, p.tiles);
         enter();
-      } else if (kSum && ++window == p.windows) {
-        window = 0, ++item;
+      } else if (++span == p.spans) {
+        span = 0, ++item;
         aim();
       } else {
-        if constexpr (!kSum) ++window;
-        code0 += kWindow / 2, code1 += kWindow / 2, scale += scale_step;
-        if constexpr (kZero) zero += scale_step / 2;
+        code0 += kSpan / 2, code1 += kSpan / 2, scale += 2 * scale_step;
+        if constexpr (kZero) zero += scale_step;
       }
     }
     copies_commit();
   };
   enter();
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(s);
+  fetch();
 
   // rows of x made ready: in shared memory, or by the kernel ahead
   const int x_groups = p.k / kGroup;
@@ -424,25 +440,38 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     auto* to_sums = reinterpret_cast<float*>(to + p.x_rows * p.x_pitch);
     float* to_roots = to_sums + p.x_rows * x_groups;
     ready = to, sums = to_sums, roots = to_roots;
-    for (int i = warp; i < p.x_rows * p.windows; i += kWarps) {
-      const int row = i / p.windows, power = power_of(tops + row * p.windows, p.windows);
-      make_ready<kGroup, kZero>(p.x + row * x_step, p.k, i - row * p.windows, power, to + row * p.x_pitch,
-                                to_sums + row * x_groups);
-      if (lane == 0) to_roots[row] = root_of(power);
+    for (int row = 0; row < p.x_rows; ++row) {
+      const int power = power_of(tops + row * p.windows, p.windows);
+#pragma unroll 4
+      for (int w = warp; w < p.windows; w += kWarps)
+        make_ready<kGroup, kZero>(p.x + row * x_step, p.k, w, power, to + row * p.x_pitch, to_sums + row * x_groups);
+      if (tid == 0) to_roots[row] = root_of(power);
     }
     __syncthreads();
   }
 
   const int g = lane >> 2, t4 = lane & 3;
-  int stage = 0, parity = 0, last = -1;
+  auto team_sync = [&] {
+    if (lg == 0)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 << lg) : "memory");
+  };
+  int last = -1;
+  const uint8_t* const words = ring + g * kPitch + t4 * 4;  // this lane's words of a stage
+  const int scale_off = R::kScaleAt + g * kEach * 2 - g * kPitch - t4 * 4, zero_off = R::kZeroAt + g * kEach - g * kPitch - t4 * 4;
+  int stage = 0;
+  // two's complement + 8 is the top bit flipped
+  const uint32_t mask_low = in_register(0x000F000Fu), mask_high = in_register(0x00F000F0u);
+  const uint32_t flip_low = in_register(0x00080008u), flip_high = in_register(0x00800080u);
   const __nv_bfloat16* xp = nullptr;                // column g of the last item, from this lane's k on
   const float *sums0 = nullptr, *sums1 = nullptr;   // of columns 2 t4 and 2 t4 + 1
   float w0 = 0.f, w1 = 0.f, root0 = 0.f, root1 = 0.f;
   bool has0 = false, has1 = false;
-  for (; here.group < groups; here.advance(dgroup, dtile, p.tiles), parity ^= 1) {
+  for (; here.group < groups; here.advance(dgroup, dtile, p.tiles)) {
     int first, at, end;
     part_of(here, first, at, end);
-    int now = first + (kSum ? at / p.windows : 0), w = kSum ? at - (now - first) * p.windows : at;
+    int now = first + (kSum ? at / p.spans : 0), w = kSum ? at - (now - first) * p.spans : at;
     float res[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (; at < end; ++at) {
       if (now != last) {
@@ -459,70 +488,77 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
           root0 = roots[r0], root1 = roots[r1];
         }
       }
-      const int k0 = w * kWindow;
-      copies_wait<kStages - 2>();
+      const int k0 = w * kSpan;
+      copies_wait<0>();
       __syncwarp();
-      fetch(stage == 0 ? kStages - 1 : stage - 1);
-      const uint8_t* codes = ring + stage * kCodeBytes + g * 128 + t4 * 4;
-      const uint8_t* scales = ring + kStages * kCodeBytes + stage * R::kScales;
-      const uint8_t* zeros = ring + kStages * (kCodeBytes + R::kScales) + stage * R::kZeros;
+      fetch();
+      const uint8_t *codes = words + stage, *scales = codes + scale_off, *zeros = codes + zero_off;
+      stage = R::kStage - stage;
+      const __nv_bfloat16* xk = xp + k0;
+      const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
       auto group = [&](int q, float s0, float s1) {
-        const float n0 = load<kStaged>(sums0 + w * kEach + q), n1 = load<kStaged>(sums1 + w * kEach + q);
-        float c[4] = {n0, n1, n0, n1};
-        if constexpr (kZero) {
-          const float z0 = float(zeros[g * kEach + q]), z1 = float(zeros[(g + 8) * kEach + q]);
-          c[0] *= z0, c[1] *= z0, c[2] *= z1, c[3] *= z1;
-        }
-        constexpr uint32_t kFlip = kZero ? 0u : 0x00080008u;  // two's complement + 8 is the top bit flipped
+        float c[4];
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
           const int chunk = q * (kGroup / 32) + j;
-          const uint4 b = load<kStaged>(reinterpret_cast<const uint4*>(xp + k0 + chunk * 32));
-          const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + ((chunk ^ g) << 4)), va = wa >> 8;
-          const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 1024 + ((chunk ^ g) << 4)), vb = wb >> 8;
-          auto low = [](uint32_t v) { return (v & 0x000F000Fu) ^ kFlip; };
-          auto high = [](uint32_t v) { return (v & 0x00F000F0u) ^ (kFlip << 4); };
-          mma(c, low(wa), low(wb), high(wa), high(wb), b.x, b.y);
-          mma(c, low(va), low(vb), high(va), high(vb), b.z, b.w);
+          const uint4 b = load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32));
+          const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + chunk * 16), va = wa >> 8;
+          const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + chunk * 16), vb = wb >> 8;
+          auto low = [&](uint32_t v) { return kZero ? v & 0x000F000Fu : masked(v, mask_low, flip_low); };
+          auto high = [&](uint32_t v) { return kZero ? v & 0x00F000F0u : masked(v, mask_high, flip_high); };
+          mma(c, low(wa), low(wb), high(wa), high(wb), b.x, b.y, j == 0);
+          mma(c, low(va), low(vb), high(va), high(vb), b.z, b.w, false);
+        }
+        const float n0 = load<kStaged>(sums0k + q), n1 = load<kStaged>(sums1k + q);
+        if constexpr (kZero) {
+          const int zq = q / kEach * (16 * kEach) + q % kEach;
+          const float z0 = float(zeros[zq]), z1 = float(zeros[8 * kEach + zq]);
+          c[0] = fmaf(z0, n0, c[0]), c[1] = fmaf(z0, n1, c[1]), c[2] = fmaf(z1, n0, c[2]), c[3] = fmaf(z1, n1, c[3]);
+        } else {
+          c[0] += n0, c[1] += n1, c[2] += n0, c[3] += n1;
         }
         acc[0] = fmaf(s0, c[0], acc[0]), acc[1] = fmaf(s0, c[1], acc[1]);
         acc[2] = fmaf(s1, c[2], acc[2]), acc[3] = fmaf(s1, c[3], acc[3]);
       };
-      if (k0 + kWindow <= p.k) {
+      if (k0 + kSpan <= p.k) {
         using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
-        const Scales sa = reinterpret_cast<const Scales*>(scales)[g], sb = reinterpret_cast<const Scales*>(scales)[g + 8];
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-          const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[q / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[q / 2];
-          group(q, __uint_as_float(q % 2 ? pa & 0xFFFF0000u : pa << 16), __uint_as_float(q % 2 ? pb & 0xFFFF0000u : pb << 16));
+        for (int half = 0; half < 2; ++half) {
+          const Scales sa = reinterpret_cast<const Scales*>(scales)[16 * half], sb = reinterpret_cast<const Scales*>(scales)[16 * half + 8];
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[i / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[i / 2];
+            group(half * kEach + i, __uint_as_float(i % 2 ? pa & 0xFFFF0000u : pa << 16),
+                  __uint_as_float(i % 2 ? pb & 0xFFFF0000u : pb << 16));
+          }
         }
       } else {
-        const __nv_bfloat16* one = reinterpret_cast<const __nv_bfloat16*>(scales) + g * kEach;
+        const __nv_bfloat16* one = reinterpret_cast<const __nv_bfloat16*>(scales);
         const int left = (p.k - k0) / kGroup;
 #pragma unroll 1
-        for (int q = 0; q < left; ++q) group(q, __bfloat162float(one[q]), __bfloat162float(one[8 * kEach + q]));
+        for (int q = 0; q < left; ++q) {
+          const int sq = q / kEach * (16 * kEach) + q % kEach;
+          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]));
+        }
       }
-      stage = stage + 1 == kStages ? 0 : stage + 1;
       if (!kSum) {
         ++w;
-      } else if (++w == p.windows || at + 1 == end) {
+      } else if (++w == p.spans || at + 1 == end) {
         if (has0) res[0] += w0 * (acc[0] * root0 * root0), res[2] += w0 * (acc[2] * root0 * root0);
         if (has1) res[1] += w1 * (acc[1] * root1 * root1), res[3] += w1 * (acc[3] * root1 * root1);
         acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        if (w == p.windows) w = 0, ++now;
+        if (w == p.spans) w = 0, ++now;
       }
     }
     const float* mine4 = kSum ? res : acc;
-    part[parity][warp][g][2 * t4] = mine4[0], part[parity][warp][g][2 * t4 + 1] = mine4[1];
-    part[parity][warp][g + 8][2 * t4] = mine4[2], part[parity][warp][g + 8][2 * t4 + 1] = mine4[3];
-    if (lg == 0)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 << lg) : "memory");
+    team_sync();  // the last unit's sums have been read
+    part[warp][g][2 * t4] = mine4[0], part[warp][g][2 * t4 + 1] = mine4[1];
+    part[warp][g + 8][2 * t4] = mine4[2], part[warp][g + 8][2 * t4 + 1] = mine4[3];
+    team_sync();
     // sums over the team's warps, and out
     constexpr int kRows = kGated ? 8 : 16;
     const int columns = kSum ? p.tokens - here.group * kCols : table.columns[here.group];
-    const float* sum = &part[parity][team << lg][0][0];
+    const float* sum = &part[team << lg][0][0];
     for (int i = member * 32 + lane; i < kRows * min(columns, kCols); i += 32 << lg) {
       const int row = i % kRows, col = i / kRows;
       const int64_t c = int64_t(here.tile) * kRows + row;
@@ -568,14 +604,14 @@ __global__ void __launch_bounds__(256) make_ready_kernel(Params p) {
   if (threadIdx.x == 0) p.roots[row] = root_of(power);
 }
 
-constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * 2 * kWarps * 16 * (kCols + 1);
+constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * kWarps * 16 * (kCols + 1);
 
 // Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the groups' sums, the roots.
 int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + k / group * 4 + 4); }
 // In shared memory rows are half a line of banks apart.
 int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
 bool is_staged(int64_t rows, int64_t k, int group, bool zero) {
-  const int64_t each = kWindow / group, ring = int64_t(kWarps) * 4 * (kCodeBytes + 16 * each * (zero ? 3 : 2));
+  const int64_t each = kWindow / group, ring = int64_t(kWarps) * 2 * (16 * kPitch + 2 * 16 * each * (zero ? 3 : 2));
   return ready_bytes(rows, staged_pitch(k), k, group) <= int64_t(kMaxShared) - ring;
 }
 int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
@@ -583,7 +619,6 @@ int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
 template <int kGroup, bool kZero, bool kGated, bool kSum>
 cudaError_t launch(const Params& p, bool staged, int64_t units, int sms, cudaStream_t stream) {
   using R = Ring<kGroup, kZero>;
-  static_assert(R::kStages == 4, "is_staged() counts them");
   const size_t smem = size_t(kWarps) * R::kBytes + (staged ? size_t(ready_bytes(p.x_rows, p.x_pitch, p.k, kGroup)) : 0);
   auto kern = staged ? matvec_kernel<kGroup, kZero, kGated, kSum, true> : matvec_kernel<kGroup, kZero, kGated, kSum, false>;
   // for every launch: the attribute is the current device's, and one size for all calls
@@ -605,7 +640,7 @@ cudaError_t matvec(Params p, int group, bool staged, int sms, cudaStream_t strea
   // units at most: a tile of each slot's expert, or of each 8 tokens with their experts one after another
   const bool sums = p.weights != nullptr;
   const int64_t units = int64_t(p.tiles) * (sums ? (p.tokens + kCols - 1) / kCols : p.tokens * p.topk);
-  const int64_t pairs = int64_t(p.windows) * (!sums ? 1 : (p.tokens < kCols ? p.tokens : kCols) * p.topk);
+  const int64_t pairs = int64_t(p.spans) * (!sums ? 1 : (p.tokens < kCols ? p.tokens : kCols) * p.topk);
   // warps to a tile: those with which the last team is done first, a unit's start and end counted as a window
   int64_t best = INT64_MAX;
   for (int lg = 0; (1 << lg) <= kWarps; ++lg) {
@@ -671,6 +706,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     p.codes = static_cast<const uint8_t*>(codes), p.scale = static_cast<const uint8_t*>(scale);
     p.zero = static_cast<const uint8_t*>(zero);
     p.experts = num_experts, p.n = int32_t(n), p.k = int32_t(k), p.windows = int32_t((k + kWindow - 1) / kWindow);
+    p.spans = int32_t((k + kSpan - 1) / kSpan);
     p.tiles = int32_t((n + 15) / 16);
     p.chosen = experts == nullptr ? nullptr : experts + t0 * topk;
     p.tokens = int32_t(count), p.topk = topk;
