@@ -489,25 +489,34 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         }
       }
       const int k0 = w * kSpan;
+      const __nv_bfloat16* xk = xp + k0;
+      // x of the next four chunks is read ahead of its use: it may come from the L2
+      uint4 b[2][4];
+      auto read_x = [&](uint4 (&to)[4], int quad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (quad * 4 + i) * 32));
+      };
+      const bool full = k0 + kSpan <= p.k;
+      if (full) read_x(b[0], 0);
       copies_wait<0>();
       __syncwarp();
       fetch();
       const uint8_t *codes = words + stage, *scales = codes + scale_off, *zeros = codes + zero_off;
       stage = R::kStage - stage;
-      const __nv_bfloat16* xk = xp + k0;
       const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
-      auto group = [&](int q, float s0, float s1) {
+      // one group, its chunks' x given by `x_of`
+      auto group = [&](int q, float s0, float s1, auto x_of) {
         float c[4];
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
           const int chunk = q * (kGroup / 32) + j;
-          const uint4 b = load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32));
+          const uint4 v = x_of(chunk);
           const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + chunk * 16), va = wa >> 8;
           const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + chunk * 16), vb = wb >> 8;
           auto low = [&](uint32_t v) { return kZero ? v & 0x000F000Fu : masked(v, mask_low, flip_low); };
           auto high = [&](uint32_t v) { return kZero ? v & 0x00F000F0u : masked(v, mask_high, flip_high); };
-          mma(c, low(wa), low(wb), high(wa), high(wb), b.x, b.y, j == 0);
-          mma(c, low(va), low(vb), high(va), high(vb), b.z, b.w, false);
+          mma(c, low(wa), low(wb), high(wa), high(wb), v.x, v.y, j == 0);
+          mma(c, low(va), low(vb), high(va), high(vb), v.z, v.w, false);
         }
         const float n0 = load<kStaged>(sums0k + q), n1 = load<kStaged>(sums1k + q);
         if constexpr (kZero) {
@@ -520,16 +529,21 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         acc[0] = fmaf(s0, c[0], acc[0]), acc[1] = fmaf(s0, c[1], acc[1]);
         acc[2] = fmaf(s1, c[2], acc[2]), acc[3] = fmaf(s1, c[3], acc[3]);
       };
-      if (k0 + kSpan <= p.k) {
+      if (full) {
         using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
+        constexpr int kQuad = 128 / kGroup;  // groups of four chunks
+        Scales sa, sb;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const Scales sa = reinterpret_cast<const Scales*>(scales)[16 * half], sb = reinterpret_cast<const Scales*>(scales)[16 * half + 8];
+        for (int quad = 0; quad < 4; ++quad) {
+          if (quad < 3) read_x(b[(quad + 1) % 2], quad + 1);
+          if (quad % 2 == 0)
+            sa = reinterpret_cast<const Scales*>(scales)[8 * quad], sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[i / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[i / 2];
-            group(half * kEach + i, __uint_as_float(i % 2 ? pa & 0xFFFF0000u : pa << 16),
-                  __uint_as_float(i % 2 ? pb & 0xFFFF0000u : pb << 16));
+          for (int i = 0; i < kQuad; ++i) {
+            const int at = quad % 2 * kQuad + i;  // in the window
+            const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
+            group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
+                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), [&](int chunk) { return b[quad % 2][chunk % 4]; });
           }
         }
       } else {
@@ -538,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 #pragma unroll 1
         for (int q = 0; q < left; ++q) {
           const int sq = q / kEach * (16 * kEach) + q % kEach;
-          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]));
+          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]),
+                [&](int chunk) { return load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
         }
       }
       if (!kSum) {
