@@ -14,8 +14,11 @@
 // it lacks, is correct to 2^-40 before its one rounding, at a third of a division's
 // instructions.  Scales whose reciprocal is not a normal number are divided by.
 //
-// Bound by memory: 2 bytes read and 1/2 written per value (bf16).  A warp takes a
-// window of 256 values of a row, a lane 8 of them.
+// Bound by memory, 2 bytes read and 1/2 written per value (bf16), and nearly by the instructions that
+// a value takes, so these are few: a lane takes 16 consecutive values, a warp 512 of a row at a time;
+// codes are rounded by adding 1.5 2^23 and put together as they stand, sum of 16^i (1.5 2^23 + code),
+// the constant part taken off at the end.  Without zero points nothing has to be kept within -8 .. 7,
+// because a scale of 8 bits is at most 2^-8 of itself below max|x| / 7 (subnormal ones take a longer way).
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -32,103 +35,170 @@ constexpr int kWindow = 256, kThreads = 256;
 
 struct QuantParams {
   const void* x;
-  int64_t rows, rows_per_batch, ld;  // of all batches
-  int64_t k, windows;
+  int64_t rows, ld;  // of all batches
+  int32_t rows_per_batch, parts_log2;  // warps to a row
+  int32_t k, windows, wide;
   uint8_t* codes;
   __nv_bfloat16* scale;
   uint8_t* zero;
 };
 
+// 16 values as they are stored.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, bool wide, float (&v)[8]) {
-  if (wide) {
-    uint4 raw[sizeof(T) / 2];
+struct Values {
+  static constexpr int kWords = 16 * int(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zeros() {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const T* t = reinterpret_cast<const T*>(raw);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = float(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = float(p[i]);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-}
-
-// round(x / s) of exact quotients.
-struct Quotient {
-  float s, r, rest;
-  bool plain;
-  __device__ __forceinline__ explicit Quotient(float scale) : s(scale) {
-    plain = !(s >= 0x1p-100f && s <= 0x1p100f);
-    r = __frcp_rn(s), rest = fmaf(-s, r, 1.f) * r;
+  __device__ __forceinline__ void load(const T* p, bool wide) {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+      }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = uint32_t(__ldg(h + 2 * i)) | uint32_t(__ldg(h + 2 * i + 1)) << 16;
+    }
   }
-  __device__ __forceinline__ float operator()(float x) const {
-    return rintf(plain ? __fdiv_rn(x, s) : fmaf(x, r, x * rest));
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  // The largest magnitude as ordered bits: a NaN is above infinity.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      return max(m & 0xFFFFu, m >> 16) << 16;
+    }
   }
 };
 
-// kLanes lanes hold a group (8 values each).
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 w, x, y, z; "
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+constexpr float kRound = 12582912.f;                  // 1.5 2^23: a sum with it is rounded to a whole number
+constexpr uint32_t kRoundBits = 0x4B400000u;
+constexpr float kLargest = 3.402823466e38f;
+
+// kLanes lanes hold a group (16 values each).
 template <class T, int kLanes, bool kZero>
-__global__ void __launch_bounds__(kThreads) quantize_int4_kernel(QuantParams p, bool wide) {
+__global__ void __launch_bounds__(kThreads) quantize_int4_kernel(QuantParams p) {
   griddep_begin();
   p.x = after_begin(p.x);
-  constexpr int kEach = 32 / kLanes;  // groups of a window
+  constexpr int kEach = 16 / kLanes;  // groups of a window
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  if (w >= p.rows * p.windows) return;
-  const int64_t row = w / p.windows, window = w - row * p.windows;
-  const int64_t c = window * kWindow + lane * 8;
-  const bool in = c < p.k;  // k is whole groups, so all of a group's lanes are
-  float v[8];
-  if (in) {
-    load8<T>(static_cast<const T*>(p.x) + row * p.ld + c, wide, v);
-  } else {
+  const int64_t warp = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t row = warp >> p.parts_log2;
+  if (row >= p.rows) return;
+  const int part = int(warp) & ((1 << p.parts_log2) - 1), step = 512 << p.parts_log2;
+  const int batch = int(row) / p.rows_per_batch, r = int(row) - batch * p.rows_per_batch;
+  const T* x = static_cast<const T*>(p.x) + row * p.ld;
+  uint8_t* codes = p.codes + row * (p.k / 2);
+  const int64_t at_batch = int64_t(batch) * p.windows;
+  const int64_t whole = int64_t(p.windows) * kWindow;
+#pragma unroll 2
+  for (int64_t c = part * 512 + lane * 16; c - lane * 16 < whole; c += step) {
+    const bool in = c < p.k;  // k is whole groups, so all of a group's lanes are
+    Values<T> v;
+    if (in)
+      v.load(x + c, p.wide != 0);
+    else
+      v.zeros();
+    float span, lo = 0.f;
+    bool fine = true;
+    if constexpr (kZero) {
+      float hi = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  }
-  float span;
-  float lo = 0.f;
-  bool fine = true;
-  if constexpr (kZero) {
-    float hi = 0.f;
+      for (int i = 0; i < 16; ++i) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]);
+      fine = v.top() < 0x7F800000u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]), fine &= fabsf(v[i]) <= 3.402823466e38f;
+      for (int d = 1; d < kLanes; d <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+        fine &= __shfl_xor_sync(0xffffffffu, int(fine), d) != 0;
+      }
+      span = hi - lo;
+      fine &= span <= kLargest;
+    } else {
+      uint32_t top = v.top();
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-      fine &= __shfl_xor_sync(0xffffffffu, int(fine), d) != 0;
+      for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      span = __uint_as_float(top);
+      fine = top < 0x7F800000u;
     }
-    span = hi - lo;
-    fine &= span <= 3.402823466e38f;
-  } else {
-    uint32_t top = 0;  // magnitudes as ordered bits: a NaN is above infinity
+    const __nv_bfloat16 scale =
+        __float2bfloat16_rn(fine ? __fdiv_rn(span, kZero ? 15.f : 7.f) : __uint_as_float(0x7FC00000u));
+    const float s = __bfloat162float(scale);
+    uint32_t code[2] = {0, 0};
+    float zero = 0.f;
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+      const float r = __frcp_rn(s), rest = fmaf(-s, r, 1.f) * r;
+      float most = 0.f;
+      if constexpr (kZero) zero = fminf(rintf(fmaf(-lo, r, -lo * rest)), 15.f), most = 15.f - zero;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t sum = 0;
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    span = __uint_as_float(top);
-    fine = top < 0x7F800000u;
-  }
-  const __nv_bfloat16 scale = __float2bfloat16_rn(fine ? __fdiv_rn(span, kZero ? 15.f : 7.f) : __uint_as_float(0x7FC00000u));
-  const float s = __bfloat162float(scale);
-  uint32_t code = 0;
-  float zero = 0.f;
-  if (s > 0.f) {
-    const Quotient q(s);
-    if constexpr (kZero) zero = fminf(q(-lo), 15.f);
+        for (int i = 6; i >= 0; i -= 2) {
+          const float2 a = make_float2(v[8 * h + i], v[8 * h + i + 1]);
+          float2 q = fma2(a, make_float2(r, r), mul2(a, make_float2(rest, rest)));
+          if constexpr (kZero) q.x = fminf(q.x, most), q.y = fminf(q.y, most);
+          q = add2(q, make_float2(kRound, kRound));
+          sum = (sum * 16 + __float_as_uint(q.y)) * 16 + __float_as_uint(q.x);
+        }
+        sum -= kRoundBits * 0x11111111u;  // sum of 16^i code, which borrows where codes are negative
+        code[h] = kZero ? sum + uint32_t(int(zero)) * 0x11111111u : (sum + 0x88888888u) ^ 0x88888888u;
+      }
+    } else if (s > 0.f) {  // reciprocals that are no normal numbers
+      if constexpr (kZero) zero = fminf(rintf(__fdiv_rn(-lo, s)), 15.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = kZero ? fminf(fmaxf(q(v[i]) + zero, 0.f), 15.f) : fminf(fmaxf(q(v[i]), -8.f), 7.f);
-      code |= (uint32_t(int(n)) & 15u) << (4 * i);
+      for (int i = 0; i < 16; ++i) {
+        const float q = rintf(__fdiv_rn(v[i], s));
+        const float n = kZero ? fminf(fmaxf(q + zero, 0.f), 15.f) : fminf(fmaxf(q, -8.f), 7.f);
+        code[i / 8] |= (uint32_t(int(n)) & 15u) << (4 * (i % 8));
+      }
     }
-  }
-  if (in) *reinterpret_cast<uint32_t*>(p.codes + row * (p.k / 2) + c / 2) = code;
-  if (lane % kLanes == 0) {
-    const int64_t batch = row / p.rows_per_batch, r = row - batch * p.rows_per_batch;
-    const int64_t at = ((batch * p.windows + window) * p.rows_per_batch + r) * kEach + lane / kLanes;
-    p.scale[at] = in ? scale : __float2bfloat16_rn(0.f);
-    if constexpr (kZero) p.zero[at] = in ? uint8_t(zero) : 0;
+    if (in) *reinterpret_cast<uint2*>(codes + c / 2) = make_uint2(code[0], code[1]);
+    const int64_t window = c / kWindow;
+    if (lane % kLanes == 0 && window < p.windows) {
+      const int64_t at = ((at_batch + window) * p.rows_per_batch + r) * kEach + lane % 16 / kLanes;
+      p.scale[at] = in ? scale : __float2bfloat16_rn(0.f);
+      if constexpr (kZero) p.zero[at] = in ? uint8_t(zero) : 0;
+    }
   }
 }
 
@@ -136,62 +206,92 @@ struct DequantParams {
   const uint8_t* codes;
   const __nv_bfloat16* scale;
   const uint8_t* zero;
-  int64_t rows, rows_per_batch, k, windows;
+  int64_t rows;
+  int32_t rows_per_batch, parts_log2, k, windows, wide;
   void* out;
 };
 
-template <class T, int kLanes>
-__global__ void __launch_bounds__(kThreads) dequantize_int4_kernel(DequantParams p, bool wide) {
+// A warp takes windows of a row, a lane 8 codes, kLanes lanes a group.
+template <class T, int kLanes, bool kZero>
+__global__ void __launch_bounds__(kThreads) dequantize_int4_kernel(DequantParams p) {
   griddep_begin();
   p.codes = after_begin(p.codes), p.scale = after_begin(p.scale), p.zero = after_begin(p.zero);
   constexpr int kEach = 32 / kLanes;
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  if (w >= p.rows * p.windows) return;
-  const int64_t row = w / p.windows, window = w - row * p.windows;
-  const int64_t c = window * kWindow + lane * 8;
-  if (c >= p.k) return;
-  const int64_t batch = row / p.rows_per_batch, r = row - batch * p.rows_per_batch;
-  const int64_t at = ((batch * p.windows + window) * p.rows_per_batch + r) * kEach + lane / kLanes;
-  const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(p.codes + row * (p.k / 2) + c / 2));
-  const float s = __bfloat162float(p.scale[at]);
-  const int zero = p.zero != nullptr ? p.zero[at] : 8;
-  const uint32_t flip = p.zero != nullptr ? 0u : 8u;  // two's complement + 8
-  T v[8];
+  const int64_t warp = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t row = warp >> p.parts_log2;
+  if (row >= p.rows) return;
+  const int part = int(warp) & ((1 << p.parts_log2) - 1), step = 1 << p.parts_log2;
+  const int batch = int(row) / p.rows_per_batch, r = int(row) - batch * p.rows_per_batch;
+  const uint8_t* codes = p.codes + row * (p.k / 2) + lane * 4;
+  T* out = static_cast<T*>(p.out) + row * p.k + lane * 8;
+  const int64_t first = (int64_t(batch) * p.windows * p.rows_per_batch + r) * kEach + lane / kLanes;
+  const int64_t pitch = int64_t(p.rows_per_batch) * kEach;
+#pragma unroll 4
+  for (int64_t w = part; w < p.windows; w += step) {
+    if (w * kWindow + lane * 8 >= p.k) break;
+    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(codes + w * (kWindow / 2)));
+    const __nv_bfloat16 s = p.scale[first + w * pitch];
+    // a nibble or-ed into 128 is 128 + code (two's complement + 8 is its top bit flipped); 128 + zero off it
+    uint32_t off = 0x43084308u;
+    if constexpr (kZero) off = 0x43004300u + p.zero[first + w * pitch] * 0x00010001u;
+    uint32_t n[4];  // codes 0 and 4, 1 and 5, 2 and 6, 3 and 7
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = T(s * float(int(((code >> (4 * i)) & 15u) ^ flip) - zero));
-  T* out = static_cast<T*>(p.out) + row * p.k + c;
-  if (wide) {
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t raw = (code >> (4 * i) & 0x000F000Fu) ^ (kZero ? 0x43004300u : 0x43084308u);
+      const __nv_bfloat162 v = __hsub2(reinterpret_cast<const __nv_bfloat162&>(raw), reinterpret_cast<const __nv_bfloat162&>(off));
+      n[i] = reinterpret_cast<const uint32_t&>(v);
+    }
+    T* to = out + w * kWindow;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(v)[i];
-  } else {
+      for (int i = 0; i < 4; ++i) {  // products of 4 and 8 bits, rounded once
+        const uint32_t pair = __byte_perm(n[i % 2 * 2], n[i % 2 * 2 + 1], i < 2 ? 0x5410 : 0x7632);
+        const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162&>(pair), __nv_bfloat162(s, s));
+        v[i] = reinterpret_cast<const uint32_t&>(y);
+      }
+      if (p.wide) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = v[i];
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint16_t*>(to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+      }
+    } else {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __bfloat162float(s) * __uint_as_float(n[i] << 16);
+        v[i + 4] = __bfloat162float(s) * __uint_as_float(n[i] & 0xFFFF0000u);
+      }
+      if (p.wide) {
+        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[i] = v[i];
+      }
+    }
   }
 }
 
 bool misaligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
-template <class F>
-cudaError_t by_group(int group, F&& go) {
-  switch (group) {
-    case 32: return go(std::integral_constant<int, 4>{});
-    case 64: return go(std::integral_constant<int, 8>{});
-    default: return go(std::integral_constant<int, 16>{});
-  }
-}
-
 int check(int dtype, int32_t batch, int64_t rows, int64_t k, int64_t ld, int32_t group) {
   if (dtype != GMM_DTYPE_BF16 && dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
   if (batch < 0 || rows < 0 || k < 1 || k > kMaxSize || rows > kMaxSize || ld < k ||
-      (group != 32 && group != 64 && group != 128) || k % group != 0)
+      (group != 32 && group != 64 && group != 128) || k % group != 0 || int64_t(batch) * rows > kMaxSize)
     return GMM_ERR_SHAPE;
-  const int64_t all = int64_t(batch) * rows;
-  if (all > kMaxSize * 8 || (all > 0 && (k + kWindow - 1) / kWindow > kMaxSize * 8 / all)) return GMM_ERR_SHAPE;
   return GMM_OK;
 }
 
-unsigned blocks_of(int64_t warps) { return unsigned((warps * 32 + kThreads - 1) / kThreads); }
+// Warps to a row: as few as keep some 4000 on the GPU, at most one for each `each` values.
+int parts_of(int64_t rows, int64_t k, int64_t each) {
+  int lg = 0;
+  while (lg < 20 && (rows << lg) < 4096 && (each << lg) < k) ++lg;
+  return lg;
+}
+unsigned blocks_of(int64_t rows, int lg) { return unsigned(((rows << lg) * 32 + kThreads - 1) / kThreads); }
 
 }  // namespace
 }  // namespace gmmk
@@ -207,19 +307,22 @@ extern "C" int gmm_quantize_int4(const void* x, int x_dtype, int32_t batch, int6
     return GMM_ERR_ALIGN;
   if (int st = require_device(nullptr)) return st;
   if (rows == 0) return GMM_OK;
-  const QuantParams p{x, rows, rows_per_batch, x_ld, k, (k + kWindow - 1) / kWindow, static_cast<uint8_t*>(codes),
+  const int lg = parts_of(rows, k, 512);
+  const QuantParams p{x, rows, x_ld, int32_t(rows_per_batch), lg, int32_t(k), int32_t((k + kWindow - 1) / kWindow),
+                      !misaligned(x, 16) && x_ld * size % 16 == 0, static_cast<uint8_t*>(codes),
                       static_cast<__nv_bfloat16*>(scale), static_cast<uint8_t*>(zero)};
-  const bool wide = !misaligned(x, 16) && x_ld * size % 16 == 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = blocks_of(rows * p.windows);
-  const cudaError_t e = by_group(group, [&](auto lanes) {
+  auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     auto kern = x_dtype == GMM_DTYPE_F32
                     ? (zero != nullptr ? quantize_int4_kernel<float, L, true> : quantize_int4_kernel<float, L, false>)
                     : (zero != nullptr ? quantize_int4_kernel<__nv_bfloat16, L, true>
                                        : quantize_int4_kernel<__nv_bfloat16, L, false>);
-    return launch_dependent(kern, grid, kThreads, 0, s, 1, p, wide);
-  });
+    return launch_dependent(kern, blocks_of(rows, lg), kThreads, 0, s, 1, p);
+  };
+  const cudaError_t e = group == 32   ? go(std::integral_constant<int, 2>{})
+                        : group == 64 ? go(std::integral_constant<int, 4>{})
+                                      : go(std::integral_constant<int, 8>{});
   return e == cudaSuccess ? GMM_OK : record_cuda_error(e);
 }
 
@@ -233,15 +336,21 @@ extern "C" int gmm_dequantize_int4(const void* codes, const void* scale, const v
   if (misaligned(codes, 4) || misaligned(scale, 2) || misaligned(out, size)) return GMM_ERR_ALIGN;
   if (int st = require_device(nullptr)) return st;
   if (rows == 0) return GMM_OK;
+  const int lg = parts_of(rows, k, kWindow);
   const DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const __nv_bfloat16*>(scale),
-                        static_cast<const uint8_t*>(zero), rows, rows_per_batch, k, (k + kWindow - 1) / kWindow, out};
-  const bool wide = !misaligned(out, 16);
+                        static_cast<const uint8_t*>(zero), rows, int32_t(rows_per_batch), lg, int32_t(k),
+                        int32_t((k + kWindow - 1) / kWindow), !misaligned(out, 16), out};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = blocks_of(rows * p.windows);
-  const cudaError_t e = by_group(group, [&](auto lanes) {
+  auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    auto kern = out_dtype == GMM_DTYPE_F32 ? dequantize_int4_kernel<float, L> : dequantize_int4_kernel<__nv_bfloat16, L>;
-    return launch_dependent(kern, grid, kThreads, 0, s, 1, p, wide);
-  });
+    auto kern = out_dtype == GMM_DTYPE_F32
+                    ? (zero != nullptr ? dequantize_int4_kernel<float, L, true> : dequantize_int4_kernel<float, L, false>)
+                    : (zero != nullptr ? dequantize_int4_kernel<__nv_bfloat16, L, true>
+                                       : dequantize_int4_kernel<__nv_bfloat16, L, false>);
+    return launch_dependent(kern, blocks_of(rows, lg), kThreads, 0, s, 1, p);
+  };
+  const cudaError_t e = group == 32   ? go(std::integral_constant<int, 4>{})
+                        : group == 64 ? go(std::integral_constant<int, 8>{})
+                                      : go(std::integral_constant<int, 16>{});
   return e == cudaSuccess ? GMM_OK : record_cuda_error(e);
 }

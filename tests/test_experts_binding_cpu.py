@@ -75,7 +75,7 @@ REFUSALS = [
     ("gmm_quantize_int4", QUANT, DTYPE, [dict(dtype=2)]),
     ("gmm_quantize_int4", QUANT, SHAPE, [dict(group=16), dict(group=256), dict(k=0), dict(k=96), dict(ld=255),
                                          dict(rows=-1), dict(batch=-1), dict(batch=64, rows=LARGEST),
-                                         dict(rows=LARGEST, k=2 ** 30, ld=2 ** 30)]),
+                                         dict(rows=LARGEST + 1), dict(k=LARGEST + 32, ld=LARGEST + 32)]),
     ("gmm_quantize_int4", QUANT, ALIGN, [dict(codes=ODD8), dict(scale=ODD8), dict(zero=ODD), dict(dtype=1, x=ODD)]),
     ("gmm_dequantize_int4", DEQUANT, NULL, [dict(codes=None), dict(scale=None), dict(out=None)]),
     ("gmm_dequantize_int4", DEQUANT, DTYPE, [dict(dtype=2)]),
@@ -119,8 +119,8 @@ def test_scratch_bytes(lib):
 
 def test_matvec_scratch_bytes(lib):
     assert lib.gmm_matvec_scratch_bytes(1, 4096, 128, 0, 8, 0) == 0
-    many = lib.gmm_matvec_scratch_bytes(64, 4096, 128, 0, 8, 0)
-    assert many == 64 * (4096 * 2 + 32 * 4 + 4) and lib.gmm_matvec_scratch_bytes(6400, 4096, 128, 0, 8, 0) == many
+    many = lib.gmm_matvec_scratch_bytes(64, 4096, 128, 0, 4, 0)
+    assert many == 64 * (4096 * 2 + 32 * 4 + 4) and lib.gmm_matvec_scratch_bytes(6400, 4096, 128, 0, 4, 0) == many
     for bad in [(0, 4096, 128, 0, 8, 0), (-1, 4096, 128, 0, 8, 0), (64, 0, 128, 0, 8, 0), (64, 4096, 16, 0, 8, 0),
                 (64, 4096, 128, 0, 0, 0), (64, 4096, 128, 0, 33, 0)]:
         assert lib.gmm_matvec_scratch_bytes(*bad) == 0
