@@ -130,14 +130,21 @@ __global__ void __launch_bounds__(kThreads) quantize_int4_kernel(QuantParams p) 
   uint8_t* codes = p.codes + row * (p.k / 2);
   const int64_t at_batch = int64_t(batch) * p.windows;
   const int64_t whole = int64_t(p.windows) * kWindow;
-#pragma unroll 2
-  for (int64_t c = part * 512 + lane * 16; c - lane * 16 < whole; c += step) {
-    const bool in = c < p.k;  // k is whole groups, so all of a group's lanes are
+  // k is whole groups, so all of a group's lanes are within it or none
+  auto read = [&](int64_t c) {
     Values<T> v;
-    if (in)
+    if (c < p.k)
       v.load(x + c, p.wide != 0);
     else
       v.zeros();
+    return v;
+  };
+  Values<T> next = read(part * 512 + lane * 16);
+#pragma unroll 1
+  for (int64_t c = part * 512 + lane * 16; c - lane * 16 < whole; c += step) {
+    const bool in = c < p.k;
+    const Values<T> v = next;
+    next = read(c + step);  // on its way while these are encoded
     float span, lo = 0.f;
     bool fine = true;
     if constexpr (kZero) {
@@ -227,49 +234,65 @@ __global__ void __launch_bounds__(kThreads) dequantize_int4_kernel(DequantParams
   T* out = static_cast<T*>(p.out) + row * p.k + lane * 8;
   const int64_t first = (int64_t(batch) * p.windows * p.rows_per_batch + r) * kEach + lane / kLanes;
   const int64_t pitch = int64_t(p.rows_per_batch) * kEach;
-#pragma unroll 4
-  for (int64_t w = part; w < p.windows; w += step) {
-    if (w * kWindow + lane * 8 >= p.k) break;
-    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(codes + w * (kWindow / 2)));
-    const __nv_bfloat16 s = p.scale[first + w * pitch];
-    // a nibble or-ed into 128 is 128 + code (two's complement + 8 is its top bit flipped); 128 + zero off it
-    uint32_t off = 0x43084308u;
-    if constexpr (kZero) off = 0x43004300u + p.zero[first + w * pitch] * 0x00010001u;
-    uint32_t n[4];  // codes 0 and 4, 1 and 5, 2 and 6, 3 and 7
+  // four windows on their way
+  constexpr int kAhead = 4;
+  for (int64_t w0 = part; w0 < p.windows; w0 += kAhead * step) {
+    uint32_t words[kAhead], zeros[kAhead];
+    __nv_bfloat16 scales[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t raw = (code >> (4 * i) & 0x000F000Fu) ^ (kZero ? 0x43004300u : 0x43084308u);
-      const __nv_bfloat162 v = __hsub2(reinterpret_cast<const __nv_bfloat162&>(raw), reinterpret_cast<const __nv_bfloat162&>(off));
-      n[i] = reinterpret_cast<const uint32_t&>(v);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t w = w0 + i * step;
+      if (w * kWindow + lane * 8 < p.k) {
+        words[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + w * (kWindow / 2)));
+        scales[i] = __ldg(p.scale + first + w * pitch);
+        if constexpr (kZero) zeros[i] = __ldg(p.zero + first + w * pitch);
+      }
     }
-    T* to = out + w * kWindow;
-    if constexpr (sizeof(T) == 2) {
-      uint32_t v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // products of 4 and 8 bits, rounded once
-        const uint32_t pair = __byte_perm(n[i % 2 * 2], n[i % 2 * 2 + 1], i < 2 ? 0x5410 : 0x7632);
-        const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162&>(pair), __nv_bfloat162(s, s));
-        v[i] = reinterpret_cast<const uint32_t&>(y);
-      }
-      if (p.wide) {
-        *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) reinterpret_cast<uint16_t*>(to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
-      }
-    } else {
-      float v[8];
+    for (int a = 0; a < kAhead; ++a) {
+      const int64_t w = w0 + a * step;
+      if (w * kWindow + lane * 8 >= p.k) break;
+      const uint32_t code = words[a];
+      const __nv_bfloat16 s = scales[a];
+      // a nibble or-ed into 128 is 128 + code (two's complement + 8 is its top bit flipped); 128 + zero off it
+      uint32_t off = 0x43084308u;
+      if constexpr (kZero) off = 0x43004300u + zeros[a] * 0x00010001u;
+      uint32_t n[4];  // codes 0 and 4, 1 and 5, 2 and 6, 3 and 7
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = __bfloat162float(s) * __uint_as_float(n[i] << 16);
-        v[i + 4] = __bfloat162float(s) * __uint_as_float(n[i] & 0xFFFF0000u);
+        const uint32_t raw = (code >> (4 * i) & 0x000F000Fu) ^ (kZero ? 0x43004300u : 0x43084308u);
+        const __nv_bfloat162 v = __hsub2(reinterpret_cast<const __nv_bfloat162&>(raw), reinterpret_cast<const __nv_bfloat162&>(off));
+        n[i] = reinterpret_cast<const uint32_t&>(v);
       }
-      if (p.wide) {
-        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
+      T* to = out + w * kWindow;
+      if constexpr (sizeof(T) == 2) {
+        uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = v[i];
+        for (int i = 0; i < 4; ++i) {  // products of 4 and 8 bits, rounded once
+          const uint32_t pair = __byte_perm(n[i % 2 * 2], n[i % 2 * 2 + 1], i < 2 ? 0x5410 : 0x7632);
+          const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162&>(pair), __nv_bfloat162(s, s));
+          v[i] = reinterpret_cast<const uint32_t&>(y);
+        }
+        if (p.wide) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) reinterpret_cast<uint16_t*>(to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+        }
+      } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = __bfloat162float(s) * __uint_as_float(n[i] << 16);
+          v[i + 4] = __bfloat162float(s) * __uint_as_float(n[i] & 0xFFFF0000u);
+        }
+        if (p.wide) {
+          reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) to[i] = v[i];
+        }
       }
     }
   }
