@@ -64,7 +64,6 @@ struct Params {
   int32_t act;            // of gated tiles
   void* out;
   int32_t out_n, out_f32;  // columns of out, its type
-  int32_t team_log2;      // of the warps to a tile
   int32_t x_rows, x_pitch;  // rows of x made ready, and elements between them
   // where not in shared memory: the rows, their groups' sums, and what takes their results to their size
   __nv_bfloat16* ready;
@@ -113,7 +112,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 constexpr int kTop = 116;                  // rows' largest values are brought to 2^116
 
-// Rows of x are made ready by windows, a warp each.  First the largest finite magnitude of each.
+// Rows of x are made ready by windows, a warp each.  First the largest finite magnitude of a lane's values.
 __device__ __forceinline__ uint32_t largest(const __nv_bfloat16* x, int k, int window) {
   const int c = window * kWindow + (threadIdx.x & 31) * 8;
   uint32_t m = 0;
@@ -127,13 +126,11 @@ __device__ __forceinline__ uint32_t largest(const __nv_bfloat16* x, int k, int w
       if (hi < 0x7F80u) m = max(m, hi);
     }
   }
-  return __reduce_max_sync(0xffffffffu, m);
+  return m;
 }
-// The power of two that a row's largest value, of these windows, has or, if that is even, the next.
-__device__ __forceinline__ int power_of(const uint32_t* tops, int windows) {
-  uint32_t top = 0;
-  for (int i = threadIdx.x & 31; i < windows; i += 32) top = max(top, tops[i]);
-  top = __reduce_max_sync(0xffffffffu, top);
+// The power of two that a row's largest value, of these n, has or, if that is even, the next.
+__device__ __forceinline__ int power_of(const uint32_t* tops, int n) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, tops[min(int(threadIdx.x & 31), n - 1)]);
   return (top == 0 ? 0 : top < 0x80u ? 31 - __clz(int(top)) - 133 : int(top >> 7) - 127) | 1;
 }
 // The root of what takes a result to its own size: 2^(133 - kTop + power).
@@ -202,6 +199,9 @@ struct Unit {
   }
 };
 
+// Groups' sums of a row of x: rows of whole 16 bytes.
+__host__ __device__ constexpr int64_t sums_pitch(int64_t k, int group) { return (k / group + 3) / 4 * 4; }
+
 template <bool kShared, class T>
 __device__ __forceinline__ T load(const T* p) {
   if constexpr (kShared)
@@ -238,12 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   const int64_t x_step = p.x_slot != 0 ? p.x_slot : p.x_token;
   uint32_t* tops = reinterpret_cast<uint32_t*>(&part[0][0][0]);  // of the windows of x
   if constexpr (kStaged) {
-    for (int row = 0; row < p.x_rows; ++row)
+    for (int row = 0; row < p.x_rows; ++row) {
+      uint32_t top = 0;
 #pragma unroll 4
-      for (int w = warp; w < p.windows; w += kWarps) {
-        const uint32_t top = largest(p.x + row * x_step, p.k, w);
-        if (lane == 0) tops[row * p.windows + w] = top;
-      }
+      for (int w = warp; w < p.windows; w += kWarps) top = max(top, largest(p.x + row * x_step, p.k, w));
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0 && warp < p.windows) tops[row * min(p.windows, kWarps) + warp] = top;
+    }
   }
   __syncthreads();
   // this thread's slot: its expert, its item's head and its column there
@@ -317,12 +318,24 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   }
 
   // ---- the warp's part of its team's units, in order: pairs of an item and a span
-  const int lg = p.team_log2, size = 1 << lg;    // warps of a team
+  // warps to a tile: so many that the last team is done first, a unit's start and end counted as a span.
+  // Lanes 0 to 4 each look at one power of two.
+  const int groups = kSum ? chunks : items;
+  int lg = 0;
+  {
+    const int at = min(lane, 4);
+    const unsigned spans = unsigned(p.spans) * (kSum ? (unsigned(items) + chunks - 1) / chunks : 1u);
+    const unsigned units = unsigned(groups) * unsigned(min(p.tiles, 1 << 20)), teams = gridDim.x * unsigned(kWarps >> at);
+    const unsigned rounds = (units + teams - 1) / teams, each = (spans + (1u << at) - 1) >> at;
+    const unsigned total = unsigned(fminf(float(rounds) * float(each + 1), 2.5e8f));
+    const unsigned cost = __reduce_min_sync(0xffffffffu, total * 8 + at);
+    lg = int(cost % 8);
+  }
+  const int size = 1 << lg;    // warps of a team
   const int member = warp & (size - 1), team = warp >> lg;
   // teams of all CTAs; a CTA's are far apart, so that the last round is spread over all of them, or next
   // to one another, so that they read the same rows of x through the SM's cache
   const int teams = int(gridDim.x) * (kWarps >> lg);
-  const int groups = kSum ? chunks : items;
   const int start = kStaged ? int(blockIdx.x) + team * int(gridDim.x) : int(blockIdx.x) * (kWarps >> lg) + team;
   const int dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
   Unit ahead{start / p.tiles, 0};
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   fetch();
 
   // rows of x made ready: in shared memory, or by the kernel ahead
-  const int x_groups = p.k / kGroup;
+  const int x_groups = sums_pitch(p.k, kGroup);
   const __nv_bfloat16* ready = p.ready;
   const float* sums = p.sums;
   const float* roots = p.roots;
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     float* to_roots = to_sums + p.x_rows * x_groups;
     ready = to, sums = to_sums, roots = to_roots;
     for (int row = 0; row < p.x_rows; ++row) {
-      const int power = power_of(tops + row * p.windows, p.windows);
+      const int power = power_of(tops + row * min(p.windows, kWarps), min(p.windows, kWarps));
 #pragma unroll 4
       for (int w = warp; w < p.windows; w += kWarps)
         make_ready<kGroup, kZero>(p.x + row * x_step, p.k, w, power, to + row * p.x_pitch, to_sums + row * x_groups);
@@ -491,21 +504,33 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       const int k0 = w * kSpan;
       const __nv_bfloat16* xk = xp + k0;
       // x of the next four chunks is read ahead of its use: it may come from the L2
+      constexpr int kQuad = 128 / kGroup;  // groups of four chunks
+      using Sums = std::conditional_t<kQuad == 1, float, std::conditional_t<kQuad == 2, float2, float4>>;
       uint4 b[2][4];
-      auto read_x = [&](uint4 (&to)[4], int quad) {
+      Sums n0[2], n1[2];
+      const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
+      auto read_x = [&](int to, int quad) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (quad * 4 + i) * 32));
+        for (int i = 0; i < 4; ++i) b[to][i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (quad * 4 + i) * 32));
+        n0[to] = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
+        n1[to] = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
       };
       const bool full = k0 + kSpan <= p.k;
-      if (full) read_x(b[0], 0);
+      if (full) read_x(0, 0);
+      uint32_t touched[2] = {0, 0};
+      if constexpr (!kStaged) {  // the next span's lines of x on their way from the L2 to the L1
+        if (at + 1 < end && k0 + 2 * kSpan <= p.k) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) touched[i] = __ldg(reinterpret_cast<const uint32_t*>(xk + kSpan + (t4 + 4 * i) * 64 - t4 * 8));
+        }
+      }
       copies_wait<0>();
       __syncwarp();
       fetch();
       const uint8_t *codes = words + stage, *scales = codes + scale_off, *zeros = codes + zero_off;
       stage = R::kStage - stage;
-      const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
       // one group, its chunks' x given by `x_of`
-      auto group = [&](int q, float s0, float s1, auto x_of) {
+      auto group = [&](int q, float s0, float s1, float n0, float n1, auto x_of) {
         float c[4];
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
@@ -518,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
           mma(c, low(wa), low(wb), high(wa), high(wb), v.x, v.y, j == 0);
           mma(c, low(va), low(vb), high(va), high(vb), v.z, v.w, false);
         }
-        const float n0 = load<kStaged>(sums0k + q), n1 = load<kStaged>(sums1k + q);
         if constexpr (kZero) {
           const int zq = q / kEach * (16 * kEach) + q % kEach;
           const float z0 = float(zeros[zq]), z1 = float(zeros[8 * kEach + zq]);
@@ -531,11 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       };
       if (full) {
         using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
-        constexpr int kQuad = 128 / kGroup;  // groups of four chunks
         Scales sa, sb;
 #pragma unroll
         for (int quad = 0; quad < 4; ++quad) {
-          if (quad < 3) read_x(b[(quad + 1) % 2], quad + 1);
+          if (quad < 3) read_x((quad + 1) % 2, quad + 1);
           if (quad % 2 == 0)
             sa = reinterpret_cast<const Scales*>(scales)[8 * quad], sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
 #pragma unroll
@@ -543,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             const int at = quad % 2 * kQuad + i;  // in the window
             const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
-                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), [&](int chunk) { return b[quad % 2][chunk % 4]; });
+                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16),
+                  reinterpret_cast<const float*>(&n0[quad % 2])[i], reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) { return b[quad % 2][chunk % 4]; });
           }
         }
       } else {
@@ -552,10 +576,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 #pragma unroll 1
         for (int q = 0; q < left; ++q) {
           const int sq = q / kEach * (16 * kEach) + q % kEach;
-          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]),
+          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]), load<kStaged>(sums0k + q),
+                load<kStaged>(sums1k + q),
                 [&](int chunk) { return load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
         }
       }
+      if constexpr (!kStaged) asm volatile("" ::"r"(touched[0]), "r"(touched[1]));
       if (!kSum) {
         ++w;
       } else if (++w == p.spans || at + 1 == end) {
@@ -603,26 +629,29 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 
 // Rows of x made ready where a CTA's shared memory does not hold them: a CTA a row.
 template <int kGroup, bool kZero>
-__global__ void __launch_bounds__(256) make_ready_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
   griddep_begin();
   p.x = after_begin(p.x);
-  __shared__ uint32_t tops[8];
+  __shared__ uint32_t tops[kWarps];
   const int row = blockIdx.x, warp = threadIdx.x >> 5;
   const __nv_bfloat16* x = p.x + row * (p.x_slot != 0 ? p.x_slot : p.x_token);
   uint32_t top = 0;
-  for (int w = warp; w < p.windows; w += 8) top = max(top, largest(x, p.k, w));
+#pragma unroll 4
+  for (int w = warp; w < p.windows; w += kWarps) top = max(top, largest(x, p.k, w));
+  top = __reduce_max_sync(0xffffffffu, top);
   if ((threadIdx.x & 31) == 0) tops[warp] = top;
   __syncthreads();
-  const int power = power_of(tops, 8);
-  for (int w = warp; w < p.windows; w += 8)
-    make_ready<kGroup, kZero>(x, p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * (p.k / kGroup));
+  const int power = power_of(tops, kWarps);
+#pragma unroll 4
+  for (int w = warp; w < p.windows; w += kWarps)
+    make_ready<kGroup, kZero>(x, p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
   if (threadIdx.x == 0) p.roots[row] = root_of(power);
 }
 
 constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * kWarps * 16 * (kCols + 1);
 
 // Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the groups' sums, the roots.
-int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + k / group * 4 + 4); }
+int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + sums_pitch(k, group) * 4 + 4); }
 // In shared memory rows are half a line of banks apart.
 int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
 bool is_staged(int64_t rows, int64_t k, int group, bool zero) {
@@ -632,42 +661,30 @@ bool is_staged(int64_t rows, int64_t k, int group, bool zero) {
 int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
 
 template <int kGroup, bool kZero, bool kGated, bool kSum>
-cudaError_t launch(const Params& p, bool staged, int64_t units, int sms, cudaStream_t stream) {
+cudaError_t launch(const Params& p, bool staged, int sms, cudaStream_t stream) {
   using R = Ring<kGroup, kZero>;
   const size_t smem = size_t(kWarps) * R::kBytes + (staged ? size_t(ready_bytes(p.x_rows, p.x_pitch, p.k, kGroup)) : 0);
   auto kern = staged ? matvec_kernel<kGroup, kZero, kGated, kSum, true> : matvec_kernel<kGroup, kZero, kGated, kSum, false>;
   // for every launch: the attribute is the current device's, and one size for all calls
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
   if (!staged)
-    if (cudaError_t e = launch_dependent(make_ready_kernel<kGroup, kZero>, unsigned(p.x_rows), 256, 0, stream, 1, p)) return e;
-  const int64_t ctas = ((units << p.team_log2) + kWarps - 1) / kWarps;
-  return launch_dependent(kern, unsigned(ctas < sms ? ctas : sms), kThreads, smem, stream, 1, p);
+    if (cudaError_t e = launch_dependent(make_ready_kernel<kGroup, kZero>, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
+  return launch_dependent(kern, unsigned(sms), kThreads, smem, stream, 1, p);
 }
 
 template <int kGroup, bool kZero>
-cudaError_t by_form(const Params& p, bool staged, int64_t units, int sms, cudaStream_t stream) {
-  if (p.weights != nullptr) return launch<kGroup, kZero, false, true>(p, staged, units, sms, stream);
-  return p.act != GMM_ACT_NONE ? launch<kGroup, kZero, true, false>(p, staged, units, sms, stream)
-                               : launch<kGroup, kZero, false, false>(p, staged, units, sms, stream);
+cudaError_t by_form(const Params& p, bool staged, int sms, cudaStream_t stream) {
+  if (p.weights != nullptr) return launch<kGroup, kZero, false, true>(p, staged, sms, stream);
+  return p.act != GMM_ACT_NONE ? launch<kGroup, kZero, true, false>(p, staged, sms, stream)
+                               : launch<kGroup, kZero, false, false>(p, staged, sms, stream);
 }
 
-cudaError_t matvec(Params p, int group, bool staged, int sms, cudaStream_t stream) {
-  // units at most: a tile of each slot's expert, or of each 8 tokens with their experts one after another
-  const bool sums = p.weights != nullptr;
-  const int64_t units = int64_t(p.tiles) * (sums ? (p.tokens + kCols - 1) / kCols : p.tokens * p.topk);
-  const int64_t pairs = int64_t(p.spans) * (!sums ? 1 : (p.tokens < kCols ? p.tokens : kCols) * p.topk);
-  // warps to a tile: those with which the last team is done first, a unit's start and end counted as a window
-  int64_t best = INT64_MAX;
-  for (int lg = 0; (1 << lg) <= kWarps; ++lg) {
-    const int64_t teams = int64_t(sms) * (kWarps >> lg), rounds = (units + teams - 1) / teams;
-    const int64_t windows = rounds * (((pairs + (1 << lg) - 1) >> lg) + 1);
-    if (windows < best) best = windows, p.team_log2 = lg;
-  }
+cudaError_t matvec(const Params& p, int group, bool staged, int sms, cudaStream_t stream) {
   const bool zero = p.zero != nullptr;
   switch (group) {
-    case 32: return zero ? by_form<32, true>(p, staged, units, sms, stream) : by_form<32, false>(p, staged, units, sms, stream);
-    case 64: return zero ? by_form<64, true>(p, staged, units, sms, stream) : by_form<64, false>(p, staged, units, sms, stream);
-    default: return zero ? by_form<128, true>(p, staged, units, sms, stream) : by_form<128, false>(p, staged, units, sms, stream);
+    case 32: return zero ? by_form<32, true>(p, staged, sms, stream) : by_form<32, false>(p, staged, sms, stream);
+    case 64: return zero ? by_form<64, true>(p, staged, sms, stream) : by_form<64, false>(p, staged, sms, stream);
+    default: return zero ? by_form<128, true>(p, staged, sms, stream) : by_form<128, false>(p, staged, sms, stream);
   }
 }
 
@@ -733,7 +750,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     if (!staged) {
       p.ready = static_cast<__nv_bfloat16*>(scratch);
       p.sums = reinterpret_cast<float*>(p.ready + int64_t(p.x_rows) * k);
-      p.roots = reinterpret_cast<float*>(p.sums + int64_t(p.x_rows) * (k / group));
+      p.roots = p.sums + int64_t(p.x_rows) * sums_pitch(k, group);
     }
     const int64_t first = t0 * (weights != nullptr ? 1 : topk) * out_n;
     p.out = static_cast<char*>(out) + first * (out_dtype == GMM_DTYPE_F32 ? 4 : 2);
