@@ -112,25 +112,28 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 constexpr int kTop = 116;                  // rows' largest values are brought to 2^116
 
-// Rows of x are made ready by windows, a warp each.  First the largest finite magnitude of a lane's values.
-__device__ __forceinline__ uint32_t largest(const __nv_bfloat16* x, int k, int window) {
+// Rows of x are made ready by windows, a warp each, 8 values a lane (zeros past k).
+__device__ __forceinline__ uint4 window_of(const __nv_bfloat16* x, int k, int window) {
   const int c = window * kWindow + (threadIdx.x & 31) * 8;
+  return c < k ? __ldg(reinterpret_cast<const uint4*>(x + c)) : make_uint4(0, 0, 0, 0);
+}
+// The largest finite magnitude of a lane's values.
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t m = 0;
-  if (c < k) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-      if (lo < 0x7F80u) m = max(m, lo);
-      if (hi < 0x7F80u) m = max(m, hi);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+    if (lo < 0x7F80u) m = max(m, lo);
+    if (hi < 0x7F80u) m = max(m, hi);
   }
   return m;
 }
 // The power of two that a row's largest value, of these n, has or, if that is even, the next.
 __device__ __forceinline__ int power_of(const uint32_t* tops, int n) {
-  const uint32_t top = __reduce_max_sync(0xffffffffu, tops[min(int(threadIdx.x & 31), n - 1)]);
+  uint32_t top = 0;
+  for (int i = threadIdx.x & 31; i < n; i += 32) top = max(top, tops[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
   return (top == 0 ? 0 : top < 0x80u ? 31 - __clz(int(top)) - 133 : int(top >> 7) - 127) | 1;
 }
 // The root of what takes a result to its own size: 2^(133 - kTop + power).
@@ -138,14 +141,12 @@ __device__ __forceinline__ float root_of(int power) { return __int_as_float((127
 // A window of the row: x 2^(kTop - power) as bf16, in each 8 in the order of the masks, 0 4 1 5 2 6 3 7,
 // the odd ones over 16; and -8 (kZero: -1) times the groups' sums times 2^-133.
 template <int kGroup, bool kZero>
-__device__ __forceinline__ void make_ready(const __nv_bfloat16* x, int k, int window, int power, __nv_bfloat16* to,
-                                           float* sums) {
+__device__ __forceinline__ void make_ready(const uint4& v, int k, int window, int power, __nv_bfloat16* to, float* sums) {
   const int lane = threadIdx.x & 31, c = window * kWindow + lane * 8;
   const int up = kTop - power, first = up / 2;  // up to 249: in two steps, each exact
   const float u0 = __int_as_float((127 + first) << 23), u1 = __int_as_float((127 + up - first) << 23);
   float sum = 0.f;
   if (c < k) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float f[8];
 #pragma unroll
@@ -183,6 +184,7 @@ struct Table {
   int16_t slot[kMaxSlots][kCols];     // of each item's columns; -1: none
   int16_t head[kMaxSlots];            // of each item: its first slot
   int16_t row[kMaxSlots];             // of each slot: its row of x
+  int16_t power[kMaxSlots];           // of each row of x, where they are made ready here
   int32_t columns[kMaxSlots];         // of each item
   int16_t first[kMaxSlots / kCols + kMaxSlots + 1];  // with weights: first item of each 8 tokens
   int16_t number[kMaxSlots];          // of the item that a slot is the head of
@@ -224,6 +226,27 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slots = p.tokens * p.topk;
 
+  // ---- kStaged: x asked for first, into the place where it is made ready below
+  __nv_bfloat16* const staged = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
+  // this warp's windows, every 16th of the rows' windows in order: each(row, window, this lane's 8 values)
+  auto each_window = [&](auto each) {
+    int row = 0, w = warp;
+    while (w >= p.windows) w -= p.windows, ++row;
+#pragma unroll 1
+    while (row < p.x_rows) {
+      each(row, w, staged + row * p.x_pitch + w * kWindow + lane * 8);
+      for (w += kWarps; w >= p.windows; w -= p.windows) ++row;
+    }
+  };
+  if constexpr (kStaged) {
+    const int64_t step = p.x_slot != 0 ? p.x_slot : p.x_token;
+    each_window([&](int row, int w, __nv_bfloat16* to) {
+      const int c = w * kWindow + lane * 8;
+      if (c < p.k) copy16(smem_u32(to), p.x + row * step + c);
+    });
+    copies_commit();
+  }
+
   // ---- items: slots of the same expert in their order, 8 at a time (kSum: those of 8 tokens; a
   // token's second slot of the same expert has an item of its own).  A head is an item's first slot.
   static_assert(kMaxSlots <= kThreads, "a slot a thread");
@@ -235,18 +258,21 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     table.columns[i] = 0;
   }
   for (int i = tid; i < kMaxSlots * kCols / 2; i += kThreads) reinterpret_cast<uint32_t*>(table.slot)[i] = 0xFFFFFFFFu;
-  const int64_t x_step = p.x_slot != 0 ? p.x_slot : p.x_token;
   uint32_t* tops = reinterpret_cast<uint32_t*>(&part[0][0][0]);  // of the windows of x
   if constexpr (kStaged) {
-    for (int row = 0; row < p.x_rows; ++row) {
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int w = warp; w < p.windows; w += kWarps) top = max(top, largest(p.x + row * x_step, p.k, w));
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0 && warp < p.windows) tops[row * min(p.windows, kWarps) + warp] = top;
-    }
+    copies_wait<0>();
+    each_window([&](int row, int w, __nv_bfloat16* at) {
+      const uint4 v = w * kWindow + lane * 8 < p.k ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, largest(v));
+      if (lane == 0) tops[row * p.windows + w] = top;
+    });
   }
   __syncthreads();
+  if constexpr (kStaged)
+    for (int row = warp; row < p.x_rows; row += kWarps) {
+      const int power = power_of(tops + row * p.windows, p.windows);
+      if (lane == 0) table.power[row] = int16_t(power);
+    }
   // this thread's slot: its expert, its item's head and its column there
   int mine = -1, head = -1, column = 0;
   if (tid < slots) mine = table.expert[tid];
@@ -449,17 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   const float* sums = p.sums;
   const float* roots = p.roots;
   if constexpr (kStaged) {
-    auto* to = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
-    auto* to_sums = reinterpret_cast<float*>(to + p.x_rows * p.x_pitch);
+    auto* to_sums = reinterpret_cast<float*>(staged + p.x_rows * p.x_pitch);
     float* to_roots = to_sums + p.x_rows * x_groups;
-    ready = to, sums = to_sums, roots = to_roots;
-    for (int row = 0; row < p.x_rows; ++row) {
-      const int power = power_of(tops + row * min(p.windows, kWarps), min(p.windows, kWarps));
-#pragma unroll 4
-      for (int w = warp; w < p.windows; w += kWarps)
-        make_ready<kGroup, kZero>(p.x + row * x_step, p.k, w, power, to + row * p.x_pitch, to_sums + row * x_groups);
-      if (tid == 0) to_roots[row] = root_of(power);
-    }
+    ready = staged, sums = to_sums, roots = to_roots;
+    each_window([&](int row, int w, __nv_bfloat16* at) {
+      const uint4 v = w * kWindow + lane * 8 < p.k ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+      make_ready<kGroup, kZero>(v, p.k, w, table.power[row], staged + row * p.x_pitch, to_sums + row * x_groups);
+    });
+    if (tid < p.x_rows) to_roots[tid] = root_of(table.power[tid]);
     __syncthreads();
   }
 
@@ -637,14 +660,14 @@ __global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
   const __nv_bfloat16* x = p.x + row * (p.x_slot != 0 ? p.x_slot : p.x_token);
   uint32_t top = 0;
 #pragma unroll 4
-  for (int w = warp; w < p.windows; w += kWarps) top = max(top, largest(x, p.k, w));
+  for (int w = warp; w < p.windows; w += kWarps) top = max(top, largest(window_of(x, p.k, w)));
   top = __reduce_max_sync(0xffffffffu, top);
   if ((threadIdx.x & 31) == 0) tops[warp] = top;
   __syncthreads();
   const int power = power_of(tops, kWarps);
 #pragma unroll 4
   for (int w = warp; w < p.windows; w += kWarps)
-    make_ready<kGroup, kZero>(x, p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
+    make_ready<kGroup, kZero>(window_of(x, p.k, w), p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
   if (threadIdx.x == 0) p.roots[row] = root_of(power);
 }
 
