@@ -19,8 +19,8 @@ extern "C" {
 
 /* ------------------------------------------------------------------ balance of the router */
 
-/* Bytes of scratch that gmm_balance_loss() needs (no content is expected, none is kept); 0 for
- * sizes that it refuses. */
+/* Bytes of scratch that gmm_balance_loss() needs (0 for few tokens, and for sizes that it refuses);
+ * no content is expected, none is kept. */
 size_t gmm_balance_scratch_bytes(int64_t tokens, int32_t num_experts, int64_t sequences);
 
 /*
@@ -41,7 +41,8 @@ size_t gmm_balance_scratch_bytes(int64_t tokens, int32_t num_experts, int64_t se
  *            rows of tokens that a mask takes out are not read into any result
  *   experts  int32 [tokens, topk], as gmm_route() chose them; topk <= GMM_MAX_TOPK
  *   losses   f32 [2];  counts  int32 [sequences, num_experts];  counted  int32 [1]: N
- *   scratch  16-byte aligned; calls that may run at the same time need one each
+ *   scratch  gmm_balance_scratch_bytes() bytes, 16-byte aligned (NULL for none); calls that may run at
+ *            the same time need one each
  * sequences >= 1 divides tokens; tokens * topk at most 2^31 - 1024.
  */
 int gmm_balance_loss(const void* logits, int logits_dtype, int64_t tokens, int32_t num_experts, int64_t logits_ld,

@@ -594,6 +594,7 @@ extern "C" size_t gmm_balance_scratch_bytes(int64_t tokens, int32_t num_experts,
   using namespace gmmk;
   if (!sizes_ok(tokens, num_experts, sequences)) return 0;
   const int64_t clusters = sequences * cut_of(tokens, sequences).clusters;
+  if (clusters == 1) return 0;
   return size_t(clusters) * (size_t(num_experts) * 8 + 8) + 16;
 }
 
@@ -605,12 +606,13 @@ extern "C" int gmm_balance_loss(const void* logits, int logits_dtype, int64_t to
   if (int st = check(logits, logits_dtype, tokens, num_experts, logits_ld, score, sequences)) return st;
   if (topk < 1 || topk > GMM_MAX_TOPK || tokens * topk > kMaxSize) return GMM_ERR_SHAPE;
   if ((tokens > 0 && (logits == nullptr || experts == nullptr)) || losses == nullptr || counts == nullptr ||
-      counted == nullptr || scratch == nullptr)
+      counted == nullptr)
     return GMM_ERR_NULL;
   if (misaligned(experts, 4) || misaligned(losses, 4) || misaligned(counts, 4) || misaligned(counted, 4) ||
       misaligned(scratch, 16))
     return GMM_ERR_ALIGN;
-  if (scratch_bytes < gmm_balance_scratch_bytes(tokens, num_experts, sequences)) return GMM_ERR_WORKSPACE;
+  const size_t needed = gmm_balance_scratch_bytes(tokens, num_experts, sequences);
+  if (scratch_bytes < needed || (needed > 0 && scratch == nullptr)) return GMM_ERR_WORKSPACE;
   if (int st = require_device(nullptr)) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Cut cut = cut_of(tokens, sequences);

@@ -59,46 +59,50 @@ struct Params {
   int32_t units;     // of half a row
 };
 
-// Blocks of x columns and 256 / x rows; each thread takes kPer units of a row.
+// Blocks of x units by 256 / x rows or fewer; a thread takes kPer units of its row at a time.
 template <class U, class T, int kAct, int kPer, bool kBack>
 __global__ void __launch_bounds__(kThreads) gated_kernel(Params p) {
   griddep_begin();
   p.h = after_begin(p.h), p.dout = after_begin(p.dout);
+  constexpr bool kFast = sizeof(T) == 2;
   const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;
-  const int c0 = blockIdx.y * (blockDim.x * kPer) + threadIdx.x;
   const U* g = reinterpret_cast<const U*>(p.h + row * p.ld);
   const U* u = reinterpret_cast<const U*>(p.h + row * p.ld + p.f);
   const U* d = reinterpret_cast<const U*>(p.dout + row * p.f);
-  U gs[kPer], us[kPer], ds[kPer];
+  U* out = reinterpret_cast<U*>(p.out + row * p.f * (kBack ? 2 : 1));
+  U* out_u = reinterpret_cast<U*>(p.out + row * p.f * 2 + p.f);
+  const int step = blockDim.x;
+  for (int c0 = threadIdx.x; c0 < p.units; c0 += step * kPer) {
+    U gs[kPer], us[kPer], ds[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = c0 + i * int(blockDim.x);
-    if (c < p.units) {
-      gs[i] = __ldg(g + c), us[i] = __ldg(u + c);
-      if constexpr (kBack) ds[i] = __ldg(d + c);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = c0 + i * int(blockDim.x);
-    if (c >= p.units) break;
-    Values<U, T> gv(gs[i]), uv(us[i]);
-    if constexpr (kBack) {
-      Values<U, T> dv(ds[i]);
-#pragma unroll
-      for (int j = 0; j < Values<U, T>::kN; ++j) {
-        float slope;
-        const float a = act_value<kAct>(gv.v[j], slope);
-        gv.v[j] = dv.v[j] * uv.v[j] * slope;
-        uv.v[j] = dv.v[j] * a;
+    for (int i = 0; i < kPer; ++i) {
+      const int c = c0 + i * step;
+      if (c < p.units) {
+        gs[i] = __ldg(g + c), us[i] = __ldg(u + c);
+        if constexpr (kBack) ds[i] = __ldg(d + c);
       }
-      reinterpret_cast<U*>(p.out + row * 2 * p.f)[c] = gv.pack();
-      reinterpret_cast<U*>(p.out + row * 2 * p.f + p.f)[c] = uv.pack();
-    } else {
+    }
 #pragma unroll
-      for (int j = 0; j < Values<U, T>::kN; ++j) gv.v[j] = act_value<kAct>(gv.v[j]) * uv.v[j];
-      reinterpret_cast<U*>(p.out + row * p.f)[c] = gv.pack();
+    for (int i = 0; i < kPer; ++i) {
+      const int c = c0 + i * step;
+      if (c >= p.units) break;
+      Values<U, T> gv(gs[i]), uv(us[i]);
+      if constexpr (kBack) {
+        Values<U, T> dv(ds[i]);
+#pragma unroll
+        for (int j = 0; j < Values<U, T>::kN; ++j) {
+          float slope;
+          const float a = act_value<kAct, kFast>(gv.v[j], slope);
+          gv.v[j] = dv.v[j] * uv.v[j] * slope;
+          uv.v[j] = dv.v[j] * a;
+        }
+        out[c] = gv.pack(), out_u[c] = uv.pack();
+      } else {
+#pragma unroll
+        for (int j = 0; j < Values<U, T>::kN; ++j) gv.v[j] = act_value<kAct, kFast>(gv.v[j]) * uv.v[j];
+        out[c] = gv.pack();
+      }
     }
   }
 }
@@ -106,14 +110,19 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(Params p) {
 template <int kBytes, class T, bool kBack>
 cudaError_t launch(Params p, int act, cudaStream_t stream) {
   using U = typename UnitOf<kBytes>::type;
-  constexpr int kPer = 2;
+  constexpr int kPer = kBytes == 16 ? 2 : 4;
   p.units = int32_t(p.f / kBytes);
-  int x = 1;
-  while (x < kThreads && x * kPer < p.units) x *= 2;
+  // whole warps of a row that its units divide among evenly, over as many turns as 256 threads need
+  const int turns = (p.units + kThreads * kPer - 1) / (kThreads * kPer);
+  int x = ((p.units + turns * kPer - 1) / (turns * kPer) + 31) / 32 * 32;
+  if (p.units <= 16 * kPer) {  // short rows: parts of a warp
+    x = 1;
+    while (x * kPer < p.units) x *= 2;
+  }
+  const int y = kThreads / x;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(unsigned(x), unsigned(kThreads / x));
-  const int64_t rows = (p.rows + kThreads / x - 1) / (kThreads / x), columns = (p.units + int64_t(x) * kPer - 1) / (x * kPer);
-  cfg.gridDim = dim3(unsigned(rows), unsigned(columns));
+  cfg.blockDim = dim3(unsigned(x), unsigned(y));
+  cfg.gridDim = dim3(unsigned((p.rows + y - 1) / y));
   cfg.stream = stream;
   cudaLaunchAttribute at[1]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -127,8 +136,7 @@ template <bool kBack>
 int gated(const void* dout, const void* h, int dtype, int64_t rows, int64_t f, int64_t h_ld, int act, void* out,
           void* stream) {
   if (dtype != GMM_DTYPE_BF16 && dtype != GMM_DTYPE_F32) return GMM_ERR_DTYPE;
-  // columns run in the grid's second dimension: at most 65535 blocks of 512 units
-  if (rows < 0 || rows > kMaxSize || f < 1 || f > (int64_t(1) << 24) || h_ld < 2 * f ||
+  if (rows < 0 || rows > kMaxSize || f < 1 || f > kMaxSize / 8 || h_ld < 2 * f ||
       (act != GMM_ACT_SILU && act != GMM_ACT_GELU))
     return GMM_ERR_SHAPE;
   if (rows > 0 && (h == nullptr || out == nullptr || (kBack && dout == nullptr))) return GMM_ERR_NULL;

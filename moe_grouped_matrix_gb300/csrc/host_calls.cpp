@@ -372,11 +372,12 @@ PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return no_answer();
     const size_t bytes = g_calls.balance_scratch(tokens, int32_t(experts), sequences);
     Tensor losses = empty({2}, kF32, *logits), counts = empty({sequences, experts}, kI32, *logits),
-           counted = empty({1}, kI32, *logits), scratch = empty({int64_t(bytes)}, kU8, *logits);
+           counted = empty({1}, kI32, *logits), scratch;
+    if (bytes > 0) scratch = empty({int64_t(bytes)}, kU8, *logits);
     const int st = g_calls.balance(logits->data_ptr(), code_of(*logits), tokens, int32_t(experts), ld,
                                    ptr<int32_t>(*chosen), int32_t(topk), int(score), ptr_or_null<uint8_t>(mask),
                                    sequences, ptr<float>(losses), ptr<int32_t>(counts), ptr<int32_t>(counted),
-                                   scratch.data_ptr(), bytes, stream_of(*logits));
+                                   bytes > 0 ? scratch.data_ptr() : nullptr, bytes, stream_of(*logits));
     return answer(st, {losses, counts, counted});
   });
 }
@@ -440,20 +441,28 @@ PyObject* gated_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 bool int4_group(int64_t group) { return group == 32 || group == 64 || group == 128; }
 
-// quantize_int4(x, group, zero points) -> (codes, scale, zero or None); 2-D x
+// quantize_int4(x, group, zero points) -> (codes, scale, zero or None); x of two dimensions, or three dense ones
 PyObject* quantize_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 3) return no_answer();
     const Tensor* x = tensor(a[0]);
-    const int64_t ld = pitch(x);
+    const bool batched = x != nullptr && x->dim() == 3;
+    if (batched && (!x->is_cuda() || !is_float(*x) || !x->is_contiguous())) return no_answer();
+    int64_t ld = batched ? x->size(2) : pitch(x);
     bool ok = ld >= 0;
     const int64_t group = integer(a[1], 32, 128, &ok), zeros = integer(a[2], 0, 1, &ok);
-    if (!ok || !int4_group(group) || x->size(1) < 1 || x->size(1) % group != 0 || !here({x})) return no_answer();
-    const int64_t rows = x->size(0), k = x->size(1), windows = (k + 255) / 256, each = 256 / group;
-    Tensor codes = empty({rows, k / 2}, kU8, *x), scale = empty({windows, rows, each}, kBF16, *x), zero;
-    if (zeros) zero = empty({windows, rows, each}, kU8, *x);
-    const int st = g_calls.quantize_int4(x->data_ptr(), code_of(*x), 1, rows, k, ld, int32_t(group), codes.data_ptr(),
-                                         scale.data_ptr(), zeros ? zero.data_ptr() : nullptr, stream_of(*x));
+    if (!ok || !int4_group(group) || !here({x})) return no_answer();
+    const int64_t batch = batched ? x->size(0) : 1, rows = x->size(batched), k = x->size(1 + batched);
+    if (k < 1 || k % group != 0 || batch > INT32_MAX) return no_answer();
+    const int64_t windows = (k + 255) / 256, each = 256 / group;
+    auto make = [&](std::initializer_list<int64_t> shape, at::ScalarType type) {
+      return empty(at::IntArrayRef(shape.begin() + !batched, shape.end()), type, *x);
+    };
+    Tensor codes = make({batch, rows, k / 2}, kU8), scale = make({batch, windows, rows, each}, kBF16), zero;
+    if (zeros) zero = make({batch, windows, rows, each}, kU8);
+    const int st = g_calls.quantize_int4(x->data_ptr(), code_of(*x), int32_t(batch), rows, k, ld, int32_t(group),
+                                         codes.data_ptr(), scale.data_ptr(), zeros ? zero.data_ptr() : nullptr,
+                                         stream_of(*x));
     return answer(st, {codes, scale, zero});
   });
 }
@@ -472,19 +481,22 @@ bool int4_of(const Tensor* codes, const Tensor* scale, const Tensor* zero, bool 
                          (!has_zero || dense(zero, kU8, {w, *rows, each}));
 }
 
-// dequantize_int4(codes, scale, zero, group, out is f32) -> values; 2-D
+// dequantize_int4(codes, scale, zero, group, out is f32) -> values; of two or three dimensions
 PyObject* dequantize_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 5) return no_answer();
     const Tensor *codes = tensor(a[0]), *scale = tensor(a[1]), *zero = tensor(a[2]);
     bool ok = true;
     const int64_t group = integer(a[3], 32, 128, &ok), f32 = integer(a[4], 0, 1, &ok);
+    const int lead = codes != nullptr && codes->dim() == 3;
     int64_t batch, rows, k;
-    if (!ok || !int4_of(codes, scale, zero, a[2] != Py_None, group, 0, &batch, &rows, &k) || !here({codes, scale, zero}))
+    if (!ok || !int4_of(codes, scale, zero, a[2] != Py_None, group, lead, &batch, &rows, &k) || batch > INT32_MAX ||
+        !here({codes, scale, zero}))
       return no_answer();
-    Tensor out = empty({rows, k}, f32 ? kF32 : kBF16, *codes);
+    Tensor out = lead ? empty({batch, rows, k}, f32 ? kF32 : kBF16, *codes) : empty({rows, k}, f32 ? kF32 : kBF16, *codes);
     const int st = g_calls.dequantize_int4(codes->data_ptr(), scale->data_ptr(), ptr_or_null<uint8_t>(zero),
-                                           int32_t(group), 1, rows, k, out.data_ptr(), code_of(out), stream_of(*codes));
+                                           int32_t(group), int32_t(batch), rows, k, out.data_ptr(), code_of(out),
+                                           stream_of(*codes));
     return answer(st, {out});
   });
 }

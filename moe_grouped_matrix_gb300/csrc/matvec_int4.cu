@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         v = v * root * root;
         if constexpr (kGated) {
           u = u * root * root;
-          v = (p.act == GMM_ACT_SILU ? act_value<GMM_ACT_SILU>(v) : act_value<GMM_ACT_GELU>(v)) * u;
+          v = (p.act == GMM_ACT_SILU ? act_value<GMM_ACT_SILU, false>(v) : act_value<GMM_ACT_GELU, false>(v)) * u;
         }
         put(to, c, v);
       }
@@ -746,9 +746,8 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
       misaligned(experts, 4) || misaligned(weights, 4) || misaligned(out, out_dtype == GMM_DTYPE_F32 ? 4 : 2))
     return GMM_ERR_ALIGN;
   if (misaligned(scratch, 16)) return GMM_ERR_ALIGN;
-  if (scratch_bytes < gmm_matvec_scratch_bytes(tokens, k, group, zero != nullptr, topk, x_per_slot) ||
-      (scratch == nullptr && scratch_bytes > 0))
-    return GMM_ERR_WORKSPACE;
+  const size_t needed = gmm_matvec_scratch_bytes(tokens, k, group, zero != nullptr, topk, x_per_slot);
+  if (scratch_bytes < needed || (needed > 0 && scratch == nullptr)) return GMM_ERR_WORKSPACE;
   int sms = 0;
   if (int st = require_device(&sms)) return st;
   const int64_t out_n = act != GMM_ACT_NONE ? n / 2 : n;

@@ -99,10 +99,10 @@ def balance_loss(logits, experts, score="softmax", token_mask=None, sequences=1,
         losses = torch.empty((2,), dtype=torch.float32, device=logits.device)
         counts = torch.empty((sequences, n), dtype=torch.int32, device=logits.device)
         counted = torch.empty((1,), dtype=torch.int32, device=logits.device)
-        scratch = torch.empty((nbytes,), dtype=torch.uint8, device=logits.device)
+        scratch = torch.empty((nbytes,), dtype=torch.uint8, device=logits.device) if nbytes else None
     _run("gmm_balance_loss", lib.gmm_balance_loss(
         logits.data_ptr(), code, tokens, n, ld, experts.data_ptr(), topk, _score(score), _ptr(token_mask), sequences,
-        losses.data_ptr(), counts.data_ptr(), counted.data_ptr(), scratch.data_ptr(), nbytes,
+        losses.data_ptr(), counts.data_ptr(), counted.data_ptr(), _ptr(scratch), nbytes,
         _on(logits.device, stream)))
     return BalanceLoss(losses, counts, counted)
 

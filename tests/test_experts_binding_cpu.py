@@ -49,7 +49,7 @@ VEC = dict(x=P, tokens=4, k=256, ld=256, per_slot=0, codes=P, scale=P, zero=None
 
 REFUSALS = [
     ("gmm_balance_loss", LOSS, NULL, [dict(logits=None), dict(chosen=None), dict(losses=None), dict(counts=None),
-                                      dict(counted=None), dict(scratch=None), dict(tokens=0, losses=None)]),
+                                      dict(counted=None), dict(tokens=0, losses=None)]),
     ("gmm_balance_loss", LOSS, DTYPE, [dict(dtype=2)]),
     ("gmm_balance_loss", LOSS, SHAPE, [dict(tokens=-2), dict(tokens=9), dict(sequences=0), dict(sequences=3),
                                        dict(experts=0), dict(experts=1025, ld=1025), dict(ld=7), dict(topk=0),
@@ -57,7 +57,7 @@ REFUSALS = [
                                        dict(tokens=LARGEST, topk=2), dict(tokens=LARGEST + 2, topk=1)]),
     ("gmm_balance_loss", LOSS, ALIGN, [dict(logits=ODD), dict(chosen=ODD), dict(losses=ODD), dict(counts=ODD),
                                        dict(counted=ODD), dict(scratch=ODD8)]),
-    ("gmm_balance_loss", LOSS, WORKSPACE, [dict(scratch_bytes=0), dict(scratch_bytes=100)]),
+    ("gmm_balance_loss", LOSS, WORKSPACE, [dict(scratch_bytes=0), dict(scratch_bytes=100), dict(scratch=None)]),
     ("gmm_balance_loss_backward", LBACK, NULL, [dict(dlosses=None), dict(counts=None), dict(counted=None),
                                                 dict(logits=None), dict(dlogits=None)]),
     ("gmm_balance_loss_backward", LBACK, DTYPE, [dict(dtype=3)]),
@@ -66,7 +66,7 @@ REFUSALS = [
     ("gmm_gated_act", ACT, NULL, [dict(h=None), dict(out=None)]),
     ("gmm_gated_act", ACT, DTYPE, [dict(dtype=2)]),
     ("gmm_gated_act", ACT, SHAPE, [dict(rows=-1), dict(f=0), dict(ld=15), dict(act=0), dict(act=3),
-                                   dict(f=2 ** 24 + 1, ld=2 ** 26), dict(rows=LARGEST + 1)]),
+                                   dict(f=2 ** 28, ld=2 ** 30), dict(rows=LARGEST + 1)]),
     ("gmm_gated_act", ACT, ALIGN, [dict(dtype=1, h=ODD), dict(dtype=1, out=ODD), dict(h=ctypes.c_void_p(4097))]),
     ("gmm_gated_act_backward", ABACK, NULL, [dict(dout=None), dict(h=None), dict(dh=None)]),
     ("gmm_gated_act_backward", ABACK, SHAPE, [dict(ld=15), dict(act=0)]),
@@ -92,7 +92,7 @@ REFUSALS = [
                                      dict(weights=ODD), dict(out_dtype=1, out=ODD), dict(scratch=ODD8)]),
     ("gmm_matvec_int4", VEC, WORKSPACE, [dict(tokens=100, k=4096, ld=4096), dict(tokens=100, k=4096, ld=4096, scratch=P,
                                                                                  scratch_bytes=1000),
-                                         dict(scratch_bytes=16)]),
+                                         dict(tokens=100, k=4096, ld=4096, scratch_bytes=1 << 30)]),
 ]
 
 
@@ -111,8 +111,9 @@ def test_good_arguments_reach_the_device_check(lib, name, base):
 
 
 def test_scratch_bytes(lib):
-    for tokens, experts, sequences in [(0, 1, 1), (1, 1, 1), (4096, 128, 1), (4096, 128, 4096), (2 ** 30, 1024, 1)]:
+    for tokens, experts, sequences in [(0, 1, 2), (4, 1, 2), (4096, 128, 1), (4096, 128, 4096), (2 ** 30, 1024, 1)]:
         assert lib.gmm_balance_scratch_bytes(tokens, experts, sequences) > 0
+    assert lib.gmm_balance_scratch_bytes(192, 8, 1) == 0
     for bad in [(-1, 8, 1), (8, 0, 1), (8, 1025, 1), (8, 8, 0), (8, 8, 3)]:
         assert lib.gmm_balance_scratch_bytes(*bad) == 0
 
