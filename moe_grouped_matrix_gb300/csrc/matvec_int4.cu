@@ -526,20 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       }
       const int k0 = w * kSpan;
       const __nv_bfloat16* xk = xp + k0;
-      // x of the next four chunks is read ahead of its use: it may come from the L2
+      // x of the next two chunks is read ahead of its use, where it may come from the L2
       constexpr int kQuad = 128 / kGroup;  // groups of four chunks
       using Sums = std::conditional_t<kQuad == 1, float, std::conditional_t<kQuad == 2, float2, float4>>;
-      uint4 b[2][4];
-      Sums n0[2], n1[2];
+      uint4 b[2][2];
       const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
-      auto read_x = [&](int to, int quad) {
+      auto read_x = [&](int pair) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[to][i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (quad * 4 + i) * 32));
-        n0[to] = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
-        n1[to] = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
+        for (int i = 0; i < 2; ++i)
+          b[pair % 2][i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (pair * 2 + i) * 32));
       };
       const bool full = k0 + kSpan <= p.k;
-      if (full) read_x(0, 0);
+      if (!kStaged && full) read_x(0);
       uint32_t touched[2] = {0, 0};
       if constexpr (!kStaged) {  // the next span's lines of x on their way from the L2 to the L1
         if (at + 1 < end && k0 + 2 * kSpan <= p.k) {
@@ -581,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         Scales sa, sb;
 #pragma unroll
         for (int quad = 0; quad < 4; ++quad) {
-          if (quad < 3) read_x((quad + 1) % 2, quad + 1);
+          const Sums n0 = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
+          const Sums n1 = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
           if (quad % 2 == 0)
             sa = reinterpret_cast<const Scales*>(scales)[8 * quad], sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
 #pragma unroll
@@ -589,8 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             const int at = quad % 2 * kQuad + i;  // in the window
             const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
-                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16),
-                  reinterpret_cast<const float*>(&n0[quad % 2])[i], reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) { return b[quad % 2][chunk % 4]; });
+                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0)[i],
+                  reinterpret_cast<const float*>(&n1)[i], [&](int chunk) {
+                    if constexpr (kStaged) return load<true>(reinterpret_cast<const uint4*>(xk + chunk * 32));
+                    if (chunk % 2 == 0 && chunk < 14) read_x(chunk / 2 + 1);
+                    return b[chunk / 2 % 2][chunk % 2];
+                  });
           }
         }
       } else {
