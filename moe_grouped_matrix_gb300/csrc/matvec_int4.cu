@@ -536,15 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         for (int i = 0; i < 2; ++i)
           b[pair % 2][i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (pair * 2 + i) * 32));
       };
+      Sums n0[2], n1[2];
+      auto read_sums = [&](int quad) {
+        n0[quad % 2] = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
+        n1[quad % 2] = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
+      };
       const bool full = k0 + kSpan <= p.k;
-      if (!kStaged && full) read_x(0);
-      uint32_t touched[2] = {0, 0};
-      if constexpr (!kStaged) {  // the next span's lines of x on their way from the L2 to the L1
-        if (at + 1 < end && k0 + 2 * kSpan <= p.k) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) touched[i] = __ldg(reinterpret_cast<const uint32_t*>(xk + kSpan + (t4 + 4 * i) * 64 - t4 * 8));
-        }
-      }
+      if (!kStaged && full) read_x(0), read_sums(0);
       copies_wait<0>();
       __syncwarp();
       fetch();
@@ -579,8 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         Scales sa, sb;
 #pragma unroll
         for (int quad = 0; quad < 4; ++quad) {
-          const Sums n0 = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
-          const Sums n1 = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
+          if constexpr (kStaged)
+            read_sums(quad);
+          else if (quad < 3)
+            read_sums(quad + 1);
           if (quad % 2 == 0)
             sa = reinterpret_cast<const Scales*>(scales)[8 * quad], sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
 #pragma unroll
@@ -588,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             const int at = quad % 2 * kQuad + i;  // in the window
             const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
-                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0)[i],
-                  reinterpret_cast<const float*>(&n1)[i], [&](int chunk) {
+                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0[quad % 2])[i],
+                  reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) {
                     if constexpr (kStaged) return load<true>(reinterpret_cast<const uint4*>(xk + chunk * 32));
                     if (chunk % 2 == 0 && chunk < 14) read_x(chunk / 2 + 1);
                     return b[chunk / 2 % 2][chunk % 2];
@@ -607,7 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
                 [&](int chunk) { return load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
         }
       }
-      if constexpr (!kStaged) asm volatile("" ::"r"(touched[0]), "r"(touched[1]));
       if (!kSum) {
         ++w;
       } else if (++w == p.spans || at + 1 == end) {
