@@ -1,10 +1,12 @@
 // The gated activation between an expert's two products, and its gradient:
 //   out = act(g) u,   dg = d u act'(g),   du = d act(g),   [g | u] = a row of h.
 //
-// Elementwise, bound by memory: 6 bytes an output in bf16 forward, 10 backward.  A
-// thread handles whole units of a row, the largest (up to 16 bytes) that all rows of
-// all operands are aligned to; a block is a patch of rows and columns, so that no
-// index is divided.
+// Elementwise, bound by memory: 6 bytes an output in bf16 forward, 10 backward (32768 rows
+// of 1024: 28.9 us and 48.1, 6.9 TB/s; 3001 rows of 2051 f32 13.6 and 20.2, 5.4 and 6.1).
+// A thread handles whole units of a row, the largest (up to 16 bytes) that all rows of all
+// operands are aligned to; a block is some rows, so that no index is divided.  bf16 results
+// take an exponential and a quotient of few instructions: with expf() and a full division
+// the instructions were the bound, not memory (39.5 us forward).
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -110,6 +112,8 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(Params p) {
 template <int kBytes, class T, bool kBack>
 cudaError_t launch(Params p, int act, cudaStream_t stream) {
   using U = typename UnitOf<kBytes>::type;
+  // two units of 16 bytes or four of fewer on their way (four and two: gradient 49.3 us for 48.1 in bf16, f32 rows
+  // of 2051 16.0 for 13.6)
   constexpr int kPer = kBytes == 16 ? 2 : 4;
   p.units = int32_t(p.f / kBytes);
   // whole warps of a row that its units divide among evenly, over as many turns as 256 threads need

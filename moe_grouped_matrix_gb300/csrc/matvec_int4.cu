@@ -2,36 +2,45 @@
 //   h[t, j] = sum over groups of scale * sum of (code - zero) x
 // for the expert of each slot (t, j), in the order of the tokens.
 //
-// Bound by memory: half a byte a weight, read once.  At 6.8 TB/s an SM gets some 47
-// weights a cycle, and may spend 2.7 issue slots of a lane on each; one fp32
-// multiply-add with its conversion takes about 2 for a single token.  So the sums run on
-// mma.sync m16n8k16, 16 weight rows by 8 columns, with operands that cost next to nothing:
-// the bit pattern of a whole number below 256 is, read as bf16, that number times 2^-133 (a
-// subnormal, or the first binade above them, whose spacing is the same), so a mask takes two
-// codes out of a word, at its bits 0-3 and 16-19 or, 16 times as large, at 4-7 and 20-23: five
-// instructions for eight weights and all their columns.  The other operand is x times a power
-// of two that puts each row's largest value at 2^116, exactly (x is bf16, so is the product:
-// what lies 2^242 below the largest is lost), divided by 16 where the codes are 16 times as
-// large.  Products are exact, sums fp32.  Codes are not negative there (two's complement ones
-// have their top bit flipped, which adds 8): the sum starts at -8 (or -zero) times the group's
-// sum of x, which is computed once for each row.  That makes the terms of a sum up to
-// |code| + 2 * 8 times |x| instead of |code - 8| times, a few units of fp32 more of error.  A
-// row with an infinity or NaN gives NaN.  A group's sum is scaled in fp32, and the power of two
-// taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the
-// eight k of a 32-bit word for its own, and x is permuted alike.  x of few tokens is made ready
-// by each CTA in its shared memory while its first weights are on their way, x of more by a kernel
-// ahead.
+// Bound by memory: half a byte a weight, read once.  At 6.8 TB/s an SM gets some 47 weights a cycle and
+// may spend 2.7 issue slots of a lane on each; one fp32 multiply-add with its conversion takes about 2 for a
+// single token.  So the sums run on mma.sync m16n8k16, 16 weight rows by 8 columns (tcgen05 wants its
+// operands written to shared memory in 8 or 16 bits first, four times the bytes, for 128 rows at least),
+// with operands that cost next to nothing: a bit pattern below 256 is, read as bf16, that whole number times
+// 2^-133 (subnormals, and the first binade above them, whose spacing is the same; the instruction takes
+// subnormals as they are), so a mask takes two codes out of a word, at its bits 0-3 and 16-19 or, 16 times
+// as large, at 4-7 and 20-23: five instructions for eight weights and all their columns.  Subtracting the
+// zero point there, exactly, took eleven, and the products of one token 34 us for 23.
 //
-// A warp streams windows of 16 rows by 256 k through a ring of its own in shared memory,
-// by asynchronous copies that only it waits for: no barrier between warps but one for each
-// unit's sums.  Whole 128-byte lines of each row are copied, 16-byte chunks permuted by row
-// so that reading a chunk's word by 8 rows and 4 lanes meets all banks.
+// The other operand is x times a power of two that brings each row's largest value to 2^116 or 2^117,
+// exactly (what lies 2^242 below the largest is lost), divided by 16 where the codes are 16 times as large.
+// Products are exact, sums fp32.  Codes are not negative there (two's complement ones have their top bit
+// flipped, which adds 8), and -8 (or -zero) times the group's sum of x, computed once for each row, is added
+// to each group's sum: the terms of a sum are then up to |code| + 8 and 8 times |x| instead of |code - 8|
+// times, some units of fp32 more of error.  A row with an infinity or NaN gives NaN; a sum of scale * x below
+// 2^-110 of a row's largest x loses bits as a subnormal.  A group's sum is scaled in fp32, and the power of two
+// taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the eight k of a
+// 32-bit word for its own, and x is permuted alike.
 //
-// A unit is 8 / KW tiles of 16 rows (with an activation 8 gates and the 8 rows they gate),
-// KW warps to a tile along k, for
+// A warp streams spans of 16 rows by 512 k through two stages of its own in shared memory, by asynchronous
+// copies that only it waits for, whole lines of each row.  Teams of 1 to 16 warps share a tile along k: few
+// for long streams, many for few tiles; each CTA finds the number with which the last team ends first (fixed
+// at 1, 4, 16: 2 of 8 experts of 28672 x 4096 take 23.4, 24.5, 46 us for 22.8 with 2, their way back 46, 21.3,
+// 22.3 for 20.9 with 8).  A unit of a team's work is a tile of 16 rows (with an activation 8 gates and the 8
+// rows they gate) for
 //   - up to 8 slots of one expert, or
-//   - with weights, 8 tokens: all of their experts, one after another, columns the
-//     tokens, so that the sum over a token's slots stays in registers.
+//   - with weights, 8 tokens: all of their experts, one after another, columns the tokens, so that the sum
+//     over a token's slots stays in registers.
+//
+// x has to come from shared memory: through the caches a span's 8 KB for 8 columns is twice the weights'.
+// Each CTA makes it ready there where it fits as a whole (2 of 8 experts of 4096 x 4096: 1 token 7.9 us for
+// 8.8, 7 tokens 18.0 for 23.9; of 512 x 1024, 4 tokens 4.8 for 6.8); else a kernel ahead does, and a CTA copies
+// one item's at a time, or where it has little to do reads it through the caches all the same.
+//
+// Measured: 1 token, 2 of 8 experts, 28672 x 4096, groups of 128, activation: 22.8 us, 121 MB at 5.3 TB/s (the
+// copies alone: 21.4 us); their way back, 4096 x 14336: 20.9 us, of which 8 before the first product, and
+// 256 tiles on 152 SMs; 8 of 128 experts, 2048 x 2048, groups of 32: 8.4 us for 19 MB, half of them before the
+// first product; 32 tokens, 4 of 64 experts, 2048 x 4096: 58 us for some 180 MB.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -49,7 +58,7 @@ constexpr int kWindow = 256;                 // k of a window of scales
 constexpr int kSpan = 2 * kWindow;           // k of a stage
 constexpr int kCols = 8;                     // columns of an item
 constexpr int kMaxSlots = 256;               // slots of a launch
-constexpr int kPitch = kSpan / 2 + 16;      // bytes between rows of codes in shared memory: see below
+constexpr int kPitch = kSpan / 2 + 16;       // bytes between rows of codes in shared memory: see below
 
 struct Params {
   const __nv_bfloat16* x;
@@ -65,6 +74,7 @@ struct Params {
   void* out;
   int32_t out_n, out_f32;  // columns of out, its type
   int32_t x_rows, x_pitch;  // rows of x made ready, and elements between them
+  int32_t item_columns, item_pitch;  // kItems: most columns of an item, elements between them in shared memory
   // where not in shared memory: the rows, their groups' sums, and what takes their results to their size
   __nv_bfloat16* ready;
   float* sums;
@@ -212,8 +222,17 @@ __device__ __forceinline__ T load(const T* p) {
     return __ldg(p);
 }
 
-template <int kGroup, bool kZero, bool kGated, bool kSum, bool kStaged>
+// Where x comes from.
+enum Mode {
+  kCaches,  // rows that a kernel ahead has made ready, through the caches
+  kAll,     // all rows, made ready by each CTA in its shared memory
+  kItems    // such rows again, those of one item at a time copied to a CTA's shared memory
+};
+
+template <int kGroup, bool kZero, bool kGated, bool kSum, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
+  constexpr bool kStaged = kMode == kAll, kShared = kMode != kCaches;
+  static_assert(!(kSum && kMode == kItems), "a unit has one item");
   using R = Ring<kGroup, kZero>;
   constexpr int kEach = R::kEach;
   griddep_begin();
@@ -274,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       if (lane == 0) table.power[row] = int16_t(power);
     }
   // this thread's slot: its expert, its item's head and its column there
+  const int columns_of_item = kMode == kItems ? p.item_columns : kCols;
   int mine = -1, head = -1, column = 0;
   if (tid < slots) mine = table.expert[tid];
   if (mine >= 0) {
@@ -294,13 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         }
       }
     } else {
-      int before = 0, at = tid;
+      int at = tid;
       for (int j = 0; j < tid; ++j)
         if (table.expert[j] == mine) {
-          if (before % kCols == 0) at = j;
-          ++before;
+          if (column == 0) at = j;
+          column = column + 1 == columns_of_item ? 0 : column + 1;
         }
-      column = before % kCols;
       head = column == 0 ? tid : at;
     }
   }
@@ -352,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     const int at = min(lane, 4);
     const unsigned spans = unsigned(p.spans) * (kSum ? (unsigned(items) + chunks - 1) / chunks : 1u);
     const unsigned units = unsigned(groups) * unsigned(min(p.tiles, 1 << 20)), teams = gridDim.x * unsigned(kWarps >> at);
-    const unsigned rounds = (units + teams - 1) / teams, each = (spans + (1u << at) - 1) >> at;
+    // (kItems: a CTA's range ends within an item, and in it)
+    const unsigned rounds = (units + teams - 1) / teams + (kMode == kItems ? 1 : 0), each = (spans + (1u << at) - 1) >> at;
     const unsigned total = unsigned(fminf(float(rounds) * float(each + 1), 2.5e8f));
     const unsigned cost = __reduce_min_sync(0xffffffffu, total * 8 + at);
     lg = int(cost % 8);
@@ -361,12 +381,40 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   const int member = warp & (size - 1), team = warp >> lg;
   // teams of all CTAs; a CTA's are far apart, so that the last round is spread over all of them, or next
   // to one another, so that they read the same rows of x through the SM's cache
-  const int teams = int(gridDim.x) * (kWarps >> lg);
-  const int start = kStaged ? int(blockIdx.x) + team * int(gridDim.x) : int(blockIdx.x) * (kWarps >> lg) + team;
-  const int dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
-  Unit ahead{start / p.tiles, 0};
-  ahead.tile = start - ahead.group * p.tiles;
-  Unit here = ahead;
+  const int cta_teams = kWarps >> lg, teams = int(gridDim.x) * cta_teams;
+  Unit ahead{0, 0}, here{0, 0};
+  int dgroup = 0, dtile = 0;            // between a team's units
+  int last_group = 0, last_tiles = 0;   // kItems: the CTA's last group, and how many of its tiles it takes
+  if constexpr (kMode == kItems) {  // a range of units for each CTA, its teams side by side within each item
+    const int64_t units = int64_t(groups) * p.tiles;
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    here.group = int(u0 / p.tiles), here.tile = int(u0 - int64_t(here.group) * p.tiles) + team;
+    last_group = int(u1 / p.tiles), last_tiles = int(u1 - int64_t(last_group) * p.tiles);
+  } else {
+    const int start = kStaged ? int(blockIdx.x) + team * int(gridDim.x) : int(blockIdx.x) * cta_teams + team;
+    dgroup = teams / p.tiles, dtile = teams - dgroup * p.tiles;
+    here.group = start / p.tiles, here.tile = start - here.group * p.tiles;
+  }
+  auto tiles_end = [&](int group) { return kMode == kItems && group >= last_group ? last_tiles : p.tiles; };
+  auto in_range = [&](const Unit& u) {
+    return kMode == kItems ? u.group < last_group || (u.group == last_group && u.tile < last_tiles) : u.group < groups;
+  };
+  // the team's next unit (kItems: from a place past its tiles, too)
+  auto settle = [&](Unit& u) {
+    if constexpr (kMode == kItems)
+      while (u.group <= last_group && u.tile >= tiles_end(u.group)) u.tile = team, ++u.group;
+  };
+  auto advance = [&](Unit& u) {
+    if constexpr (kMode == kItems) {
+      u.tile += cta_teams;
+      settle(u);
+    } else {
+      u.advance(dgroup, dtile, p.tiles);
+    }
+  };
+  const int first_group = here.group;
+  settle(here);
+  ahead = here;
   uint8_t* const ring = smem + warp * R::kBytes;
   const int lane_row = lane >> 4, lane_chunk = lane & 15;
   // where this lane's pieces of the next span go
@@ -407,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
              lane % kZeroPieces * 16;
   };
   auto enter = [&] {
-    while (ahead.group < groups) {
+    while (in_range(ahead)) {
       int first;
       part_of(ahead, first, pair, pair_end);
       if (pair < pair_end) {
@@ -416,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         aim();
         return;
       }
-      ahead.advance(dgroup, dtile, p.tiles);
+      advance(ahead);
     }
   };
   auto fetch = [&] {  // and on to the next
-    if (ahead.group < groups) {
+    if (in_range(ahead)) {
       const uint32_t to = fill_codes + fill, to_lane = fill_lane + fill;
       if (second && span < whole) {
         const uint8_t *c0 = code0, *c1 = code1;
@@ -454,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       }
       fill = R::kStage - fill;
       if (++pair == pair_end) {
-        ahead.advance(dgroup, dtile, p.tiles);
+        advance(ahead);
         enter();
       } else if (++span == p.spans) {
         span = 0, ++item;
@@ -504,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   const float *sums0 = nullptr, *sums1 = nullptr;   // of columns 2 t4 and 2 t4 + 1
   float w0 = 0.f, w1 = 0.f, root0 = 0.f, root1 = 0.f;
   bool has0 = false, has1 = false;
-  for (; here.group < groups; here.advance(dgroup, dtile, p.tiles)) {
+  auto work = [&] {  // on the unit here
     int first, at, end;
     part_of(here, first, at, end);
     int now = first + (kSum ? at / p.spans : 0), w = kSum ? at - (now - first) * p.spans : at;
@@ -513,11 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       if (now != last) {
         last = now;
         // a column without a slot takes the head's x: nothing of it is used
-        const int head = table.row[table.head[now]];
         const int s = table.slot[now][g], s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
         has0 = s0 >= 0, has1 = s1 >= 0;
-        const int r0 = has0 ? table.row[s0] : head, r1 = has1 ? table.row[s1] : head;
-        xp = ready + int64_t(s < 0 ? head : table.row[s]) * p.x_pitch + t4 * 8;
+        int r, r0, r1;  // the columns' rows of x: of the item's, or of all
+        if constexpr (kMode == kItems) {
+          r = s < 0 ? 0 : g, r0 = has0 ? 2 * t4 : 0, r1 = has1 ? 2 * t4 + 1 : 0;
+        } else {
+          const int head = table.row[table.head[now]];
+          r = s < 0 ? head : table.row[s], r0 = has0 ? table.row[s0] : head, r1 = has1 ? table.row[s1] : head;
+        }
+        xp = ready + int64_t(r) * (kMode == kItems ? p.item_pitch : p.x_pitch) + t4 * 8;
         sums0 = sums + int64_t(r0) * x_groups, sums1 = sums + int64_t(r1) * x_groups;
         if constexpr (kSum) {
           w0 = has0 ? p.weights[s0] : 0.f, w1 = has1 ? p.weights[s1] : 0.f;
@@ -534,15 +587,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       auto read_x = [&](int pair) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          b[pair % 2][i] = load<kStaged>(reinterpret_cast<const uint4*>(xk + (pair * 2 + i) * 32));
+          b[pair % 2][i] = load<kShared>(reinterpret_cast<const uint4*>(xk + (pair * 2 + i) * 32));
       };
       Sums n0[2], n1[2];
       auto read_sums = [&](int quad) {
-        n0[quad % 2] = load<kStaged>(reinterpret_cast<const Sums*>(sums0k) + quad);
-        n1[quad % 2] = load<kStaged>(reinterpret_cast<const Sums*>(sums1k) + quad);
+        n0[quad % 2] = load<kShared>(reinterpret_cast<const Sums*>(sums0k) + quad);
+        n1[quad % 2] = load<kShared>(reinterpret_cast<const Sums*>(sums1k) + quad);
       };
       const bool full = k0 + kSpan <= p.k;
-      if (!kStaged && full) read_x(0), read_sums(0);
+      if (!kShared && full) read_x(0), read_sums(0);
       copies_wait<0>();
       __syncwarp();
       fetch();
@@ -577,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         Scales sa, sb;
 #pragma unroll
         for (int quad = 0; quad < 4; ++quad) {
-          if constexpr (kStaged)
+          if constexpr (kShared)
             read_sums(quad);
           else if (quad < 3)
             read_sums(quad + 1);
@@ -590,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
                   __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0[quad % 2])[i],
                   reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) {
-                    if constexpr (kStaged) return load<true>(reinterpret_cast<const uint4*>(xk + chunk * 32));
+                    if constexpr (kShared) return load<true>(reinterpret_cast<const uint4*>(xk + chunk * 32));
                     if (chunk % 2 == 0 && chunk < 14) read_x(chunk / 2 + 1);
                     return b[chunk / 2 % 2][chunk % 2];
                   });
@@ -602,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 #pragma unroll 1
         for (int q = 0; q < left; ++q) {
           const int sq = q / kEach * (16 * kEach) + q % kEach;
-          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]), load<kStaged>(sums0k + q),
-                load<kStaged>(sums1k + q),
-                [&](int chunk) { return load<kStaged>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
+          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]), load<kShared>(sums0k + q),
+                load<kShared>(sums1k + q),
+                [&](int chunk) { return load<kShared>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
         }
       }
       if (!kSum) {
@@ -648,6 +701,28 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         put(to, c, v);
       }
     }
+  };
+  if constexpr (kMode == kItems) {
+    auto* rows = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
+    float* row_sums = reinterpret_cast<float*>(rows + p.item_columns * p.item_pitch);
+    const int eights = p.k / 8, fours = x_groups / 4;
+    ready = rows, sums = row_sums;
+    for (int group = first_group; group <= last_group && (group < last_group || last_tiles > 0); ++group) {
+      __syncthreads();  // the last item's x has been read
+      const int columns = table.columns[group];
+      for (int c = 0; c < columns; ++c) {
+        const int64_t row = table.row[table.slot[group][c]];
+        for (int i = tid; i < eights; i += kThreads) copy16(smem_u32(rows + c * p.item_pitch + i * 8), p.ready + row * p.x_pitch + i * 8);
+        for (int i = tid; i < fours; i += kThreads) copy16(smem_u32(row_sums + c * x_groups + i * 4), p.sums + row * x_groups + i * 4);
+      }
+      copies_commit();
+      copies_wait<0>();
+      __syncthreads();
+      last = -1;
+      for (; here.group == group && in_range(here); advance(here)) work();
+    }
+  } else {
+    for (; in_range(here); advance(here)) work();
   }
   copies_wait<0>();
 }
@@ -679,37 +754,56 @@ constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) *
 int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + sums_pitch(k, group) * 4 + 4); }
 // In shared memory rows are half a line of banks apart.
 int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
-bool is_staged(int64_t rows, int64_t k, int group, bool zero) {
+// Rows that fit the shared memory.
+int64_t staged_rows(int64_t k, int group, bool zero) {
   const int64_t each = kWindow / group, ring = int64_t(kWarps) * 2 * (16 * kPitch + 2 * 16 * each * (zero ? 3 : 2));
-  return ready_bytes(rows, staged_pitch(k), k, group) <= int64_t(kMaxShared) - ring;
+  return (int64_t(kMaxShared) - ring) / ready_bytes(1, staged_pitch(k), k, group);
 }
 int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
 
-template <int kGroup, bool kZero, bool kGated, bool kSum>
-cudaError_t launch(const Params& p, bool staged, int sms, cudaStream_t stream) {
+template <int kGroup, bool kZero, bool kGated, bool kSum, Mode kMode>
+cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
   using R = Ring<kGroup, kZero>;
-  const size_t smem = size_t(kWarps) * R::kBytes + (staged ? size_t(ready_bytes(p.x_rows, p.x_pitch, p.k, kGroup)) : 0);
-  auto kern = staged ? matvec_kernel<kGroup, kZero, kGated, kSum, true> : matvec_kernel<kGroup, kZero, kGated, kSum, false>;
+  const int64_t rows = kMode == kAll ? p.x_rows : kMode == kItems ? p.item_columns : 0;
+  const size_t smem = size_t(kWarps) * R::kBytes + size_t(ready_bytes(rows, staged_pitch(p.k), p.k, kGroup));
+  auto kern = matvec_kernel<kGroup, kZero, kGated, kSum, kMode>;
   // for every launch: the attribute is the current device's, and one size for all calls
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
-  if (!staged)
+  if (kMode != kAll)
     if (cudaError_t e = launch_dependent(make_ready_kernel<kGroup, kZero>, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
   return launch_dependent(kern, unsigned(sms), kThreads, smem, stream, 1, p);
 }
 
-template <int kGroup, bool kZero>
-cudaError_t by_form(const Params& p, bool staged, int sms, cudaStream_t stream) {
-  if (p.weights != nullptr) return launch<kGroup, kZero, false, true>(p, staged, sms, stream);
-  return p.act != GMM_ACT_NONE ? launch<kGroup, kZero, true, false>(p, staged, sms, stream)
-                               : launch<kGroup, kZero, false, false>(p, staged, sms, stream);
+template <int kGroup, bool kZero, bool kGated, bool kSum>
+cudaError_t by_mode(Params p, int sms, cudaStream_t stream) {
+  const int64_t fit = staged_rows(p.k, kGroup, kZero);
+  if (p.x_rows <= fit) return launch<kGroup, kZero, kGated, kSum, kAll>(p, sms, stream);
+  if constexpr (!kSum) {
+    // Copying an item's x pays where a CTA then has at least some 50 spans of weights for its warps (experts
+    // counted at most once): 16 tokens, 2 of 8 experts of 4096 x 4096 (108 spans) take 23.7 us and through the
+    // caches 25.9, 32 of 4 of 16 of 1024 x 1024 (13) 15.8 and 11.2.  Fewer columns than half of an item's would
+    // read the weights more than twice as often.
+    const int64_t items = p.experts < p.tokens * p.topk ? p.experts : p.tokens * p.topk;
+    p.item_columns = int32_t(fit < kCols ? fit : kCols), p.item_pitch = int32_t(staged_pitch(p.k));
+    if (p.item_columns >= kCols / 2 && items * p.tiles * p.spans >= 50 * int64_t(sms))
+      return launch<kGroup, kZero, kGated, kSum, kItems>(p, sms, stream);
+  }
+  return launch<kGroup, kZero, kGated, kSum, kCaches>(p, sms, stream);
 }
 
-cudaError_t matvec(const Params& p, int group, bool staged, int sms, cudaStream_t stream) {
+template <int kGroup, bool kZero>
+cudaError_t by_form(const Params& p, int sms, cudaStream_t stream) {
+  if (p.weights != nullptr) return by_mode<kGroup, kZero, false, true>(p, sms, stream);
+  return p.act != GMM_ACT_NONE ? by_mode<kGroup, kZero, true, false>(p, sms, stream)
+                               : by_mode<kGroup, kZero, false, false>(p, sms, stream);
+}
+
+cudaError_t matvec(const Params& p, int group, int sms, cudaStream_t stream) {
   const bool zero = p.zero != nullptr;
   switch (group) {
-    case 32: return zero ? by_form<32, true>(p, staged, sms, stream) : by_form<32, false>(p, staged, sms, stream);
-    case 64: return zero ? by_form<64, true>(p, staged, sms, stream) : by_form<64, false>(p, staged, sms, stream);
-    default: return zero ? by_form<128, true>(p, staged, sms, stream) : by_form<128, false>(p, staged, sms, stream);
+    case 32: return zero ? by_form<32, true>(p, sms, stream) : by_form<32, false>(p, sms, stream);
+    case 64: return zero ? by_form<64, true>(p, sms, stream) : by_form<64, false>(p, sms, stream);
+    default: return zero ? by_form<128, true>(p, sms, stream) : by_form<128, false>(p, sms, stream);
   }
 }
 
@@ -727,7 +821,7 @@ extern "C" size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t gr
   const int64_t most = launch_tokens(topk), count = tokens < most ? tokens : most;
   const int64_t rows = x_per_slot != 0 ? count * topk : count;
   // a last launch of fewer tokens may not need what the others do
-  return is_staged(rows, k, group, has_zero != 0) ? 0 : size_t(ready_bytes(rows, k, k, group));
+  return rows <= staged_rows(k, group, has_zero != 0) ? 0 : size_t(ready_bytes(rows, k, k, group));
 }
 
 extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t x_ld, int x_per_slot, const void* codes,
@@ -769,7 +863,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     p.weights = weights == nullptr ? nullptr : weights + t0 * topk;
     p.act = act, p.out_n = int32_t(out_n), p.out_f32 = out_dtype == GMM_DTYPE_F32;
     p.x_rows = int32_t(x_per_slot != 0 ? count * topk : count);
-    const bool staged = is_staged(p.x_rows, k, group, zero != nullptr);
+    const bool staged = p.x_rows <= staged_rows(k, group, zero != nullptr);
     p.x_pitch = int32_t(staged ? staged_pitch(k) : k);
     if (!staged) {
       p.ready = static_cast<__nv_bfloat16*>(scratch);
@@ -778,7 +872,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     }
     const int64_t first = t0 * (weights != nullptr ? 1 : topk) * out_n;
     p.out = static_cast<char*>(out) + first * (out_dtype == GMM_DTYPE_F32 ? 4 : 2);
-    const cudaError_t e = matvec(p, group, staged, sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = matvec(p, group, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return record_cuda_error(e);
   }
   return GMM_OK;

@@ -19,6 +19,8 @@
 // codes are rounded by adding 1.5 2^23 and put together as they stand, sum of 16^i (1.5 2^23 + code),
 // the constant part taken off at the end.  Without zero points nothing has to be kept within -8 .. 7,
 // because a scale of 8 bits is at most 2^-8 of itself below max|x| / 7 (subnormal ones take a longer way).
+// Measured: 8 x 4096 x 4096 bf16, groups of 128: 58 us (339 MB, 5.8 TB/s) and back 51.7 (6.6); 2048 x 4000 f32,
+// groups of 32 with zero points, 8.6 and 5.2.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -308,7 +310,8 @@ int check(int dtype, int32_t batch, int64_t rows, int64_t k, int64_t ld, int32_t
   return GMM_OK;
 }
 
-// Warps to a row: as few as keep some 4000 on the GPU, at most one for each `each` values.
+// Warps to a row: as few as keep some 4000 on the GPU, at most one for each `each` values (one row of 16384
+// 1.5 us, with one warp 12; 256 rows of 4096 2.2 and 4.4).
 int parts_of(int64_t rows, int64_t k, int64_t each) {
   int lg = 0;
   while (lg < 20 && (rows << lg) < 4096 && (each << lg) < k) ++lg;
