@@ -45,7 +45,7 @@ def check_quantize(x, group, zero_points):
     return q
 
 
-SHAPES = [(1, 128), (3, 256), (8, 384), (17, 1280), (5, 4096), (301, 640), (1, 16384)]
+SHAPES = [(1, 128), (3, 256), (8, 384), (17, 1280), (5, 4096), (301, 640), (1, 16384), (5000, 256)]
 
 
 @pytest.mark.parametrize("zero_points", BOTH)
@@ -192,6 +192,35 @@ def test_one_matrix(tokens, n, k, zero_points):
     w = G.Int4Tensor(w.codes[0], w.scale[0], None if w.zero is None else w.zero[0], 64)
     check_matvec(normal((tokens, k), 2, dtype=torch.bfloat16), w)
     check_matvec(normal((tokens, k), 2, dtype=torch.bfloat16), w, act="silu") if n % 16 == 0 else None
+
+
+# tokens, experts, topk, n, k, group, zero points: much work for each CTA, where an item's x is copied at a time;
+# the whole of 8 columns, and fewer than that, and ends of k and n within a tile
+@pytest.mark.parametrize("case", [(40, 8, 2, 4096, 2176, 128, False), (40, 8, 2, 4104, 2048, 64, True),
+                                  (24, 4, 2, 4096, 4096, 32, True), (48, 8, 2, 4112, 2080, 32, False),
+                                  (17, 9, 1, 2064, 4096, 64, False)])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_products_of_many_tokens(case, act):
+    tokens, E, topk, n, k, group, zero_points = case
+    if act is not None and n % 16:
+        n += 8
+    w = make(E, n, k, group, zero_points)
+    experts = choose(tokens, min(E, 9), topk, k)
+    check_matvec(normal((tokens, k), 2, dtype=torch.bfloat16), w, experts, act=act)
+
+
+@pytest.mark.parametrize("tokens,topk", [(256, 1), (257, 1), (128, 2), (8, 32), (9, 32)])
+def test_the_most_slots_of_a_launch(tokens, topk):
+    w = make(40, 48, 256, 64, False)
+    x, experts = normal((tokens, 256), 2, dtype=torch.bfloat16), choose(tokens, 40, topk, 3)
+    check_matvec(x, w, experts)
+    check_matvec(x, w, experts, normal((tokens, topk), 5))
+
+
+def test_long_rows_of_several_tokens():
+    w = make(3, 64, 16384, 128, False)
+    check_matvec(normal((9, 16384), 2, dtype=torch.bfloat16), w, choose(9, 3, 2, 1))
+    check_matvec(normal((9, 2, 16384), 2, dtype=torch.bfloat16), w, choose(9, 3, 2, 1), normal((9, 2), 5))
 
 
 def test_more_slots_than_a_launch_takes():
