@@ -123,6 +123,8 @@ size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t group, int ha
  * and nothing to a sum.  Each expert's weights are read once for every 8 of its tokens (for
  * every 8 tokens, with weights), so this is for the few rows an expert has in decoding; gmm()
  * is for more.  The same inputs give the same bits.  A row of x with an infinity or NaN gives NaN.
+ * Products of scales below 2^-110 lose bits as subnormals, and so does x below 2^-242 of its row's
+ * largest value.
  *
  *   x        BF16 [tokens, k] with row pitch x_ld (x_per_slot 0: all slots of a token share
  *            it) or dense [tokens, topk, k] (x_per_slot 1; x_ld is not used)

@@ -4,7 +4,7 @@
 // ABI.  At decoding sizes an operator is a few microseconds on the GPU, and this
 // work done in Python costs more: combine() takes the host 10 us in Python, 3 here.
 //
-// Every function returns None for any other arguments, and moe.py then goes
+// Every function returns None for any other arguments, and moe.py or experts.py then goes
 // through them one by one and says what is wrong or handles the case; an int is
 // the C ABI's status, not GMM_OK.  The C ABI's functions come from the library
 // that the binding has loaded, by address.

@@ -17,8 +17,8 @@
 // Products are exact, sums fp32.  Codes are not negative there (two's complement ones have their top bit
 // flipped, which adds 8), and -8 (or -zero) times the group's sum of x, computed once for each row, is added
 // to each group's sum: the terms of a sum are then up to |code| + 8 and 8 times |x| instead of |code - 8|
-// times, some units of fp32 more of error.  A row with an infinity or NaN gives NaN; a sum of scale * x below
-// 2^-110 of a row's largest x loses bits as a subnormal.  A group's sum is scaled in fp32, and the power of two
+// times, some units of fp32 more of error.  A row with an infinity or NaN gives NaN; scales below 2^-110
+// lose bits, as their products with sums of 2^-17 of x are subnormal.  A group's sum is scaled in fp32, and the power of two
 // taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the eight k of a
 // 32-bit word for its own, and x is permuted alike.
 //
