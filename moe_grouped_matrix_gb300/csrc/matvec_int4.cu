@@ -18,9 +18,9 @@
 // flipped, which adds 8), and -8 (or -zero) times the group's sum of x, computed once for each row, is added
 // to each group's sum: the terms of a sum are then up to |code| + 8 and 8 times |x| instead of |code - 8|
 // times, some units of fp32 more of error.  A row with an infinity or NaN gives NaN; scales below 2^-110
-// lose bits, as their products with sums of 2^-17 of x are subnormal.  A group's sum is scaled in fp32, and the power of two
-// taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the eight k of a
-// 32-bit word for its own, and x is permuted alike.
+// lose bits, as their products with sums of 2^-17 of x are subnormal.  A group's sum is scaled in fp32, and the
+// power of two taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the
+// eight k of a 32-bit word for its own, and x is permuted alike.
 //
 // A warp streams spans of 16 rows by 512 k through two stages of its own in shared memory, by asynchronous
 // copies that only it waits for, whole lines of each row.  Teams of 1 to 16 warps share a tile along k: few
@@ -712,8 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       const int columns = table.columns[group];
       for (int c = 0; c < columns; ++c) {
         const int64_t row = table.row[table.slot[group][c]];
-        for (int i = tid; i < eights; i += kThreads) copy16(smem_u32(rows + c * p.item_pitch + i * 8), p.ready + row * p.x_pitch + i * 8);
-        for (int i = tid; i < fours; i += kThreads) copy16(smem_u32(row_sums + c * x_groups + i * 4), p.sums + row * x_groups + i * 4);
+        for (int i = tid; i < eights; i += kThreads)
+          copy16(smem_u32(rows + c * p.item_pitch + i * 8), p.ready + row * p.x_pitch + i * 8);
+        for (int i = tid; i < fours; i += kThreads)
+          copy16(smem_u32(row_sums + c * x_groups + i * 4), p.sums + row * x_groups + i * 4);
       }
       copies_commit();
       copies_wait<0>();
@@ -744,7 +746,8 @@ __global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
   const int power = power_of(tops, kWarps);
 #pragma unroll 4
   for (int w = warp; w < p.windows; w += kWarps)
-    make_ready<kGroup, kZero>(window_of(x, p.k, w), p.k, w, power, p.ready + int64_t(row) * p.x_pitch, p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
+    make_ready<kGroup, kZero>(window_of(x, p.k, w), p.k, w, power, p.ready + int64_t(row) * p.x_pitch,
+                              p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
   if (threadIdx.x == 0) p.roots[row] = root_of(power);
 }
 
