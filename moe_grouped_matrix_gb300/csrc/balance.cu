@@ -32,6 +32,7 @@ namespace gmmk {
 namespace {
 
 constexpr int kWarps = 16, kBackWarps = 8;
+constexpr int kSms = 152;  // of a GB300
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -107,7 +108,8 @@ __device__ __forceinline__ float exponentials(float (&l)[V], float high) {
 // is.  sigmoid(l) / exp(high) = ex / (1 + exp(l)) loses none of a row's scores however small all of them are;
 // where exp(high) is near fp32's end they are 1 / (1 + exp(-l)).  One quotient of a few units of error each.
 template <int V>
-__device__ __forceinline__ void sigmoids(const float (&l)[V], const float (&ex)[V], float high, float (&score)[V], float (&off)[V]) {
+__device__ __forceinline__ void sigmoids(const float (&l)[V], const float (&ex)[V], float high, float (&score)[V],
+                                         float (&off)[V]) {
   if (!(high > 60.f)) {
     const float scale = expf(high);
 #pragma unroll
@@ -533,7 +535,7 @@ Cut cut_of(int64_t tokens, int64_t sequences) {
   Cut c{1, 1, per > 0 ? per : 1};
   if (per == 0) return c;
   const int64_t wanted = (per + 2 * kWarps - 1) / (2 * kWarps);  // CTAs of a sequence, were there no others
-  const int64_t share = sequences < 304 ? 304 / sequences : 1;
+  const int64_t share = sequences < 2 * kSms ? 2 * kSms / sequences : 1;
   int64_t ctas = wanted < share ? wanted : share;
   if (sequences == 1 && tokens <= 8 * kWarps * kMaxCtas && ctas > kMaxCtas) ctas = kMaxCtas;
   c.ctas = sequences == 1 && ctas == kMaxCtas ? kMaxCtas : ctas >= 8 ? 8 : ctas >= 4 ? 4 : ctas >= 2 ? 2 : 1;
@@ -637,7 +639,8 @@ extern "C" int gmm_balance_loss(const void* logits, int logits_dtype, int64_t to
     const int64_t turns = sequences * ((num_experts + 31) / 32);
     int ctas = 1;
     while (ctas < kMaxCtas && ctas * 2 <= sequences && ctas * 2 * kJoinWarps < turns) ctas *= 2;
-    const JoinParams j{sums, run_counts, rest, sequences, int32_t(cut.clusters), num_experts, ctas, losses, counts, counted};
+    const JoinParams j{sums, run_counts, rest, sequences, int32_t(cut.clusters), num_experts, ctas, losses, counts,
+                       counted};
     if (ctas > 8) e = allow_16(balance_join_kernel);
     if (e == cudaSuccess) e = launch_dependent(balance_join_kernel, unsigned(ctas), 32 * kJoinWarps, 0, s, ctas, j);
   }
@@ -659,7 +662,7 @@ extern "C" int gmm_balance_loss_backward(const float* dlosses, const int32_t* co
   if (int st = require_device(nullptr)) return st;
   if (tokens == 0) return GMM_OK;
   // tokens of a warp: one while all warps fit the GPU at once
-  int64_t run = tokens / (152 * 6 * kBackWarps);
+  int64_t run = tokens / (kSms * 6 * kBackWarps);
   run = run < 1 ? 1 : run > 8 ? 8 : run;
   const BackParams p{dlosses, counts, counted, logits, tokens, logits_ld, tokens / sequences, num_experts, int32_t(run),
                      token_mask, dlogits};

@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     const unsigned spans = unsigned(p.spans) * (kSum ? (unsigned(items) + chunks - 1) / chunks : 1u);
     const unsigned units = unsigned(groups) * unsigned(min(p.tiles, 1 << 20)), teams = gridDim.x * unsigned(kWarps >> at);
     // (kItems: a CTA's range ends within an item, and in it)
-    const unsigned rounds = (units + teams - 1) / teams + (kMode == kItems ? 1 : 0), each = (spans + (1u << at) - 1) >> at;
+    const unsigned rounds = (units + teams - 1) / teams + (kMode == kItems ? 1 : 0);
+    const unsigned each = (spans + (1u << at) - 1) >> at;
     const unsigned total = unsigned(fminf(float(rounds) * float(each + 1), 2.5e8f));
     const unsigned cost = __reduce_min_sync(0xffffffffu, total * 8 + at);
     lg = int(cost % 8);
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   uint8_t* const ring = smem + warp * R::kBytes;
   const int lane_row = lane >> 4, lane_chunk = lane & 15;
   // where this lane's pieces of the next span go
-  const uint32_t fill_codes = smem_u32(ring) + lane_row * kPitch + lane_chunk * 16, fill_lane = smem_u32(ring) + lane * 16;
+  const uint32_t fill_codes = smem_u32(ring) + lane_row * kPitch + lane_chunk * 16;
+  const uint32_t fill_lane = smem_u32(ring) + lane * 16;
   uint32_t fill = 0;
   // the pairs of a unit that are this warp's: [begin, end) of its items' spans
   const int begin_one = int((int64_t(p.spans) * member) >> lg), end_one = int((int64_t(p.spans) * (member + 1)) >> lg);
@@ -448,11 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
     const uint8_t* at = p.codes + (e * p.n + lane_row) * pitch + int64_t(span) * (kSpan / 2) + lane_chunk * 16;
     code0 = at + row0 * pitch, code1 = at + row1 * pitch;
     const int64_t in_window = (e * p.windows + 2 * int64_t(span)) * p.n;
-    scale = p.scale + (in_window + int64_t(lane / (2 * kPieces)) * p.n + (lane / kPieces % 2 ? row1 : row0)) * (kEach * 2) +
-            lane % kPieces * 16;
-    if constexpr (kZero)
-      zero = p.zero + (in_window + int64_t(lane / (2 * kZeroPieces)) * p.n + (lane / kZeroPieces % 2 ? row1 : row0)) * kEach +
-             lane % kZeroPieces * 16;
+    const int64_t of_scales = in_window + int64_t(lane / (2 * kPieces)) * p.n + (lane / kPieces % 2 ? row1 : row0);
+    scale = p.scale + of_scales * (kEach * 2) + lane % kPieces * 16;
+    if constexpr (kZero) {
+      const int64_t of_zeros = in_window + int64_t(lane / (2 * kZeroPieces)) * p.n + (lane / kZeroPieces % 2 ? row1 : row0);
+      zero = p.zero + of_zeros * kEach + lane % kZeroPieces * 16;
+    }
   };
   auto enter = [&] {
     while (in_range(ahead)) {
@@ -543,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   };
   int last = -1;
   const uint8_t* const words = ring + g * kPitch + t4 * 4;  // this lane's words of a stage
-  const int scale_off = R::kScaleAt + g * kEach * 2 - g * kPitch - t4 * 4, zero_off = R::kZeroAt + g * kEach - g * kPitch - t4 * 4;
+  const int scale_off = R::kScaleAt + g * kEach * 2 - g * kPitch - t4 * 4;
+  const int zero_off = R::kZeroAt + g * kEach - g * kPitch - t4 * 4;
   int stage = 0;
   // two's complement + 8 is the top bit flipped
   const uint32_t mask_low = in_register(0x000F000Fu), mask_high = in_register(0x00F000F0u);
@@ -634,12 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             read_sums(quad);
           else if (quad < 3)
             read_sums(quad + 1);
-          if (quad % 2 == 0)
-            sa = reinterpret_cast<const Scales*>(scales)[8 * quad], sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
+          if (quad % 2 == 0) {
+            sa = reinterpret_cast<const Scales*>(scales)[8 * quad];
+            sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
+          }
 #pragma unroll
           for (int i = 0; i < kQuad; ++i) {
             const int at = quad % 2 * kQuad + i;  // in the window
-            const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2], pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
+            const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2];
+            const uint32_t pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
                   __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0[quad % 2])[i],
                   reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) {
@@ -754,7 +761,9 @@ __global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
 constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * kWarps * 16 * (kCols + 1);
 
 // Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the groups' sums, the roots.
-int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) { return rows * (pitch * 2 + sums_pitch(k, group) * 4 + 4); }
+int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) {
+  return rows * (pitch * 2 + sums_pitch(k, group) * 4 + 4);
+}
 // In shared memory rows are half a line of banks apart.
 int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
 // Rows that fit the shared memory.
@@ -772,8 +781,10 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
   auto kern = matvec_kernel<kGroup, kZero, kGated, kSum, kMode>;
   // for every launch: the attribute is the current device's, and one size for all calls
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
-  if (kMode != kAll)
-    if (cudaError_t e = launch_dependent(make_ready_kernel<kGroup, kZero>, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
+  if constexpr (kMode != kAll) {
+    auto first = make_ready_kernel<kGroup, kZero>;
+    if (cudaError_t e = launch_dependent(first, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
+  }
   return launch_dependent(kern, unsigned(sms), kThreads, smem, stream, 1, p);
 }
 

@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_int4_kernel(DequantParams
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t raw = (code >> (4 * i) & 0x000F000Fu) ^ (kZero ? 0x43004300u : 0x43084308u);
-        const __nv_bfloat162 v = __hsub2(reinterpret_cast<const __nv_bfloat162&>(raw), reinterpret_cast<const __nv_bfloat162&>(off));
+        const __nv_bfloat162 v =
+            __hsub2(reinterpret_cast<const __nv_bfloat162&>(raw), reinterpret_cast<const __nv_bfloat162&>(off));
         n[i] = reinterpret_cast<const uint32_t&>(v);
       }
       T* to = out + w * kWindow;

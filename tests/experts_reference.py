@@ -63,7 +63,8 @@ def balance_gradient(dlosses, logits, parts, N, score):
     b = dlosses[1] * 2.0 / max(N, 1) * lse[:, None] * soft
     of = live[:, None]
     return (np.where(of, a * (f - mean) + b, 0.0),
-            np.where(of, np.abs(a) * (f + mean) + np.abs(dlosses[1] * 2.0 / max(N, 1) * soft) * (np.abs(lse) + 1)[:, None], 0.0))
+            np.where(of, np.abs(a) * (f + mean)
+                     + np.abs(dlosses[1] * 2.0 / max(N, 1) * soft) * (np.abs(lse) + 1)[:, None], 0.0))
 
 
 # ---------------------------------------------------------------- the activation
@@ -165,7 +166,8 @@ def matvec(x, w, experts, weights=None, kind=None, sizes=None):
         a, slope, arg, slopes = act(h[..., :f], kind)
         u = h[..., f:]
         # what an error of `size` units in either half moves the product by, and the activation's own
-        size = np.abs(slope) * size[..., :f] * np.abs(u) + np.abs(a) * size[..., f:] + (16 + 8 * np.abs(arg)) * np.abs(a * u)
+        own = (16 + 8 * np.abs(arg)) * np.abs(a * u)
+        size = np.abs(slope) * size[..., :f] * np.abs(u) + np.abs(a) * size[..., f:] + own
         h = a * u
     if weights is not None:
         h, size = (h * weights[..., None]).sum(1), (size * np.abs(weights)[..., None]).sum(1)
