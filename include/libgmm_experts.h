@@ -114,17 +114,16 @@ size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t group, int ha
  * Products of few tokens with the 4-bit weights of the experts that each chose, in the
  * order of the tokens (no sort):
  *   h[t, j] = W(experts[t, j]) x[t, j]
- *           = sum over groups of scale * (sum of code x - zero * sum of x)
- *             (codes 0 .. 15, two's complement ones counted from -8 with zero 8; exact products
- *             and fp32 sums)
+ *           = sum over groups of scale * sum of (code - zero) x
+ *             (exact differences and products, fp32 sums)
  *   y[t, j] = h[t, j], or with act: act(first half of h[t, j]) * second half
  *   out[t, j] = y[t, j], or with weights: out[t] = sum over j of weights[t, j] * y[t, j]
  * rounded once to out_dtype.  A slot whose expert is outside [0, num_experts) gives zeros,
  * and nothing to a sum.  Each expert's weights are read once for every 8 of its tokens (for
  * every 8 tokens, with weights), so this is for the few rows an expert has in decoding; gmm()
  * is for more.  The same inputs give the same bits.  A row of x with an infinity or NaN gives NaN.
- * Products of scales below 2^-110 lose bits as subnormals, and so does x below 2^-242 of its row's
- * largest value.
+ * Sums are held to at least 2^-129 of the row's largest |x|: terms below 2^-105 of it lose bits, before
+ * or after their scale.
  *
  *   x        BF16 [tokens, k] with row pitch x_ld (x_per_slot 0: all slots of a token share
  *            it) or dense [tokens, topk, k] (x_per_slot 1; x_ld is not used)

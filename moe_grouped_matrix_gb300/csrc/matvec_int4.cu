@@ -5,22 +5,26 @@
 // Bound by memory: half a byte a weight, read once.  At 6.8 TB/s an SM gets some 47 weights a cycle and
 // may spend 2.7 issue slots of a lane on each; one fp32 multiply-add with its conversion takes about 2 for a
 // single token.  So the sums run on mma.sync m16n8k16, 16 weight rows by 8 columns (tcgen05 wants its
-// operands written to shared memory in 8 or 16 bits first, four times the bytes, for 128 rows at least),
-// with operands that cost next to nothing: a bit pattern below 256 is, read as bf16, that whole number times
-// 2^-133 (subnormals, and the first binade above them, whose spacing is the same; the instruction takes
-// subnormals as they are), so a mask takes two codes out of a word, at its bits 0-3 and 16-19 or, 16 times
-// as large, at 4-7 and 20-23: five instructions for eight weights and all their columns.  Subtracting the
-// zero point there, exactly, took eleven, and the products of one token 34 us for 23.
+// operands written to shared memory in 8 or 16 bits first, four times the bytes, for 128 rows at least).
+// A bit pattern below 256 is, read as bf16, that whole number times 2^-133 (subnormals, and the first binade
+// above them, whose spacing is the same), so a mask takes two codes out of a word, at its bits 0-3 and 16-19 or,
+// 16 times as large, at 4-7 and 20-23, and one packed multiply-add makes both 2^-110 (code - zero), exactly
+// (two's complement codes have their top bit flipped, which adds 8, and 8 is their zero point): nine
+// instructions for eight weights and all their columns.
 //
-// The other operand is x times a power of two that brings each row's largest value to 2^116 or 2^117,
-// exactly (what lies 2^242 below the largest is lost), divided by 16 where the codes are 16 times as large.
-// Products are exact, sums fp32.  Codes are not negative there (two's complement ones have their top bit
-// flipped, which adds 8), and -8 (or -zero) times the group's sum of x, computed once for each row, is added
-// to each group's sum: the terms of a sum are then up to |code| + 8 and 8 times |x| instead of |code - 8|
-// times, some units of fp32 more of error.  A row with an infinity or NaN gives NaN; scales below 2^-110
-// lose bits, as their products with sums of 2^-17 of x are subnormal.  A group's sum is scaled in fp32, and the
-// power of two taken off the result.  A matrix instruction's k are a set without an order, so a lane takes the
-// eight k of a 32-bit word for its own, and x is permuted alike.
+// Both halves of that are for the sums' precision.  Codes from 0 up, their zero points taken off through sums of
+// x, took five instructions, and with a channel of x 1000 times the others that meets weights of 0 the result
+// was off by up to 5e-6 of its size; it is by 1e-7, as in fp32 products.  And codes left subnormal had the matrix
+// instruction cut its sums off at 2^-17 of their largest term, as it lines products up by their operands'
+// exponents, which say 2^-126 for all subnormals.  1 token, 2 of 8 experts of 28672 x 4096: groups of 128 25.5 us
+// for 23.0 without either, of 32 26.3 for 26.2.
+//
+// The other operand is x times a power of two that brings each row's largest value to between 2^90 and 2^92.
+// Products are exact, sums fp32, whose least number is then at most 2^-129 of the row's largest |x|: terms
+// below 2^-105 of it lose bits, before or after their scale.  A row with an infinity or NaN gives NaN, by the
+// factor that takes its results to their size.  A group's sum is scaled in fp32, and the power of two taken off
+// the result.  A matrix instruction's k are a set without an order, so a lane takes the eight k of a 32-bit
+// word for its own, and x is permuted alike.
 //
 // A warp streams spans of 16 rows by 512 k through two stages of its own in shared memory, by asynchronous
 // copies that only it waits for, whole lines of each row.  Teams of 1 to 16 warps share a tile along k: few
@@ -75,9 +79,8 @@ struct Params {
   int32_t out_n, out_f32;  // columns of out, its type
   int32_t x_rows, x_pitch;  // rows of x made ready, and elements between them
   int32_t item_columns, item_pitch;  // kItems: most columns of an item, elements between them in shared memory
-  // where not in shared memory: the rows, their groups' sums, and what takes their results to their size
+  // where not in shared memory: the rows, and what takes their results to their size
   __nv_bfloat16* ready;
-  float* sums;
   float* roots;
 };
 
@@ -104,6 +107,12 @@ __device__ __forceinline__ uint32_t in_register(uint32_t v) {
   asm volatile("" : "+r"(v));
   return v;
 }
+// a b + c of two bf16 each; a subnormal is taken as it is.
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 
 // c += A B, or c = A B.
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -120,60 +129,47 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kTop = 116;                  // rows' largest values are brought to 2^116
+constexpr int kTop = 91;         // rows' largest values are brought to between 2^90 and 2^92
+constexpr int kNotFinite = 129;  // in the place of the power of a row with an infinity or NaN
 
 // Rows of x are made ready by windows, a warp each, 8 values a lane (zeros past k).
 __device__ __forceinline__ uint4 window_of(const __nv_bfloat16* x, int k, int window) {
   const int c = window * kWindow + (threadIdx.x & 31) * 8;
   return c < k ? __ldg(reinterpret_cast<const uint4*>(x + c)) : make_uint4(0, 0, 0, 0);
 }
-// The largest finite magnitude of a lane's values.
+// The largest magnitude of a lane's values, as its bits: infinities and NaN above the numbers.
 __device__ __forceinline__ uint32_t largest(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-    if (lo < 0x7F80u) m = max(m, lo);
-    if (hi < 0x7F80u) m = max(m, hi);
-  }
-  return m;
+  const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+  const uint32_t m = __vmaxu2(a, b);
+  return max(m & 0xFFFFu, m >> 16);
 }
 // The power of two that a row's largest value, of these n, has or, if that is even, the next.
 __device__ __forceinline__ int power_of(const uint32_t* tops, int n) {
   uint32_t top = 0;
   for (int i = threadIdx.x & 31; i < n; i += 32) top = max(top, tops[i]);
   top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= 0x7F80u) return kNotFinite;
   return (top == 0 ? 0 : top < 0x80u ? 31 - __clz(int(top)) - 133 : int(top >> 7) - 127) | 1;
 }
-// The root of what takes a result to its own size: 2^(133 - kTop + power).
-__device__ __forceinline__ float root_of(int power) { return __int_as_float((127 + (133 - kTop + power) / 2) << 23); }
-// A window of the row: x 2^(kTop - power) as bf16, in each 8 in the order of the masks, 0 4 1 5 2 6 3 7,
-// the odd ones over 16; and -8 (kZero: -1) times the groups' sums times 2^-133.
-template <int kGroup, bool kZero>
-__device__ __forceinline__ void make_ready(const uint4& v, int k, int window, int power, __nv_bfloat16* to, float* sums) {
-  const int lane = threadIdx.x & 31, c = window * kWindow + lane * 8;
-  const int up = kTop - power, first = up / 2;  // up to 249: in two steps, each exact
+// The root of what takes a result to its own size: 2^(110 - kTop + power), or NaN.
+__device__ __forceinline__ float root_of(int power) {
+  return __int_as_float(power == kNotFinite ? 0x7FC00000 : (127 + (110 - kTop + power) / 2) << 23);
+}
+// A window of the row: x 2^(kTop - power) as bf16, in each 8 in the order of the masks, 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ void make_ready(const uint4& v, int k, int window, int power, __nv_bfloat16* to) {
+  const int c = window * kWindow + (threadIdx.x & 31) * 8;
+  if (c >= k) return;
+  const int up = kTop - power, first = up / 2;  // up to 224: in two steps, each exact
   const float u0 = __int_as_float((127 + first) << 23), u1 = __int_as_float((127 + up - first) << 23);
-  float sum = 0.f;
-  if (c < k) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) * u0 * u1;
-      sum += f[i];
-      if (i % 2) f[i] *= 0.0625f;
-    }
-    uint32_t out[4];
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) * u0 * u1;
+  uint32_t out[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      out[i] = __float_as_uint(f[i]) >> 16 | (__float_as_uint(f[i + 4]) & 0xFFFF0000u);
-    *reinterpret_cast<uint4*>(to + c) = make_uint4(out[0], out[1], out[2], out[3]);
-  }
-#pragma unroll
-  for (int d = 1; d < kGroup / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane % (kGroup / 8) == 0 && c < k) sums[c / kGroup] = sum * (kZero ? -0x1p-100f : -0x1p-97f) * 0x1p-33f;
+  for (int i = 0; i < 4; ++i)
+    out[i] = __float_as_uint(f[i]) >> 16 | (__float_as_uint(f[i + 4]) & 0xFFFF0000u);
+  *reinterpret_cast<uint4*>(to + c) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // A warp's two stages: codes, scales, zero points of a span.  Rows of codes are a 16-byte piece apart
@@ -211,9 +207,6 @@ struct Unit {
   }
 };
 
-// Groups' sums of a row of x: rows of whole 16 bytes.
-__host__ __device__ constexpr int64_t sums_pitch(int64_t k, int group) { return (k / group + 3) / 4 * 4; }
-
 template <bool kShared, class T>
 __device__ __forceinline__ T load(const T* p) {
   if constexpr (kShared)
@@ -238,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   griddep_begin();
   p.x = after_begin(p.x), p.codes = after_begin(p.codes), p.scale = after_begin(p.scale);
   p.zero = after_begin(p.zero), p.chosen = after_begin(p.chosen), p.weights = after_begin(p.weights);
-  p.ready = after_begin(p.ready), p.sums = after_begin(p.sums), p.roots = after_begin(p.roots);
+  p.ready = after_begin(p.ready), p.roots = after_begin(p.roots);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Table table;
   __shared__ float part[kWarps][16][kCols + 1];
@@ -521,17 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   fetch();
 
   // rows of x made ready: in shared memory, or by the kernel ahead
-  const int x_groups = sums_pitch(p.k, kGroup);
   const __nv_bfloat16* ready = p.ready;
-  const float* sums = p.sums;
   const float* roots = p.roots;
   if constexpr (kStaged) {
-    auto* to_sums = reinterpret_cast<float*>(staged + p.x_rows * p.x_pitch);
-    float* to_roots = to_sums + p.x_rows * x_groups;
-    ready = staged, sums = to_sums, roots = to_roots;
+    auto* to_roots = reinterpret_cast<float*>(staged + p.x_rows * p.x_pitch);
+    ready = staged, roots = to_roots;
     each_window([&](int row, int w, __nv_bfloat16* at) {
       const uint4 v = w * kWindow + lane * 8 < p.k ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
-      make_ready<kGroup, kZero>(v, p.k, w, table.power[row], staged + row * p.x_pitch, to_sums + row * x_groups);
+      make_ready(v, p.k, w, table.power[row], staged + row * p.x_pitch);
     });
     if (tid < p.x_rows) to_roots[tid] = root_of(table.power[tid]);
     __syncthreads();
@@ -552,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   // two's complement + 8 is the top bit flipped
   const uint32_t mask_low = in_register(0x000F000Fu), mask_high = in_register(0x00F000F0u);
   const uint32_t flip_low = in_register(0x00080008u), flip_high = in_register(0x00800080u);
-  const __nv_bfloat16* xp = nullptr;                // column g of the last item, from this lane's k on
-  const float *sums0 = nullptr, *sums1 = nullptr;   // of columns 2 t4 and 2 t4 + 1
+  const uint32_t up_low = in_register(0x4B004B00u), up_high = in_register(0x49004900u);  // 2^23, 2^19
+  const __nv_bfloat16* xp = nullptr;  // column g of the last item, from this lane's k on
   float w0 = 0.f, w1 = 0.f, root0 = 0.f, root1 = 0.f;
   bool has0 = false, has1 = false;
   auto work = [&] {  // on the unit here
@@ -567,46 +557,43 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         // a column without a slot takes the head's x: nothing of it is used
         const int s = table.slot[now][g], s0 = table.slot[now][2 * t4], s1 = table.slot[now][2 * t4 + 1];
         has0 = s0 >= 0, has1 = s1 >= 0;
-        int r, r0, r1;  // the columns' rows of x: of the item's, or of all
-        if constexpr (kMode == kItems) {
-          r = s < 0 ? 0 : g, r0 = has0 ? 2 * t4 : 0, r1 = has1 ? 2 * t4 + 1 : 0;
-        } else {
-          const int head = table.row[table.head[now]];
-          r = s < 0 ? head : table.row[s], r0 = has0 ? table.row[s0] : head, r1 = has1 ? table.row[s1] : head;
-        }
+        const int head = table.row[table.head[now]];
+        // column g's row of x: of the item's, or of all
+        const int r = kMode == kItems ? (s < 0 ? 0 : g) : s < 0 ? head : table.row[s];
         xp = ready + int64_t(r) * (kMode == kItems ? p.item_pitch : p.x_pitch) + t4 * 8;
-        sums0 = sums + int64_t(r0) * x_groups, sums1 = sums + int64_t(r1) * x_groups;
         if constexpr (kSum) {
           w0 = has0 ? p.weights[s0] : 0.f, w1 = has1 ? p.weights[s1] : 0.f;
-          root0 = roots[r0], root1 = roots[r1];
+          root0 = roots[has0 ? table.row[s0] : head], root1 = roots[has1 ? table.row[s1] : head];
         }
       }
       const int k0 = w * kSpan;
       const __nv_bfloat16* xk = xp + k0;
       // x of the next two chunks is read ahead of its use, where it may come from the L2
       constexpr int kQuad = 128 / kGroup;  // groups of four chunks
-      using Sums = std::conditional_t<kQuad == 1, float, std::conditional_t<kQuad == 2, float2, float4>>;
       uint4 b[2][2];
-      const float *sums0k = sums0 + w * (2 * kEach), *sums1k = sums1 + w * (2 * kEach);
       auto read_x = [&](int pair) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           b[pair % 2][i] = load<kShared>(reinterpret_cast<const uint4*>(xk + (pair * 2 + i) * 32));
       };
-      Sums n0[2], n1[2];
-      auto read_sums = [&](int quad) {
-        n0[quad % 2] = load<kShared>(reinterpret_cast<const Sums*>(sums0k) + quad);
-        n1[quad % 2] = load<kShared>(reinterpret_cast<const Sums*>(sums1k) + quad);
-      };
       const bool full = k0 + kSpan <= p.k;
-      if (!kShared && full) read_x(0), read_sums(0);
+      if (!kShared && full) read_x(0);
       copies_wait<0>();
       __syncwarp();
       fetch();
       const uint8_t *codes = words + stage, *scales = codes + scale_off, *zeros = codes + zero_off;
       stage = R::kStage - stage;
+      constexpr uint32_t kEight = 0x8A008A00u;  // -2^-110 times 8
+      auto off_of = [&](uint32_t z) { return fma2(z, 0xCB00CB00u, 0); };
       // one group, its chunks' x given by `x_of`
-      auto group = [&](int q, float s0, float s1, float n0, float n1, auto x_of) {
+      // (z0, z1: -2^-110 times the zero points of rows g and g + 8, twice each)
+      auto group = [&](int q, float s0, float s1, uint32_t z0, uint32_t z1, auto x_of) {
+        auto low = [&](uint32_t v, uint32_t z) {
+          return fma2(kZero ? v & mask_low : masked(v, mask_low, flip_low), up_low, z);
+        };
+        auto high = [&](uint32_t v, uint32_t z) {
+          return fma2(kZero ? v & mask_high : masked(v, mask_high, flip_high), up_high, z);
+        };
         float c[4];
 #pragma unroll
         for (int j = 0; j < kGroup / 32; ++j) {
@@ -614,17 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
           const uint4 v = x_of(chunk);
           const uint32_t wa = *reinterpret_cast<const uint32_t*>(codes + chunk * 16), va = wa >> 8;
           const uint32_t wb = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + chunk * 16), vb = wb >> 8;
-          auto low = [&](uint32_t v) { return kZero ? v & 0x000F000Fu : masked(v, mask_low, flip_low); };
-          auto high = [&](uint32_t v) { return kZero ? v & 0x00F000F0u : masked(v, mask_high, flip_high); };
-          mma(c, low(wa), low(wb), high(wa), high(wb), v.x, v.y, j == 0);
-          mma(c, low(va), low(vb), high(va), high(vb), v.z, v.w, false);
-        }
-        if constexpr (kZero) {
-          const int zq = q / kEach * (16 * kEach) + q % kEach;
-          const float z0 = float(zeros[zq]), z1 = float(zeros[8 * kEach + zq]);
-          c[0] = fmaf(z0, n0, c[0]), c[1] = fmaf(z0, n1, c[1]), c[2] = fmaf(z1, n0, c[2]), c[3] = fmaf(z1, n1, c[3]);
-        } else {
-          c[0] += n0, c[1] += n1, c[2] += n0, c[3] += n1;
+          mma(c, low(wa, z0), low(wb, z1), high(wa, z0), high(wb, z1), v.x, v.y, j == 0);
+          mma(c, low(va, z0), low(vb, z1), high(va, z0), high(vb, z1), v.z, v.w, false);
         }
         acc[0] = fmaf(s0, c[0], acc[0]), acc[1] = fmaf(s0, c[1], acc[1]);
         acc[2] = fmaf(s1, c[2], acc[2]), acc[3] = fmaf(s1, c[3], acc[3]);
@@ -632,15 +610,23 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
       if (full) {
         using Scales = std::conditional_t<kEach == 2, uint32_t, std::conditional_t<kEach == 4, uint2, uint4>>;
         Scales sa, sb;
+        using Zeros = std::conditional_t<kEach == 2, uint16_t, std::conditional_t<kEach == 4, uint32_t, uint2>>;
+        uint32_t za[2] = {0, 0}, zb[2] = {0, 0};
+        auto zeros_of = [](uint32_t (&z)[2], const Zeros& v) {
+          if constexpr (kEach == 8)
+            z[0] = v.x, z[1] = v.y;
+          else
+            z[0] = v;
+        };
 #pragma unroll
         for (int quad = 0; quad < 4; ++quad) {
-          if constexpr (kShared)
-            read_sums(quad);
-          else if (quad < 3)
-            read_sums(quad + 1);
           if (quad % 2 == 0) {
             sa = reinterpret_cast<const Scales*>(scales)[8 * quad];
             sb = reinterpret_cast<const Scales*>(scales)[8 * quad + 8];
+            if constexpr (kZero) {
+              zeros_of(za, reinterpret_cast<const Zeros*>(zeros)[8 * quad]);
+              zeros_of(zb, reinterpret_cast<const Zeros*>(zeros)[8 * quad + 8]);
+            }
           }
 #pragma unroll
           for (int i = 0; i < kQuad; ++i) {
@@ -648,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
             const uint32_t pa = reinterpret_cast<const uint32_t*>(&sa)[at / 2];
             const uint32_t pb = reinterpret_cast<const uint32_t*>(&sb)[at / 2];
             group(quad * kQuad + i, __uint_as_float(at % 2 ? pa & 0xFFFF0000u : pa << 16),
-                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16), reinterpret_cast<const float*>(&n0[quad % 2])[i],
-                  reinterpret_cast<const float*>(&n1[quad % 2])[i], [&](int chunk) {
+                  __uint_as_float(at % 2 ? pb & 0xFFFF0000u : pb << 16),
+                  kZero ? off_of(__byte_perm(za[at / 4], 0, 0x4040u + at % 4 * 0x0101u)) : kEight,
+                  kZero ? off_of(__byte_perm(zb[at / 4], 0, 0x4040u + at % 4 * 0x0101u)) : kEight, [&](int chunk) {
                     if constexpr (kShared) return load<true>(reinterpret_cast<const uint4*>(xk + chunk * 32));
                     if (chunk % 2 == 0 && chunk < 14) read_x(chunk / 2 + 1);
                     return b[chunk / 2 % 2][chunk % 2];
@@ -662,8 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 #pragma unroll 1
         for (int q = 0; q < left; ++q) {
           const int sq = q / kEach * (16 * kEach) + q % kEach;
-          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]), load<kShared>(sums0k + q),
-                load<kShared>(sums1k + q),
+          uint32_t z0 = kEight, z1 = kEight;
+          if constexpr (kZero) z0 = off_of(zeros[sq] * 0x00010001u), z1 = off_of(zeros[8 * kEach + sq] * 0x00010001u);
+          group(q, __bfloat162float(one[sq]), __bfloat162float(one[8 * kEach + sq]), z0, z1,
                 [&](int chunk) { return load<kShared>(reinterpret_cast<const uint4*>(xk + chunk * 32)); });
         }
       }
@@ -711,9 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
   };
   if constexpr (kMode == kItems) {
     auto* rows = reinterpret_cast<__nv_bfloat16*>(smem + kWarps * R::kBytes);
-    float* row_sums = reinterpret_cast<float*>(rows + p.item_columns * p.item_pitch);
-    const int eights = p.k / 8, fours = x_groups / 4;
-    ready = rows, sums = row_sums;
+    const int eights = p.k / 8;
+    ready = rows;
     for (int group = first_group; group <= last_group && (group < last_group || last_tiles > 0); ++group) {
       __syncthreads();  // the last item's x has been read
       const int columns = table.columns[group];
@@ -721,8 +708,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
         const int64_t row = table.row[table.slot[group][c]];
         for (int i = tid; i < eights; i += kThreads)
           copy16(smem_u32(rows + c * p.item_pitch + i * 8), p.ready + row * p.x_pitch + i * 8);
-        for (int i = tid; i < fours; i += kThreads)
-          copy16(smem_u32(row_sums + c * x_groups + i * 4), p.sums + row * x_groups + i * 4);
       }
       copies_commit();
       copies_wait<0>();
@@ -737,7 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(Params p) {
 }
 
 // Rows of x made ready where a CTA's shared memory does not hold them: a CTA a row.
-template <int kGroup, bool kZero>
 __global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
   griddep_begin();
   p.x = after_begin(p.x);
@@ -753,23 +737,20 @@ __global__ void __launch_bounds__(kThreads) make_ready_kernel(Params p) {
   const int power = power_of(tops, kWarps);
 #pragma unroll 4
   for (int w = warp; w < p.windows; w += kWarps)
-    make_ready<kGroup, kZero>(window_of(x, p.k, w), p.k, w, power, p.ready + int64_t(row) * p.x_pitch,
-                              p.sums + int64_t(row) * sums_pitch(p.k, kGroup));
+    make_ready(window_of(x, p.k, w), p.k, w, power, p.ready + int64_t(row) * p.x_pitch);
   if (threadIdx.x == 0) p.roots[row] = root_of(power);
 }
 
 constexpr size_t kMaxShared = 227 * 1024 - 256 - sizeof(Table) - sizeof(float) * kWarps * 16 * (kCols + 1);
 
-// Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the groups' sums, the roots.
-int64_t ready_bytes(int64_t rows, int64_t pitch, int64_t k, int group) {
-  return rows * (pitch * 2 + sums_pitch(k, group) * 4 + 4);
-}
+// Bytes of `rows` rows of x made ready, `pitch` elements apart: the values, the roots.
+int64_t ready_bytes(int64_t rows, int64_t pitch) { return rows * (pitch * 2 + 4); }
 // In shared memory rows are half a line of banks apart.
 int64_t staged_pitch(int64_t k) { return k % 64 == 0 ? k + 32 : k; }
 // Rows that fit the shared memory.
 int64_t staged_rows(int64_t k, int group, bool zero) {
   const int64_t each = kWindow / group, ring = int64_t(kWarps) * 2 * (16 * kPitch + 2 * 16 * each * (zero ? 3 : 2));
-  return (int64_t(kMaxShared) - ring) / ready_bytes(1, staged_pitch(k), k, group);
+  return (int64_t(kMaxShared) - ring) / ready_bytes(1, staged_pitch(k));
 }
 int64_t launch_tokens(int64_t topk) { return kMaxSlots / topk / kCols * kCols; }
 
@@ -777,14 +758,12 @@ template <int kGroup, bool kZero, bool kGated, bool kSum, Mode kMode>
 cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
   using R = Ring<kGroup, kZero>;
   const int64_t rows = kMode == kAll ? p.x_rows : kMode == kItems ? p.item_columns : 0;
-  const size_t smem = size_t(kWarps) * R::kBytes + size_t(ready_bytes(rows, staged_pitch(p.k), p.k, kGroup));
+  const size_t smem = size_t(kWarps) * R::kBytes + size_t(ready_bytes(rows, staged_pitch(p.k)));
   auto kern = matvec_kernel<kGroup, kZero, kGated, kSum, kMode>;
   // for every launch: the attribute is the current device's, and one size for all calls
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxShared))) return e;
-  if constexpr (kMode != kAll) {
-    auto first = make_ready_kernel<kGroup, kZero>;
-    if (cudaError_t e = launch_dependent(first, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
-  }
+  if constexpr (kMode != kAll)
+    if (cudaError_t e = launch_dependent(make_ready_kernel, unsigned(p.x_rows), kThreads, 0, stream, 1, p)) return e;
   return launch_dependent(kern, unsigned(sms), kThreads, smem, stream, 1, p);
 }
 
@@ -835,7 +814,8 @@ extern "C" size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t gr
   const int64_t most = launch_tokens(topk), count = tokens < most ? tokens : most;
   const int64_t rows = x_per_slot != 0 ? count * topk : count;
   // a last launch of fewer tokens may not need what the others do
-  return rows <= staged_rows(k, group, has_zero != 0) ? 0 : size_t(ready_bytes(rows, k, k, group));
+  // the size it has had: four more bytes for each group of a row than are used
+  return rows <= staged_rows(k, group, has_zero != 0) ? 0 : size_t(ready_bytes(rows, k) + rows * ((k / group + 3) / 4 * 16));
 }
 
 extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t x_ld, int x_per_slot, const void* codes,
@@ -881,8 +861,7 @@ extern "C" int gmm_matvec_int4(const void* x, int64_t tokens, int64_t k, int64_t
     p.x_pitch = int32_t(staged ? staged_pitch(k) : k);
     if (!staged) {
       p.ready = static_cast<__nv_bfloat16*>(scratch);
-      p.sums = reinterpret_cast<float*>(p.ready + int64_t(p.x_rows) * k);
-      p.roots = p.sums + int64_t(p.x_rows) * sums_pitch(k, group);
+      p.roots = reinterpret_cast<float*>(p.ready + int64_t(p.x_rows) * k);
     }
     const int64_t first = t0 * (weights != nullptr ? 1 : topk) * out_n;
     p.out = static_cast<char*>(out) + first * (out_dtype == GMM_DTYPE_F32 ? 4 : 2);
