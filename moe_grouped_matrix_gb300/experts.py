@@ -263,9 +263,14 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
     topk, n / 2] (n a multiple of 16); with weights float32 [tokens, topk] the sum over j of
     weights[t, j] h[t, j], [tokens, n].  Slots outside [0, E) are zeros, and nothing to a sum.
     Without experts w is one matrix [n, k] and h is [tokens, n].  Sums are fp32, rounded once to
-    out_dtype (bfloat16 or float32); a row of x with an infinity or NaN gives NaN.  Weights are read
-    once for every 8 tokens of an expert (with weights, for every 8 tokens): for more than a few,
-    sort the rows and use gmm()."""
+    out_dtype (bfloat16 or float32); a row of x with an infinity or NaN gives NaN.
+
+    Weights are read once for every 8 tokens of an expert (with weights, for every 8 tokens), which
+    pays up to some 4 to 8 tokens an expert; past that, sort the rows and use gmm().  It takes the
+    codes of groups of 128 without zero points as they are,
+        scale = w.scale.transpose(2, 3).flatten(1, 2)[:, :k // 128, None].float().contiguous()  # once
+        gmm(rows, w.codes, sizes, scale, rhs_format="int4")
+    and others as dequantize_int4(w)."""
     if stream is None and experts is not None:
         got = (_moe._calls or _moe._bind()).matvec_int4(x, w.codes, w.scale, w.zero, w.group, experts, weights,
                                                         0 if act is None else ACTS.get(act), _OUT_F32.get(out_dtype))
