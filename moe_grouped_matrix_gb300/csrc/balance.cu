@@ -32,7 +32,9 @@ namespace gmmk {
 namespace {
 
 constexpr int kWarps = 16, kBackWarps = 8;
-constexpr int kSms = 152;  // of a GB300
+// CTAs that a forward pass is cut into, about: two for each SM of a GB300.  A constant, as the size of the scratch,
+// which is asked for without a device, follows from it.
+constexpr int kCtas = 304;
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -527,7 +529,7 @@ struct Cut {
   int ctas;
   int64_t clusters, run;
 };
-// A CTA has two tokens for each of its warps; all of them are about two for each SM, or one cluster where its
+// A CTA has two tokens for each of its warps; all of them are about kCtas, or one cluster where its
 // warps have at most eight (512 tokens 5.3 us, in two kernels 6.9; 1024: 5.8 and 8.0; 2048: 8.0 and 8.6; 4096:
 // 12.0 and 9.8).
 Cut cut_of(int64_t tokens, int64_t sequences) {
@@ -535,7 +537,7 @@ Cut cut_of(int64_t tokens, int64_t sequences) {
   Cut c{1, 1, per > 0 ? per : 1};
   if (per == 0) return c;
   const int64_t wanted = (per + 2 * kWarps - 1) / (2 * kWarps);  // CTAs of a sequence, were there no others
-  const int64_t share = sequences < 2 * kSms ? 2 * kSms / sequences : 1;
+  const int64_t share = sequences < kCtas ? kCtas / sequences : 1;
   int64_t ctas = wanted < share ? wanted : share;
   if (sequences == 1 && tokens <= 8 * kWarps * kMaxCtas && ctas > kMaxCtas) ctas = kMaxCtas;
   c.ctas = sequences == 1 && ctas == kMaxCtas ? kMaxCtas : ctas >= 8 ? 8 : ctas >= 4 ? 4 : ctas >= 2 ? 2 : 1;
@@ -659,10 +661,11 @@ extern "C" int gmm_balance_loss_backward(const float* dlosses, const int32_t* co
   if (misaligned(dlosses, 4) || misaligned(counts, 4) || misaligned(counted, 4) ||
       misaligned(dlogits, logits_dtype == GMM_DTYPE_F32 ? 4 : 2))
     return GMM_ERR_ALIGN;
-  if (int st = require_device(nullptr)) return st;
+  int sms = 0;
+  if (int st = require_device(&sms)) return st;
   if (tokens == 0) return GMM_OK;
   // tokens of a warp: one while all warps fit the GPU at once
-  int64_t run = tokens / (kSms * 6 * kBackWarps);
+  int64_t run = tokens / (int64_t(sms) * 6 * kBackWarps);
   run = run < 1 ? 1 : run > 8 ? 8 : run;
   const BackParams p{dlosses, counts, counted, logits, tokens, logits_ld, tokens / sequences, num_experts, int32_t(run),
                      token_mask, dlogits};
