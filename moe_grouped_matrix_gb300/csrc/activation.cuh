@@ -15,8 +15,8 @@ __device__ __forceinline__ float act_inner(float g) {
   return kAct == GMM_ACT_SILU ? g : kGeluTwice * (g + kGeluCube * g * g * g);
 }
 
-// kFast: for results in bf16, an exponential and a quotient of few instructions, off by (2 + |x|) and 2
-// units of 2^-23.
+// kFast: for results in bf16, an exponential and a quotient of few instructions, off by 2 + |1.173 x| and 2
+// units of their last place (CUDA's bounds): 2^-15 at exp(-90), for bf16's half step of 2^-9.
 template <bool kFast>
 __device__ __forceinline__ float act_exp(float x) {
   return kFast ? __expf(x) : expf(x);
