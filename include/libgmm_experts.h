@@ -120,12 +120,13 @@ size_t gmm_matvec_scratch_bytes(int64_t tokens, int64_t k, int32_t group, int ha
  *   out[t, j] = y[t, j], or with weights: out[t] = sum over j of weights[t, j] * y[t, j]
  * rounded once to out_dtype.  A slot whose expert is outside [0, num_experts) gives zeros,
  * and nothing to a sum.  Each expert's weights are read once for every 8 of its tokens (for
- * every 8 tokens, with weights), so this is for the few rows an expert has in decoding, some 4
+ * every 8 tokens, with weights), so this is for the few rows an expert has in decoding, some 3
  * to 8 at most.  For more, gmm() takes the codes of groups of 128 without zero points as GMM_DTYPE_INT4
  * weights, with rhs_scale [num_experts, k / 128, 1, n] the scales in f32; other groups, and zero
- * points, it takes as gmm_dequantize_int4()'s bf16 values.  The same inputs give the same bits.  A row of x with an infinity or NaN gives NaN.
- * Sums are held to at least 2^-129 of the row's largest |x|: terms below 2^-105 of it lose bits, before
- * or after their scale.
+ * points, it takes as gmm_dequantize_int4()'s bf16 values.
+ * The same inputs give the same bits.  A row of x with an infinity or NaN gives NaN.  Sums are held to
+ * at least 2^-129 of the row's largest |x|: terms below 2^-105 of it lose bits, before or after their
+ * scale.
  *
  *   x        BF16 [tokens, k] with row pitch x_ld (x_per_slot 0: all slots of a token share
  *            it) or dense [tokens, topk, k] (x_per_slot 1; x_ld is not used)

@@ -17,8 +17,9 @@
 //
 // Bound by latency: 192 tokens, 2 of 8 experts 4.8 us and the gradient 2.1; 4096 tokens, 8
 // of 128 experts 9.8 us (the first kernel 6.4, of which 2 to 4 are the tokens, the join 3)
-// and 3.1 for 1 MB of logits; 16384 tokens of 250 f32 logits in 16 sequences, sigmoid
-// scores, 15 us and 9.9 for 16 MB (5 at memory's rate).
+// and 3.1 for 1 MB of logits.  Of many logits by instructions: 16384 tokens of 250 f32 logits
+// in 16 sequences, sigmoid scores, 15 us and 9.9 for 16 MB (2.4 and 4.8 at memory's rate), of
+// which 5.9 and 6.6 are issue slots: 420 and 467 instructions a token.
 #include <cuda_bf16.h>
 
 #include <climits>

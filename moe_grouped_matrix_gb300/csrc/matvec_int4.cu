@@ -29,22 +29,26 @@
 // A warp streams spans of 16 rows by 512 k through two stages of its own in shared memory, by asynchronous
 // copies that only it waits for, whole lines of each row.  Teams of 1 to 16 warps share a tile along k: few
 // for long streams, many for few tiles; each CTA finds the number with which the last team ends first (fixed
-// at 1, 4, 16: 2 of 8 experts of 28672 x 4096 take 23.4, 24.5, 46 us for 22.8 with 2, their way back 46, 21.3,
-// 22.3 for 20.9 with 8).  A unit of a team's work is a tile of 16 rows (with an activation 8 gates and the 8
-// rows they gate) for
+// at 1, 2, 4, 8, 16: 2 of 8 experts of 28672 x 4096 take 25.5, 25.0, 26.9, 30.8, 52 us for 25.4, their way back
+// 46, 27, 21.7, 21.0, 22.7 for 21.3).  A unit of a team's work is a tile of 16 rows (with an activation 8 gates
+// and the 8 rows they gate) for
 //   - up to 8 slots of one expert, or
 //   - with weights, 8 tokens: all of their experts, one after another, columns the tokens, so that the sum
 //     over a token's slots stays in registers.
 //
 // x has to come from shared memory: through the caches a span's 8 KB for 8 columns is twice the weights'.
-// Each CTA makes it ready there where it fits as a whole (2 of 8 experts of 4096 x 4096: 1 token 7.9 us for
-// 8.8, 7 tokens 18.0 for 23.9; of 512 x 1024, 4 tokens 4.8 for 6.8); else a kernel ahead does, and a CTA copies
-// one item's at a time, or where it has little to do reads it through the caches all the same.
+// Each CTA makes it ready there where it fits as a whole (2 of 8 experts of 4096 x 4096: 1 token 8.1 us for
+// 8.5, 7 tokens 19.1 for 22.3; of 512 x 1024, 4 tokens 4.8 for 6.2; but 32 tokens, 4 of 16 experts of 1024 x 1024,
+// 13.3 for 11.3); else a kernel ahead does, and a CTA copies one item's at a time, or where it has little to do
+// reads it through the caches all the same.
 //
-// Measured: 1 token, 2 of 8 experts, 28672 x 4096, groups of 128, activation: 22.8 us, 121 MB at 5.3 TB/s (the
-// copies alone: 21.4 us); their way back, 4096 x 14336: 20.9 us, of which 8 before the first product, and
-// 256 tiles on 152 SMs; 8 of 128 experts, 2048 x 2048, groups of 32: 8.4 us for 19 MB, half of them before the
-// first product; 32 tokens, 4 of 64 experts, 2048 x 4096: 58 us for some 180 MB.
+// Measured: 1 token, 2 of 8 experts, 28672 x 4096, groups of 128, activation: 25.4 us, 121 MB at 4.8 TB/s (the
+// copies alone: 21.4 us; 3.9 before the first product), instructions in 58 % of the issue slots, which wait for
+// their pipes more than for memory; their way back, 4096 x 14336: 21.3 us, of which 7 before the first product,
+// and 256 tiles on 152 SMs; 8 of 128 experts, 2048 x 2048, groups of 32: 8.4 us for 19 MB, 3.9 of them before the
+// first product; 32 tokens, 4 of 64 experts, 2048 x 4096: 54 us for 193 MB, 3.6 TB/s.
+// Of several tokens the sums over the slots read an expert's weights once for every 8 tokens: 32 tokens, 2 of 8
+// experts of 4096 x 14336 take 195 us, without the sum 104.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -773,9 +777,9 @@ cudaError_t by_mode(Params p, int sms, cudaStream_t stream) {
   if (p.x_rows <= fit) return launch<kGroup, kZero, kGated, kSum, kAll>(p, sms, stream);
   if constexpr (!kSum) {
     // Copying an item's x pays where a CTA then has at least some 50 spans of weights for its warps (experts
-    // counted at most once): 16 tokens, 2 of 8 experts of 4096 x 4096 (108 spans) take 23.7 us and through the
-    // caches 25.9, 32 of 4 of 16 of 1024 x 1024 (13) 15.8 and 11.2.  Fewer columns than half of an item's would
-    // read the weights more than twice as often.
+    // counted at most once): 16 tokens, 2 of 8 experts of 4096 x 4096 (108 spans) take 22.3 us and through the
+    // caches 24.9, 32 of 4 of 16 of 1024 x 1024 (13; it fits as a whole, but put through both) 14.1 and 11.3.
+    // Fewer columns than half of an item's would read the weights more than twice as often.
     const int64_t items = p.experts < p.tokens * p.topk ? p.experts : p.tokens * p.topk;
     p.item_columns = int32_t(fit < kCols ? fit : kCols), p.item_pitch = int32_t(staged_pitch(p.k));
     if (p.item_columns >= kCols / 2 && items * p.tiles * p.spans >= 50 * int64_t(sms))

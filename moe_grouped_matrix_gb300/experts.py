@@ -265,9 +265,9 @@ def matvec_int4(x, w, experts=None, weights=None, act=None, out_dtype=torch.bflo
     Without experts w is one matrix [n, k] and h is [tokens, n].  Sums are fp32, rounded once to
     out_dtype (bfloat16 or float32); a row of x with an infinity or NaN gives NaN.
 
-    Weights are read once for every 8 tokens of an expert (with weights, for every 8 tokens), which
-    pays up to some 4 to 8 tokens an expert; past that, sort the rows and use gmm().  It takes the
-    codes of groups of 128 without zero points as they are,
+    The matrices are read once for every 8 tokens of an expert (with weights, for every 8 tokens),
+    which pays up to some 3 to 8 tokens an expert; past that, sort the rows and use gmm().  It takes
+    the codes of groups of 128 without zero points as they are (for up to some 16 rows an expert),
         scale = w.scale.transpose(2, 3).flatten(1, 2)[:, :k // 128, None].float().contiguous()  # once
         gmm(rows, w.codes, sizes, scale, rhs_format="int4")
     and others as dequantize_int4(w)."""
