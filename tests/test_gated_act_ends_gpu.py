@@ -14,7 +14,8 @@ INF, NAN = float("inf"), float("nan")
 
 def rows(dtype, f, seed):
     gen = torch.Generator(device=DEV).manual_seed(seed)
-    return torch.randn((6, 2 * f), generator=gen, device=DEV).to(dtype), torch.randn((6, f), generator=gen, device=DEV).to(dtype)
+    h, d = (torch.randn((6, n), generator=gen, device=DEV).to(dtype) for n in (2 * f, f))
+    return h, d
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -25,8 +26,8 @@ def test_infinities_and_nans_stay_in_their_place(dtype, act, f):
     h[h == 0] = 1
     d[d == 0] = 1
     want, back = G.gated_act(h, act), G.gated_act_backward(d, h, act)
-    at = {"gate nan": (1, 3, NAN), "up nan": (1, f + 8, NAN), "gate inf": (2, 5, INF), "gate -inf": (2, 9, -INF), "up inf": (3, f + 4, INF),
-          "up -inf": (4, 2 * f - 1, -INF)}
+    at = {"gate nan": (1, 3, NAN), "up nan": (1, f + 8, NAN), "gate inf": (2, 5, INF), "gate -inf": (2, 9, -INF),
+          "up inf": (3, f + 4, INF), "up -inf": (4, 2 * f - 1, -INF)}
     bad = h.clone()
     for r, c, v in at.values():
         bad[r, c] = v
@@ -41,7 +42,8 @@ def test_infinities_and_nans_stay_in_their_place(dtype, act, f):
     both = torch.cat((touched, touched), 1)
     assert torch.equal(dh[~both], back[~both])
     assert out[1, 3].isnan() and out[1, 8].isnan()
-    assert out[2, 5] == INF * float(torch.sign(h[2, f + 5])) and out[3, 4] == INF * float(torch.sign(want[3, 4] / h[3, f + 4]))
+    assert out[2, 5] == INF * float(torch.sign(h[2, f + 5]))
+    assert out[3, 4] == INF * float(torch.sign(want[3, 4] / h[3, f + 4]))
     assert out[4, f - 1] == -INF * float(torch.sign(want[4, f - 1] / h[4, 2 * f - 1]))
     assert dh[1, 3].isnan() and dh[1, f + 3].isnan() and dh[1, 8].isnan() and dh[1, f + 8] == back[1, f + 8]
     assert dh[2, 5] == d[2, 5] * h[2, f + 5] and dh[2, f + 5] == INF * float(torch.sign(d[2, 5]))  # act' is 1 there
